@@ -421,6 +421,169 @@ NVFP4_API nvfp4_status nvfp4_gemm_static_ws(const nvfp4_operand *a, const nvfp4_
                                   int64_t m, int64_t n, int64_t k, void *d,
                                   int32_t out_dtype, nvfp4_stream_t stream);
 
+/*
+ * ---------------------------------------------------------------------------
+ * Layer operators: what a pre-norm linear block computes around the NVFP4 products.
+ * They share the conventions above (device pointers, the caller's buffers and
+ * workspaces, the given stream, NVFP4_ERR_INVALID before anything is enqueued) and
+ * take no noop flag.  Matrices are row-major and compact; any element alignment and
+ * any size from 0 up to the stated limits is accepted (aligned rows are faster).
+ * Sums, norms and statistics are FP32; each output is rounded once, to nearest even.
+ * NaN and infinities travel as IEEE arithmetic moves them, except that maxima (row_amax,
+ * col_amax, the scales' amax) skip NaN, so codes made from a row that holds one are
+ * unspecified.
+ * ---------------------------------------------------------------------------
+ */
+
+/* Element-wise activations:
+ *   RELU  max(z, 0)
+ *   GELU  z/2 (1 + tanh(sqrt(2/pi) (z + 0.044715 z^3)))
+ *   SILU  z / (1 + exp(-z)) */
+typedef enum {
+    NVFP4_ACT_NONE = 0,
+    NVFP4_ACT_RELU = 1,
+    NVFP4_ACT_GELU = 2,
+    NVFP4_ACT_SILU = 3
+} nvfp4_activation;
+
+/* An 8-bit rowwise output: y ~ E4M3 code * scale. */
+typedef struct {
+    uint8_t *codes;  /* [rows][cols] E4M3 bytes */
+    float *scale;    /* [rows] (block 0) or [rows][ceil(cols/block)] */
+    int32_t block;   /* columns per scale: 0 (the whole row) or 128 */
+} nvfp4_fp8_out;
+
+/*
+ * nvfp4_add_rmsnorm -- residual addition and root-mean-square norm of each row:
+ *   h = x + residual (x where residual is NULL)
+ *   rstd = 1 / sqrt(mean_c(h^2) + eps)
+ *   y = h * weight * rstd
+ * computed in FP32 from the unrounded h, in one read of x and residual.
+ *   x, residual, h, y: [rows][cols] of in_dtype; weight [cols] of weight_dtype.
+ *   h (optional, with a residual): receives the sum; it may be x or residual itself.
+ *   rstd (optional, [rows] FP32): what nvfp4_add_rmsnorm_backward takes.
+ *   Outputs of y (at least one of y, fp8, row must be given unless x is empty):
+ *   y    in in_dtype (it may be x or residual itself where h is not the same buffer);
+ *   fp8  E4M3 with a scale per row or per 128 columns: scale = amax / 448 (at least
+ *        2^-126; 1 where amax is 0), code = E4M3(y * (448 / amax));
+ *   row  the rowwise NVFP4 output that nvfp4_quantize_rowwise defines, of the FP32 y,
+ *        with cfg: 1x16 blocks, NVFP4_ROW_SCALED (each row's own amax, found in the same
+ *        pass, or row->amax_in), or NVFP4_PER_TENSOR with row->amax_in (the amax of
+ *        another call or step; NVFP4_ERR_UNSUPPORTED without); four-over-six allowed.
+ *   fp8 and row together: NVFP4_ERR_UNSUPPORTED.
+ *   cols <= NVFP4_RMSNORM_MAX_COLS (NVFP4_ERR_UNSUPPORTED otherwise); eps >= 0.
+ *   cols == 0: rstd is 1/sqrt(eps), scales are 1, amax is 0.
+ */
+#define NVFP4_RMSNORM_MAX_COLS 32768
+NVFP4_API nvfp4_status nvfp4_add_rmsnorm(const void *x, const void *residual, int32_t in_dtype,
+                                         const void *weight, int32_t weight_dtype, int64_t rows,
+                                         int64_t cols, float eps, void *h, void *y, float *rstd,
+                                         const nvfp4_fp8_out *fp8, const nvfp4_config *cfg,
+                                         const nvfp4_out *row, nvfp4_stream_t stream);
+
+/*
+ * nvfp4_add_rmsnorm_backward -- gradients of nvfp4_add_rmsnorm (a quantized output
+ * passes its gradient straight through).  With n = h * rstd and g = dy * weight:
+ *   dx = rstd * (g - n * mean_c(g * n)) + dh      (the gradient of x and of residual)
+ *   dweight = sum_rows dy * n
+ *   dy, h, dh, dx: [rows][cols] of in_dtype; dh (optional) is the gradient that reaches
+ *   h beside the norm's; dx may be dy, h or dh itself.
+ *   weight [cols] of weight_dtype; rstd [rows] FP32, as the forward wrote it.
+ *   dweight (optional): [cols] FP32, overwritten; its sum runs in a fixed order.
+ *   workspace: device, 16-byte aligned, at least
+ *   nvfp4_add_rmsnorm_backward_workspace_size(rows, cols) bytes (unused without
+ *   dweight); two calls in flight at once need two workspaces.
+ *   cols <= NVFP4_RMSNORM_MAX_COLS.
+ */
+NVFP4_API nvfp4_status nvfp4_add_rmsnorm_backward_workspace_size(int64_t rows, int64_t cols,
+                                                                 uint64_t *bytes);
+NVFP4_API nvfp4_status nvfp4_add_rmsnorm_backward(const void *dy, const void *h, const void *dh,
+                                                  int32_t in_dtype, const void *weight,
+                                                  int32_t weight_dtype, const float *rstd,
+                                                  int64_t rows, int64_t cols, void *dx,
+                                                  float *dweight, void *workspace,
+                                                  uint64_t workspace_bytes,
+                                                  nvfp4_stream_t stream);
+
+/*
+ * nvfp4_gemm_bias_act -- nvfp4_gemm with bias, activation and residual in its epilogue:
+ *   z = dequant(a) x dequant(b)^T + bias,   d = act(z) + residual
+ * in FP32 from the tensor cores' accumulator, without the product going to memory.
+ *   a, b, m, n, k, d, out_dtype, workspace: as for nvfp4_gemm, workspace_bytes at least
+ *   nvfp4_gemm_bias_act_workspace_size(m, n, k).
+ *   epilogue->bias     optional, [n] of bias_dtype (NVFP4_IN_BF16 or NVFP4_IN_FP32)
+ *   epilogue->act      nvfp4_activation
+ *   epilogue->residual optional, [m][n] of out_dtype; it may be d itself
+ *   epilogue->z        optional, [m][n] of out_dtype: receives z, for
+ *                      nvfp4_bias_act_backward
+ *   Few rows (decoding) run on a kernel of their own that streams b once.
+ *   k == 0: z = bias.
+ */
+typedef struct {
+    const void *bias;
+    int32_t bias_dtype;
+    int32_t act;
+    const void *residual;
+    void *z;
+} nvfp4_epilogue;
+NVFP4_API nvfp4_status nvfp4_gemm_bias_act_workspace_size(int64_t m, int64_t n, int64_t k,
+                                                          uint64_t *bytes);
+NVFP4_API nvfp4_status nvfp4_gemm_bias_act(const nvfp4_operand *a, const nvfp4_operand *b,
+                                           int64_t m, int64_t n, int64_t k,
+                                           const nvfp4_epilogue *epilogue, void *d,
+                                           int32_t out_dtype, void *workspace,
+                                           uint64_t workspace_bytes, nvfp4_stream_t stream);
+
+/*
+ * nvfp4_bias_act_backward -- gradients of d = act(z), z = product + bias:
+ *   dz = dd * act'(z)   (relu'(0) = 0)
+ *   dbias = sum_rows dz (of the unrounded dz, in a fixed order)
+ * and the exact row and column maxima of |dz| as it is stored, which the quantization
+ * of dz takes as amax_in, so that it needs no amax pass.
+ *   dd, z, dz: [rows][cols] of dtype; z may be NULL with NVFP4_ACT_NONE (never read
+ *   then); dz may be dd or z itself.
+ *   dbias (optional): [cols] FP32; row_amax [rows], col_amax [cols] (optional) FP32.
+ *   workspace: device, 16-byte aligned, at least
+ *   nvfp4_bias_act_backward_workspace_size(rows, cols) bytes (unused when dbias,
+ *   row_amax and col_amax are all NULL); two calls in flight at once need two workspaces.
+ */
+NVFP4_API nvfp4_status nvfp4_bias_act_backward_workspace_size(int64_t rows, int64_t cols,
+                                                              uint64_t *bytes);
+NVFP4_API nvfp4_status nvfp4_bias_act_backward(const void *dd, const void *z, int32_t dtype,
+                                               int32_t act, int64_t rows, int64_t cols, void *dz,
+                                               float *dbias, float *row_amax, float *col_amax,
+                                               void *workspace, uint64_t workspace_bytes,
+                                               nvfp4_stream_t stream);
+
+/*
+ * nvfp4_grad_norm / nvfp4_clip_grad_norm -- the global 2-norm of a list of gradients, and
+ * the list scaled so that its norm is at most max_norm:
+ *   norm = sqrt(sum over all tensors of g^2),  coef = min(1, max_norm / (norm + 1e-6))
+ *   out = g * coef
+ *   tensors: HOST array of `count` entries (read before the call returns); data and out
+ *   are device pointers to n values of dtype (nvfp4_in_dtype).  out (clip only) may be
+ *   data itself; other overlaps between entries' out and any data are the caller's error.
+ *   norm: device float [1], written by both.  Squares are summed in FP32 per thread and
+ *   in FP64 across them, in a fixed order; a norm whose squares overflow FP32 is inf, and
+ *   then coef is 0; a NaN anywhere makes norm and every out NaN.
+ *   workspace: device, 16-byte aligned, at least nvfp4_clip_grad_norm_workspace_size()
+ *   bytes; two calls in flight at once need two workspaces.
+ *   count >= 0; max_norm >= 0.
+ */
+typedef struct {
+    const void *data;
+    void *out;      /* nvfp4_clip_grad_norm: where the scaled values go */
+    int64_t n;
+    int32_t dtype;  /* nvfp4_in_dtype */
+} nvfp4_tensor;
+NVFP4_API nvfp4_status nvfp4_clip_grad_norm_workspace_size(uint64_t *bytes);
+NVFP4_API nvfp4_status nvfp4_grad_norm(const nvfp4_tensor *tensors, int32_t count, float *norm,
+                                       void *workspace, uint64_t workspace_bytes,
+                                       nvfp4_stream_t stream);
+NVFP4_API nvfp4_status nvfp4_clip_grad_norm(const nvfp4_tensor *tensors, int32_t count,
+                                            float max_norm, float *norm, void *workspace,
+                                            uint64_t workspace_bytes, nvfp4_stream_t stream);
+
 /* Message for the last non-OK status returned on this host thread ("" if none). */
 NVFP4_API const char *nvfp4_last_error(void);
 

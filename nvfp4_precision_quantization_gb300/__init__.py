@@ -32,6 +32,12 @@ __all__ = [
     "NVFP4_GEMM_STATIC_WS_BYTES", "alloc_out", "EXPORTED_SYMBOLS", "nvfp4_rht16",
     "nvfp4_quantize_columnwise_rht", "nvfp4_quantize_both_rht",
     "nvfp4_grouped_quantize_columnwise_rht",
+    "NVFP4_ACT_NONE", "NVFP4_ACT_RELU", "NVFP4_ACT_GELU", "NVFP4_ACT_SILU", "Fp8Out",
+    "NVFP4_RMSNORM_MAX_COLS", "nvfp4_add_rmsnorm", "nvfp4_add_rmsnorm_backward",
+    "nvfp4_add_rmsnorm_backward_workspace_size", "nvfp4_gemm_bias_act",
+    "nvfp4_gemm_bias_act_workspace_size", "nvfp4_bias_act_backward",
+    "nvfp4_bias_act_backward_workspace_size", "nvfp4_grad_norm", "nvfp4_clip_grad_norm",
+    "nvfp4_clip_grad_norm_workspace_size",
 ]
 
 NVFP4_OK = 0
@@ -48,6 +54,11 @@ NVFP4_ROW_SCALED = 1
 NVFP4_DEVICE_TIMEOUT = 1
 NVFP4_DEVICE_BAD_GROUPS = 2
 NVFP4_GEMM_STATIC_WS_BYTES = 64 << 20
+NVFP4_ACT_NONE = 0
+NVFP4_ACT_RELU = 1
+NVFP4_ACT_GELU = 2
+NVFP4_ACT_SILU = 3
+NVFP4_RMSNORM_MAX_COLS = 32768
 
 EXPORTED_SYMBOLS = (
     "nvfp4_amax", "nvfp4_quantize_rowwise", "nvfp4_quantize_columnwise", "nvfp4_quantize_both",
@@ -59,6 +70,11 @@ EXPORTED_SYMBOLS = (
     "nvfp4_grouped_gemm_workspace_size", "nvfp4_grouped_gemm", "nvfp4_grouped_gemm_wgrad",
     "nvfp4_rht16", "nvfp4_quantize_columnwise_rht", "nvfp4_quantize_both_rht",
     "nvfp4_grouped_quantize_columnwise_rht",
+    "nvfp4_add_rmsnorm", "nvfp4_add_rmsnorm_backward",
+    "nvfp4_add_rmsnorm_backward_workspace_size", "nvfp4_gemm_bias_act",
+    "nvfp4_gemm_bias_act_workspace_size", "nvfp4_bias_act_backward",
+    "nvfp4_bias_act_backward_workspace_size", "nvfp4_grad_norm", "nvfp4_clip_grad_norm",
+    "nvfp4_clip_grad_norm_workspace_size",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -144,6 +160,18 @@ def load_library():
         "nvfp4_quantize_both_rht": [vp, i32, i64, i64, C.c_uint32, vp, vp, vp, vp, vp],
         "nvfp4_grouped_quantize_columnwise_rht": [vp, i32, i64, i64, vp, i32, C.c_uint32, vp, vp,
                                                   vp, vp],
+        "nvfp4_add_rmsnorm": [vp, vp, i32, vp, i32, i64, i64, f32, vp, vp, vp, vp, vp, vp, vp],
+        "nvfp4_add_rmsnorm_backward_workspace_size": [i64, i64, C.POINTER(C.c_uint64)],
+        "nvfp4_add_rmsnorm_backward": [vp, vp, vp, i32, vp, i32, vp, i64, i64, vp, vp, vp,
+                                       C.c_uint64, vp],
+        "nvfp4_gemm_bias_act_workspace_size": [i64, i64, i64, C.POINTER(C.c_uint64)],
+        "nvfp4_gemm_bias_act": [vp, vp, i64, i64, i64, vp, vp, i32, vp, C.c_uint64, vp],
+        "nvfp4_bias_act_backward_workspace_size": [i64, i64, C.POINTER(C.c_uint64)],
+        "nvfp4_bias_act_backward": [vp, vp, i32, i32, i64, i64, vp, vp, vp, vp, vp, C.c_uint64,
+                                    vp],
+        "nvfp4_clip_grad_norm_workspace_size": [C.POINTER(C.c_uint64)],
+        "nvfp4_grad_norm": [vp, i32, vp, vp, C.c_uint64, vp],
+        "nvfp4_clip_grad_norm": [vp, i32, f32, vp, vp, C.c_uint64, vp],
     }
     for name, args in sig.items():
         fn = getattr(L, name)
@@ -488,6 +516,230 @@ def nvfp4_gemm_static_ws(a: Operand, b: Operand, d: torch.Tensor, stream=None) -
     ca, cb = a._c(), b._c()
     _check(load_library().nvfp4_gemm_static_ws(C.byref(ca), C.byref(cb), m, n, k, _ptr(d), od,
                                                 _stream(stream)))
+
+
+# ---------------------------------------------------------------- layer operators
+
+
+class _CFp8Out(C.Structure):
+    _fields_ = [("codes", C.c_void_p), ("scale", C.c_void_p), ("block", C.c_int32)]
+
+
+@dataclass
+class Fp8Out:
+    """An 8-bit rowwise output: E4M3 codes [rows][cols] (uint8 or float8_e4m3fn), FP32 scale
+    [rows] (block 0) or [rows][ceil(cols/128)] (block 128)."""
+    codes: torch.Tensor
+    scale: torch.Tensor
+    block: int = 0
+
+
+class _CEpilogue(C.Structure):
+    _fields_ = [("bias", C.c_void_p), ("bias_dtype", C.c_int32), ("act", C.c_int32),
+                ("residual", C.c_void_p), ("z", C.c_void_p)]
+
+
+class _CTensor(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("out", C.c_void_p), ("n", C.c_int64),
+                ("dtype", C.c_int32)]
+
+
+def _like(name: str, t: Optional[torch.Tensor], ref: torch.Tensor) -> None:
+    """An optional tensor of ref's shape and type, contiguous."""
+    if t is not None and (t.shape != ref.shape or t.dtype != ref.dtype or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {ref.dtype} tensor of shape "
+                         f"{tuple(ref.shape)}")
+
+
+def _floats(name: str, t: Optional[torch.Tensor], n: int) -> None:
+    """An optional FP32 vector of n elements (any contiguous shape)."""
+    if t is not None and (t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous()):
+        raise ValueError(f"{name} must be contiguous float32 with {n} elements")
+
+
+def _vector(name: str, t: torch.Tensor, n: int) -> int:
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with {n} elements")
+    return _in_dtype(t)
+
+
+def _workspace(workspace: Optional[torch.Tensor], need: int, device):
+    if workspace is None:
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def nvfp4_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float,
+                      residual: Optional[torch.Tensor] = None,
+                      h: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                      rstd: Optional[torch.Tensor] = None, fp8: Optional[Fp8Out] = None,
+                      row: Optional[Out] = None, cfg: Optional[Config] = None,
+                      stream=None) -> None:
+    """h = x + residual, y = h * weight / sqrt(mean(h^2) + eps) of each row of x [rows][cols]
+    (bfloat16 or float32).  Outputs: h, y (x's type), rstd [rows], and one quantized form of
+    the FP32 y: fp8 (Fp8Out) or row with cfg (rowwise NVFP4, as nvfp4_quantize_rowwise)."""
+    rows, cols = _matrix(x)
+    wd = _vector("weight", weight, cols)
+    for name, t in (("residual", residual), ("h", h), ("y", y)):
+        _like(name, t, x)
+    _floats("rstd", rstd, rows)
+    cfp8 = crow = None
+    if fp8 is not None:
+        if fp8.codes.shape != x.shape or not fp8.codes.is_contiguous() or \
+                fp8.codes.element_size() != 1:
+            raise ValueError("fp8.codes must be a contiguous one-byte tensor of x's shape")
+        _floats("fp8.scale", fp8.scale, rows * (-(-cols // 128) if fp8.block else 1))
+        cfp8 = _CFp8Out(_ptr(fp8.codes), _ptr(fp8.scale), fp8.block)
+    if row is not None:
+        if cfg is None:
+            raise ValueError("a row output needs cfg")
+        for name, t, n in (("codes", row.codes, rows * ((cols + 1) // 2)),
+                           ("scales", row.scales, rows * ((cols + 15) // 16))):
+            if t.element_size() != 1 or t.numel() != n or not t.is_contiguous():
+                raise ValueError(f"row.{name} must be contiguous bytes, {n} of them")
+        lines = rows if cfg.mode == NVFP4_ROW_SCALED else 1
+        _floats("row.amax", row.amax, lines)
+        _floats("row.amax_in", row.amax_in, lines)
+        crow = row._c()
+    _check(load_library().nvfp4_add_rmsnorm(
+        _ptr(x), _ptr(residual), _in_dtype(x), _ptr(weight), wd, rows, cols, eps, _ptr(h),
+        _ptr(y), _ptr(rstd), C.byref(cfp8) if cfp8 is not None else None,
+        C.byref(cfg) if cfg is not None else None,
+        C.byref(crow) if crow is not None else None, _stream(stream)))
+
+
+def nvfp4_add_rmsnorm_backward_workspace_size(rows: int, cols: int) -> int:
+    v = C.c_uint64(0)
+    _check(load_library().nvfp4_add_rmsnorm_backward_workspace_size(rows, cols, C.byref(v)))
+    return v.value
+
+
+def nvfp4_add_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor,
+                               rstd: torch.Tensor, dx: torch.Tensor,
+                               dweight: Optional[torch.Tensor] = None,
+                               dh: Optional[torch.Tensor] = None,
+                               workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Gradients of nvfp4_add_rmsnorm: dx (of x and of residual; dh, the gradient reaching h
+    beside the norm's, is added) and dweight [cols] float32."""
+    rows, cols = _matrix(h)
+    for name, t in (("dy", dy), ("dx", dx), ("dh", dh)):
+        _like(name, t, h)
+    wd = _vector("weight", weight, cols)
+    _floats("rstd", rstd, rows)
+    _floats("dweight", dweight, cols)
+    size = 0
+    if dweight is not None:
+        need = 0 if workspace is not None else \
+            nvfp4_add_rmsnorm_backward_workspace_size(rows, cols)
+        workspace, size = _workspace(workspace, need, h.device)
+    _check(load_library().nvfp4_add_rmsnorm_backward(
+        _ptr(dy), _ptr(h), _ptr(dh), _in_dtype(h), _ptr(weight), wd, _ptr(rstd), rows, cols,
+        _ptr(dx), _ptr(dweight), _ptr(workspace), size, _stream(stream)))
+
+
+def nvfp4_gemm_bias_act_workspace_size(m: int, n: int, k: int) -> int:
+    v = C.c_uint64(0)
+    _check(load_library().nvfp4_gemm_bias_act_workspace_size(m, n, k, C.byref(v)))
+    return v.value
+
+
+def nvfp4_gemm_bias_act(a: Operand, b: Operand, d: torch.Tensor,
+                        bias: Optional[torch.Tensor] = None, act: int = NVFP4_ACT_NONE,
+                        residual: Optional[torch.Tensor] = None,
+                        z: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """d [m][n] (bfloat16 or float32) = act(z) + residual, z = dequant(a) x dequant(b)^T +
+    bias.  bias [n] bfloat16 or float32; residual and z (receives the pre-activation) have
+    d's shape and type; residual may be d."""
+    m, n = _matrix(d)
+    od = NVFP4_OUT_FP32 if d.dtype == torch.float32 else NVFP4_OUT_BF16
+    _in_dtype(d)
+    k = a.codes.shape[1] * 2
+    if a.codes.shape[0] != m or b.codes.shape[0] != n or b.codes.shape[1] * 2 != k:
+        raise ValueError("operand shapes do not match d")
+    _like("residual", residual, d)
+    _like("z", z, d)
+    bd = _vector("bias", bias, n) if bias is not None else NVFP4_IN_FP32
+    need = 0 if workspace is not None else nvfp4_gemm_bias_act_workspace_size(m, n, k)
+    workspace, size = _workspace(workspace, need, d.device)
+    ca, cb = a._c(), b._c()
+    epi = _CEpilogue(_ptr(bias), bd, act, _ptr(residual), _ptr(z))
+    _check(load_library().nvfp4_gemm_bias_act(C.byref(ca), C.byref(cb), m, n, k, C.byref(epi),
+                                              _ptr(d), od, _ptr(workspace), size,
+                                              _stream(stream)))
+
+
+def nvfp4_bias_act_backward_workspace_size(rows: int, cols: int) -> int:
+    v = C.c_uint64(0)
+    _check(load_library().nvfp4_bias_act_backward_workspace_size(rows, cols, C.byref(v)))
+    return v.value
+
+
+def nvfp4_bias_act_backward(dd: torch.Tensor, z: Optional[torch.Tensor], act: int,
+                            dz: torch.Tensor, dbias: Optional[torch.Tensor] = None,
+                            row_amax: Optional[torch.Tensor] = None,
+                            col_amax: Optional[torch.Tensor] = None,
+                            workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """dz = dd * act'(z), dbias [cols] = its column sums, row_amax [rows] / col_amax [cols] =
+    the maxima of |dz|, ready to be the amax_in of the quantization of dz."""
+    rows, cols = _matrix(dd)
+    _like("z", z, dd)
+    _like("dz", dz, dd)
+    _floats("dbias", dbias, cols)
+    _floats("row_amax", row_amax, rows)
+    _floats("col_amax", col_amax, cols)
+    size = 0
+    if dbias is not None or row_amax is not None or col_amax is not None:
+        need = 0 if workspace is not None else nvfp4_bias_act_backward_workspace_size(rows, cols)
+        workspace, size = _workspace(workspace, need, dd.device)
+    _check(load_library().nvfp4_bias_act_backward(
+        _ptr(dd), _ptr(z), _in_dtype(dd), act, rows, cols, _ptr(dz), _ptr(dbias),
+        _ptr(row_amax), _ptr(col_amax), _ptr(workspace), size, _stream(stream)))
+
+
+def nvfp4_clip_grad_norm_workspace_size() -> int:
+    v = C.c_uint64(0)
+    _check(load_library().nvfp4_clip_grad_norm_workspace_size(C.byref(v)))
+    return v.value
+
+
+def _tensor_list(tensors, out):
+    items = (_CTensor * len(tensors))()
+    for i, t in enumerate(tensors):
+        if not t.is_contiguous():
+            raise ValueError(f"tensor {i} must be contiguous")
+        o = t if out is None else out[i]
+        if o is not t and (o.dtype != t.dtype or o.numel() != t.numel()
+                           or not o.is_contiguous()):
+            raise ValueError(f"out {i} must be contiguous, of its tensor's type and size")
+        e = items[i]
+        e.data, e.out, e.n, e.dtype = t.data_ptr(), o.data_ptr(), t.numel(), _in_dtype(t)
+    return items
+
+
+def nvfp4_grad_norm(tensors, norm: torch.Tensor, workspace: Optional[torch.Tensor] = None,
+                    stream=None) -> None:
+    """norm [1] (float32) = the 2-norm of all tensors (bfloat16 or float32) together."""
+    _floats("norm", norm, 1)
+    need = 0 if workspace is not None else nvfp4_clip_grad_norm_workspace_size()
+    workspace, size = _workspace(workspace, need, norm.device)
+    items = _tensor_list(tensors, None)
+    _check(load_library().nvfp4_grad_norm(items, len(items), _ptr(norm), _ptr(workspace), size,
+                                          _stream(stream)))
+
+
+def nvfp4_clip_grad_norm(tensors, max_norm: float, norm: torch.Tensor, out=None,
+                         workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Scale the tensors (in place, or into the list out) by min(1, max_norm / (norm + 1e-6));
+    norm [1] (float32) receives their global 2-norm before that."""
+    _floats("norm", norm, 1)
+    if out is not None and len(out) != len(tensors):
+        raise ValueError("out must have one tensor for each tensor")
+    need = 0 if workspace is not None else nvfp4_clip_grad_norm_workspace_size()
+    workspace, size = _workspace(workspace, need, norm.device)
+    items = _tensor_list(tensors, out)
+    _check(load_library().nvfp4_clip_grad_norm(items, len(items), max_norm, _ptr(norm),
+                                               _ptr(workspace), size, _stream(stream)))
 
 
 def alloc_out(lines: int, n: int, amax_len: int, device="cuda", fill=None) -> Out:

@@ -18,6 +18,7 @@
 #include <string>
 
 #include "../../include/nvfp4.h"
+#include "api_common.h"
 #include "internal.h"
 
 namespace nvfp4 {
@@ -33,6 +34,8 @@ static __device__ __align__(256) uint8_t g_gemm_static_ws[NVFP4_GEMM_STATIC_WS_B
 namespace {
 
 thread_local std::string g_last_error;
+
+}  // namespace
 
 nvfp4_status fail(nvfp4_status st, const std::string& msg) {
   g_last_error = msg;
@@ -51,6 +54,7 @@ bool bytes_overlap(const void* a, uint64_t na, const void* b, uint64_t nb) {
   return pa < pb + nb && pb < pa + na;
 }
 
+namespace {
 struct DevCacheEntry {
   bool ready = false;
   int num_sms = 0;
@@ -61,6 +65,7 @@ struct DevCacheEntry {
 constexpr int kMaxDevices = 64;
 std::mutex g_mu;
 DevCacheEntry g_dev[kMaxDevices];
+}  // namespace
 
 nvfp4_status current_device(DeviceInfo* out) {
   int dev = 0;
@@ -129,6 +134,7 @@ nvfp4_status check_out(const nvfp4_out* o, const char* name, int64_t lines, int6
   return NVFP4_OK;
 }
 
+namespace {
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                    const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                                    const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
@@ -608,7 +614,8 @@ namespace {
 nvfp4_status gemm_impl(const nvfp4_operand* a, const nvfp4_operand* b, const int64_t* group_ends,
                        int32_t num_groups, int64_t m, int64_t n, int64_t k, void* d,
                        int32_t out_dtype, void* workspace, uint64_t workspace_bytes,
-                       nvfp4_stream_t stream, bool static_ws, bool k_grouped = false) {
+                       nvfp4_stream_t stream, bool static_ws, bool k_grouped = false,
+                       const Epilogue* epilogue = nullptr) {
   nvfp4_status st;
   if ((st = check_sizes(m, n)) != NVFP4_OK) return st;
   if ((st = check_sizes(k, 0)) != NVFP4_OK) return st;
@@ -624,6 +631,13 @@ nvfp4_status gemm_impl(const nvfp4_operand* a, const nvfp4_operand* b, const int
   if (m == 0 || n == 0) return NVFP4_OK;
   if (d == nullptr) return fail(NVFP4_ERR_INVALID, "d is NULL");
   const size_t esize = out_dtype == NVFP4_OUT_BF16 ? 2 : 4;
+  if (k == 0 && epilogue != nullptr) {  // the empty sum's epilogue
+    DeviceInfo dev;
+    if ((st = current_device(&dev)) != NVFP4_OK) return st;
+    cudaError_t e = launch_epilogue_only(*epilogue, d, out_dtype == NVFP4_OUT_BF16, m, n, dev,
+                                         stream);
+    return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "epilogue launch");
+  }
   if (k == 0) {  // the empty sum
     const size_t blocks = k_grouped ? (size_t)num_groups : 1;
     cudaError_t e = cudaMemsetAsync(d, 0, blocks * (size_t)m * (size_t)n * esize, stream);
@@ -676,6 +690,7 @@ nvfp4_status gemm_impl(const nvfp4_operand* a, const nvfp4_operand* b, const int
   g.group_ends = group_ends;
   g.num_groups = num_groups;
   g.k_grouped = k_grouped;
+  g.epilogue = epilogue;
   cudaError_t e = launch_gemm(g, dev, stream);
   if (e != cudaSuccess) return cuda_fail(e, "gemm launch");
   return NVFP4_OK;
@@ -687,6 +702,33 @@ nvfp4_status nvfp4_gemm(const nvfp4_operand* a, const nvfp4_operand* b, int64_t 
                         uint64_t workspace_bytes, nvfp4_stream_t stream) {
   return gemm_impl(a, b, nullptr, 0, m, n, k, d, out_dtype, workspace, workspace_bytes, stream,
                    false);
+}
+
+nvfp4_status nvfp4_gemm_bias_act_workspace_size(int64_t m, int64_t n, int64_t k,
+                                                uint64_t* bytes) {
+  return nvfp4_gemm_workspace_size(m, n, k, bytes);
+}
+
+nvfp4_status nvfp4_gemm_bias_act(const nvfp4_operand* a, const nvfp4_operand* b, int64_t m,
+                                 int64_t n, int64_t k, const nvfp4_epilogue* epilogue, void* d,
+                                 int32_t out_dtype, void* workspace, uint64_t workspace_bytes,
+                                 nvfp4_stream_t stream) {
+  if (epilogue == nullptr) return fail(NVFP4_ERR_INVALID, "epilogue is NULL");
+  if (epilogue->bias != nullptr && !valid_in_dtype(epilogue->bias_dtype))
+    return fail(NVFP4_ERR_INVALID, "unknown bias_dtype");
+  if (!valid_activation(epilogue->act)) return fail(NVFP4_ERR_INVALID, "unknown activation");
+  if (m > 0 && n > 0 && (out_dtype == NVFP4_OUT_BF16 || out_dtype == NVFP4_OUT_FP32)) {
+    const uint64_t bytes = (uint64_t)m * (uint64_t)n * (out_dtype == NVFP4_OUT_BF16 ? 2 : 4);
+    if (epilogue->residual != d && bytes_overlap(epilogue->residual, bytes, d, bytes))
+      return fail(NVFP4_ERR_INVALID, "residual overlaps d without being d");
+    if (bytes_overlap(epilogue->z, bytes, d, bytes) ||
+        bytes_overlap(epilogue->z, bytes, epilogue->residual, bytes))
+      return fail(NVFP4_ERR_INVALID, "z overlaps d or residual");
+  }
+  const Epilogue e{epilogue->bias, epilogue->bias_dtype == NVFP4_IN_BF16, epilogue->act,
+                   epilogue->residual, epilogue->z};
+  return gemm_impl(a, b, nullptr, 0, m, n, k, d, out_dtype, workspace, workspace_bytes, stream,
+                   false, false, &e);
 }
 
 nvfp4_status nvfp4_grouped_gemm_workspace_size(int64_t rows, int64_t n, int64_t k,

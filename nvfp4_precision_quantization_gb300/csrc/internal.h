@@ -197,6 +197,26 @@ bool rht16_amax_rows_supported(const void* x, bool bf16, int64_t cols);
 cudaError_t launch_rht16_amax_rows(const RhtAmaxArgs& a, float* row_max, float* row_tensor,
                                    const DeviceInfo& dev, cudaStream_t stream);
 
+// What nvfp4_gemm_bias_act applies to the product: z = product + bias, kept in z if given,
+// then act(z) + residual.
+struct Epilogue {
+  const void* bias;
+  bool bias_bf16;
+  int act;
+  const void* residual;  // of D's type
+  void* z;               // of D's type
+#ifdef __CUDACC__
+  // bias of column c (0 without a bias, or for c < 0)
+  __device__ __forceinline__ float bias_at(int c) const {
+    if (bias == nullptr || c < 0) return 0.0f;
+    return bias_bf16 ? __uint_as_float((uint32_t) static_cast<const uint16_t*>(bias)[c] << 16)
+                     : static_cast<const float*>(bias)[c];
+  }
+#endif
+};
+cudaError_t launch_epilogue_only(const Epilogue& e, void* d, bool bf16, int64_t m, int64_t n,
+                                 const DeviceInfo& dev, cudaStream_t stream);
+
 struct GemmArgs {
   const uint8_t* a_codes;
   const uint8_t* a_scales;
@@ -221,6 +241,7 @@ struct GemmArgs {
   // K (tokens, ends multiples of 256): group g writes d + g*M*N from its K range,
   // a_amax [num_groups*M] or [num_groups], b_amax [num_groups*N] or [num_groups]
   bool k_grouped;
+  const Epilogue* epilogue;  // optional, not with groups
 };
 struct GemmLayout {
   int64_t k_tiles, tiles_m, tiles_n;
@@ -229,6 +250,84 @@ struct GemmLayout {
 // b_lines: rows of B (N, or num_groups * N for the grouped GEMM)
 GemmLayout gemm_layout(int64_t M, int64_t N, int64_t K, int64_t b_lines);
 cudaError_t launch_gemm(const GemmArgs& a, const DeviceInfo& dev, cudaStream_t stream);
+
+// Residual addition and RMS norm of each row (kernels_norm.cu).
+struct NormArgs {
+  const void* x;
+  const void* residual;  // or NULL
+  InType in;
+  const void* weight;
+  bool weight_bf16;
+  int64_t rows, cols;
+  float eps;
+  void* h;      // or NULL
+  void* y;      // or NULL
+  float* rstd;  // or NULL
+  // E4M3 output (q8 == NULL: none): a scale per row or per q8_block (128) columns
+  uint8_t* q8;
+  float* q8_scale;
+  int q8_block;
+  // rowwise NVFP4 output (codes and amax NULL: none)
+  uint8_t* codes;
+  uint8_t* scales;
+  float* amax;
+  const float* amax_in;  // NULL: each row's own
+  bool amax_per_tensor;
+  bool four_over_six;
+  float bound;
+};
+cudaError_t launch_add_rmsnorm(const NormArgs& a, const DeviceInfo& dev, cudaStream_t stream);
+
+struct NormBackwardArgs {
+  const void* dy;
+  const void* h;
+  const void* dh;  // or NULL
+  InType in;
+  const void* weight;
+  bool weight_bf16;
+  const float* rstd;
+  int64_t rows, cols;
+  void* dx;
+  float* dweight;   // or NULL
+  void* workspace;  // >= add_rmsnorm_backward_workspace(rows, cols) bytes with dweight
+};
+constexpr int64_t kNormBackwardParts = 608;  // at most this many CTAs, one partial dw each
+int64_t add_rmsnorm_backward_workspace(int64_t rows, int64_t cols);
+cudaError_t launch_add_rmsnorm_backward(const NormBackwardArgs& a, const DeviceInfo& dev,
+                                        cudaStream_t stream);
+// out[c] = sum of the n rows of part [n][cols], in a fixed order
+cudaError_t launch_column_sum(const float* part, int n, int64_t cols, float* out,
+                              cudaStream_t stream);
+
+// Gradients of bias and activation (kernels_act.cu).
+struct ActBackwardArgs {
+  const void* dd;
+  const void* z;
+  InType in;
+  int act;
+  int64_t rows, cols;
+  void* dz;
+  float* dbias;     // or NULL, as the two below
+  float* row_amax;
+  float* col_amax;
+  void* workspace;  // >= bias_act_backward_workspace(rows, cols) bytes with any of the three
+};
+int64_t bias_act_backward_workspace(int64_t rows, int64_t cols);
+cudaError_t launch_bias_act_backward(const ActBackwardArgs& a, const DeviceInfo& dev,
+                                     cudaStream_t stream);
+
+// Global norm of a list of tensors, and clipping by it (kernels_clip.cu).
+struct TensorEntry {
+  const void* data;
+  void* out;
+  int64_t n;
+  bool bf16;
+};
+constexpr int kClipMaxLaunches = 64;
+int64_t clip_workspace();  // bytes
+int64_t clip_capacity();   // most tensors of a list
+cudaError_t launch_clip(const TensorEntry* t, int count, bool clip, float max_norm, float* norm,
+                        void* workspace, const DeviceInfo& dev, cudaStream_t stream);
 
 // Grid size shared by the TMA amax and encode kernels (same tile -> CTA mapping).
 int pipe_grid_size(int64_t num_tiles, int num_sms);

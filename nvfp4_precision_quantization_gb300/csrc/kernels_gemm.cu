@@ -42,8 +42,10 @@
 
 #include <algorithm>
 
+#include "activation.cuh"
 #include "device_common.cuh"
 #include "internal.h"
+#include "row_io.cuh"
 
 namespace nvfp4 {
 namespace {
@@ -274,6 +276,7 @@ struct GemmParams {
   bool k_grouped;
   int64_t group_total;      // what the last group end must equal (rows of A, or K)
   int a_amax_group_stride;  // where group g's amax starts in a_amax (K-grouped: M, 1)
+  Epilogue epi;             // k_gemm_nvf4<SF, true> only (no groups)
 };
 
 // One output tile of this CTA's walk: its group, tile coordinates and K tiles.
@@ -327,10 +330,94 @@ __device__ __forceinline__ void tile_coords(int idx, int tiles_m, int tiles_n, i
   tn = rem / gm;
 }
 
+// 32 consecutive output columns of one row, FP32 -> D's type.  whole32 / whole16: all
+// of them inside the row, the run 32- / 16-byte aligned; else element stores of the
+// first n.
+__device__ __forceinline__ void store_run32(void* base, bool bf16, int64_t off, const float* v,
+                                            bool whole32, bool whole16, int n) {
+  if (bf16) {
+    uint16_t* dst = static_cast<uint16_t*>(base) + off;
+    uint32_t w[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) w[j] = bf16x2_bits(v[2 * j], v[2 * j + 1]);
+    if (whole32) {
+      stg_v8(dst, w);
+      stg_v8(dst + 16, w + 8);
+    } else if (whole16) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        *reinterpret_cast<uint4*>(dst + 8 * g) =
+            make_uint4(w[4 * g], w[4 * g + 1], w[4 * g + 2], w[4 * g + 3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (j < n) dst[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
+    }
+  } else {
+    uint32_t* dst = static_cast<uint32_t*>(base) + off;
+    uint32_t w[32];
+#pragma unroll
+    for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(v[j]);
+    if (whole32) {
+#pragma unroll
+      for (int g = 0; g < 4; ++g) stg_v8(dst + 8 * g, w + 8 * g);
+    } else if (whole16) {
+#pragma unroll
+      for (int g = 0; g < 8; ++g)
+        *reinterpret_cast<uint4*>(dst + 4 * g) =
+            make_uint4(w[4 * g], w[4 * g + 1], w[4 * g + 2], w[4 * g + 3]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 32; ++j)
+        if (j < n) dst[j] = w[j];
+    }
+  }
+}
+
+// The epilogue of 32 columns of one row: v (the product) plus bias becomes z, kept if
+// asked for, then act(z) + residual, stored.  bias: 32 FP32 values in shared memory.
+__device__ __forceinline__ void epilogue_run32(const Epilogue& e, void* d, bool bf16, int64_t off,
+                                               float* v, const float* bias, bool vec32,
+                                               bool vec16, int n) {
+#pragma unroll
+  for (int j4 = 0; j4 < 8; ++j4) {
+    const float4 b = *reinterpret_cast<const float4*>(bias + 4 * j4);
+    v[4 * j4] = __fadd_rn(v[4 * j4], b.x);
+    v[4 * j4 + 1] = __fadd_rn(v[4 * j4 + 1], b.y);
+    v[4 * j4 + 2] = __fadd_rn(v[4 * j4 + 2], b.z);
+    v[4 * j4 + 3] = __fadd_rn(v[4 * j4 + 3], b.w);
+  }
+  if (e.z != nullptr) store_run32(e.z, bf16, off, v, vec32, vec16, n);
+  if (e.act == kActRelu) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = act_value<kActRelu>(v[j]);
+  } else if (e.act == kActGelu) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = act_value<kActGelu>(v[j]);
+  } else if (e.act == kActSilu) {
+#pragma unroll
+    for (int j = 0; j < 32; ++j) v[j] = act_value<kActSilu>(v[j]);
+  }
+  if (e.residual != nullptr) {
+    const int grain = vec32 ? 32 : (vec16 ? 16 : 0);
+#pragma unroll
+    for (int c = 0; c < 2; ++c) {
+      const int left = n - kChunk * c;
+      float r[kChunk];
+      load_vector16(e.residual, bf16, off + kChunk * c,
+                    left < 0 ? 0 : (left < kChunk ? left : kChunk), grain, r);
+#pragma unroll
+      for (int j = 0; j < kChunk; ++j) v[kChunk * c + j] = __fadd_rn(v[kChunk * c + j], r[j]);
+    }
+  }
+  store_run32(d, bf16, off, v, vec32, vec16, n);
+}
+
 // Persistent: CTA c computes tiles c, c + gridDim.x, ...  The load ring runs on
 // across tile boundaries; the epilogue copies the accumulator to registers,
 // hands TMEM back (acc_empty) and stores while the MMAs of the next tile run.
-template <class SF>
+// EPI: with bias, activation and residual (p.epi) applied to the scaled accumulator.
+template <class SF, bool EPI>
 __global__ void __launch_bounds__(kThreads, 1)
     k_gemm_nvf4(const __grid_constant__ CUtensorMap map_a,
                 const __grid_constant__ CUtensorMap map_b, const GemmParams p) {
@@ -483,6 +570,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool b_lines = p.b_amax_stride != 0;  // one amax per line of B
     uint32_t t = 0;
     float* beta = s_beta + (warp - 2) * kEpiCols;  // this warp's column factors
+    // and its bias, where a grouped GEMM keeps its group ends
+    float* bias = reinterpret_cast<float*>(s_ends) + (warp - 2) * kEpiCols;
     for (int tile = blockIdx.x; tile < num_tiles; tile += gridDim.x, ++t) {
       const TileJob job = tile_job(p, ends, tile);
       const int tm = job.tm, tn = job.tn;
@@ -516,6 +605,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                __float_as_uint(__fmul_rn(b4[1], p.b_finv)),
                __float_as_uint(__fmul_rn(b4[2], p.b_finv)),
                __float_as_uint(__fmul_rn(b4[3], p.b_finv)));
+        if constexpr (EPI) {  // and its bias
+          float c[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            c[j] = p.epi.bias_at(c4 + j < p.N ? c4 + j : -1);
+          sts_v4(bias + 4 * lane, __float_as_uint(c[0]), __float_as_uint(c[1]),
+                 __float_as_uint(c[2]), __float_as_uint(c[3]));
+        }
         __syncwarp();
       }
       const bool ready = mbar_wait_bounded(acc_full, t & 1);
@@ -541,8 +638,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       // whole 32-byte sectors per store where the row's run is 32-byte aligned,
       // else 16-byte stores, else (ragged N or odd alignment) element stores
       const uintptr_t d_addr = reinterpret_cast<uintptr_t>(p.d) + off * (p.d_bf16 ? 2 : 4);
-      const bool vec = nvalid == kEpiCols && (d_addr & 15) == 0;
-      const bool vec32 = vec && (d_addr & 31) == 0;
+      uintptr_t run_addr = d_addr;
+      if constexpr (EPI) {  // the residual and z take D's accesses
+        const int64_t at = off * (p.d_bf16 ? 2 : 4);
+        if (p.epi.residual) run_addr |= reinterpret_cast<uintptr_t>(p.epi.residual) + at;
+        if (p.epi.z) run_addr |= reinterpret_cast<uintptr_t>(p.epi.z) + at;
+      }
+      const bool vec = nvalid == kEpiCols && (run_addr & 15) == 0;
+      const bool vec32 = vec && (run_addr & 31) == 0;
 #pragma unroll
       for (int c = 0; c < kEpiCols / 32; ++c) {
         uint32_t* vc = v + c * 32;
@@ -555,6 +658,14 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < 4; ++j)
             vc[4 * j4 + j] =
                 __float_as_uint(__fmul_rn(__fmul_rn(__uint_as_float(vc[4 * j4 + j]), alpha), bj[j]));
+        }
+        if constexpr (EPI) {
+          float f[32];
+#pragma unroll
+          for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(vc[j]);
+          epilogue_run32(p.epi, p.d, p.d_bf16, off + c * 32, f, bias + c * 32, vec32, vec,
+                         nvalid - c * 32);
+          continue;
         }
         if (p.d_bf16) {
           uint16_t* dst = static_cast<uint16_t*>(p.d) + off + c * 32;
@@ -616,7 +727,36 @@ constexpr uint32_t make_idesc_nvf4(int m, int n) {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// d = act(bias) + residual: the epilogue of an empty sum (k == 0).
+__global__ void __launch_bounds__(256) k_epilogue_only(const Epilogue e, void* d, bool bf16,
+                                                       int64_t m, int n) {
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < m * n;
+       i += (int64_t)gridDim.x * 256) {
+    float v = e.bias_at((int)(i % n));
+    if (e.z != nullptr) {
+      if (bf16) static_cast<__nv_bfloat16*>(e.z)[i] = __float2bfloat16_rn(v);
+      else static_cast<float*>(e.z)[i] = v;
+    }
+    v = e.act == kActRelu   ? act_value<kActRelu>(v)
+        : e.act == kActGelu ? act_value<kActGelu>(v)
+        : e.act == kActSilu ? act_value<kActSilu>(v)
+                            : v;
+    if (e.residual != nullptr)
+      v = __fadd_rn(v, bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(e.residual)[i])
+                            : static_cast<const float*>(e.residual)[i]);
+    if (bf16) static_cast<__nv_bfloat16*>(d)[i] = __float2bfloat16_rn(v);
+    else static_cast<float*>(d)[i] = v;
+  }
+}
+
 }  // namespace
+
+cudaError_t launch_epilogue_only(const Epilogue& e, void* d, bool bf16, int64_t m, int64_t n,
+                                 const DeviceInfo& dev, cudaStream_t stream) {
+  const int64_t grid = std::min<int64_t>((m * n + 255) / 256, 8LL * dev.num_sms);
+  k_epilogue_only<<<(unsigned)grid, 256, 0, stream>>>(e, d, bf16, m, (int)n);
+  return cudaGetLastError();
+}
 
 GemmLayout gemm_layout(int64_t M, int64_t N, int64_t K, int64_t b_lines) {
   GemmLayout L;
@@ -630,7 +770,7 @@ GemmLayout gemm_layout(int64_t M, int64_t N, int64_t K, int64_t b_lines) {
   return L;
 }
 
-template <class SF>
+template <class SF, bool EPI>
 static cudaError_t launch_gemm_t(const GemmArgs& a, const GemmLayout& L, const DeviceInfo& dev,
                                  cudaStream_t stream) {
   using G = GemmGeom<SF>;
@@ -651,7 +791,7 @@ static cudaError_t launch_gemm_t(const GemmArgs& a, const GemmLayout& L, const D
 
   static bool attr_set[64] = {};
   if (dev.device < 64 && !attr_set[dev.device]) {
-    e = cudaFuncSetAttribute(k_gemm_nvf4<SF>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    e = cudaFuncSetAttribute(k_gemm_nvf4<SF, EPI>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              G::kSmemBytes);
     if (e != cudaSuccess) return e;
     attr_set[dev.device] = true;
@@ -683,14 +823,16 @@ static cudaError_t launch_gemm_t(const GemmArgs& a, const GemmLayout& L, const D
   p.group_total = p.k_grouped ? a.K : a.M;
   const int64_t tiles = (a.group_ends && a.k_grouped ? a.num_groups : 1) * L.tiles_m * L.tiles_n;
   const int grid = (int)std::min<int64_t>(tiles, dev.num_sms);
-  k_gemm_nvf4<SF><<<grid, kThreads, G::kSmemBytes, stream>>>(map_a, map_b, p);
+  if constexpr (EPI) p.epi = *a.epilogue;
+  k_gemm_nvf4<SF, EPI><<<grid, kThreads, G::kSmemBytes, stream>>>(map_a, map_b, p);
   return cudaGetLastError();
 }
 
 cudaError_t launch_gemm(const GemmArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
   const GemmLayout L = gemm_layout(
       a.M, a.N, a.K, a.group_ends && !a.k_grouped ? (int64_t)a.num_groups * a.N : a.N);
-  return launch_gemm_t<SfLayout>(a, L, dev, stream);
+  return a.epilogue != nullptr ? launch_gemm_t<SfLayout, true>(a, L, dev, stream)
+                               : launch_gemm_t<SfLayout, false>(a, L, dev, stream);
 }
 
 }  // namespace nvfp4

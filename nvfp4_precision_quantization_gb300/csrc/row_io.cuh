@@ -1,0 +1,132 @@
+// row_io.cuh -- 16 consecutive row elements per thread: loads and stores shared by the
+// layer operators' kernels (BF16 or FP32 rows, widened to FP32).
+//
+// A row may start at any element.  `grain` is the widest access that every full
+// 16-element chunk of the tensor allows (32 or 16 bytes, 0 for element accesses), the
+// same for the whole tensor, so the choice is one uniform branch: 32-byte accesses move
+// whole sectors (one request of a warp covers 1 KB), and an odd row length falls back
+// to elements.  A chunk cut by the row's end is always moved element by element.
+#pragma once
+
+#include <cuda_bf16.h>
+
+#include "device_common.cuh"
+
+namespace nvfp4 {
+
+constexpr int kChunk = 16;  // elements per thread and access group
+
+// The grain of rows of `cols` elements of `elem` bytes at p.
+inline int row_grain(const void* p, int64_t cols, int elem) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p) | (uintptr_t)(cols * elem);
+  return a % 32 == 0 ? 32 : (a % 16 == 0 ? 16 : 0);
+}
+
+__device__ __forceinline__ void ldg_v8(const void* p, uint32_t* w) {
+  asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
+                 "=r"(w[6]), "=r"(w[7])
+               : "l"(p));
+}
+__device__ __forceinline__ void ldg_v4(const void* p, uint32_t* w) {
+  asm volatile("ld.global.v4.b32 {%0, %1, %2, %3}, [%4];"
+               : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+               : "l"(p));
+}
+
+__device__ __forceinline__ uint32_t bf16x2_bits(float lo, float hi) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// One chunk as it lies in memory: 8 words of BF16 pairs or 16 FP32 words; elements from n
+// on are zero.
+template <bool BF16>
+struct Chunk {
+  static constexpr int kWords = BF16 ? 8 : 16;
+  uint32_t w[kWords];
+
+  __device__ __forceinline__ void load(const void* base, int64_t off, int n, int grain) {
+    const char* p = static_cast<const char*>(base) + off * (BF16 ? 2 : 4);
+    if (n == kChunk && grain == 32) {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 8) ldg_v8(p + 4 * i, w + i);
+    } else if (n == kChunk && grain == 16) {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 4) ldg_v4(p + 4 * i, w + i);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kWords; ++i) w[i] = 0;
+      if constexpr (BF16) {
+        const uint16_t* q = reinterpret_cast<const uint16_t*>(p);
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i)
+          if (i < n) w[i >> 1] |= (uint32_t)q[i] << (16 * (i & 1));
+      } else {
+        const uint32_t* q = reinterpret_cast<const uint32_t*>(p);
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i)
+          if (i < n) w[i] = q[i];
+      }
+    }
+  }
+  __device__ __forceinline__ float get(int i) const {
+    if constexpr (BF16) return (i & 1) ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
+    else return __uint_as_float(w[i]);
+  }
+  // Round 16 values into the chunk (nearest even).
+  __device__ __forceinline__ void set(const float* v) {
+    if constexpr (BF16) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = bf16x2_bits(v[2 * i], v[2 * i + 1]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 16; ++i) w[i] = __float_as_uint(v[i]);
+    }
+  }
+  __device__ __forceinline__ void store(void* base, int64_t off, int n, int grain) const {
+    char* p = static_cast<char*>(base) + off * (BF16 ? 2 : 4);
+    if (n == kChunk && grain == 32) {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 8) stg_v8(p + 4 * i, w + i);
+    } else if (n == kChunk && grain == 16) {
+#pragma unroll
+      for (int i = 0; i < kWords; i += 4)
+        *reinterpret_cast<uint4*>(p + 4 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
+    } else if constexpr (BF16) {
+      uint16_t* q = reinterpret_cast<uint16_t*>(p);
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i)
+        if (i < n) q[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+    } else {
+      uint32_t* q = reinterpret_cast<uint32_t*>(p);
+#pragma unroll
+      for (int i = 0; i < kChunk; ++i)
+        if (i < n) q[i] = w[i];
+    }
+  }
+};
+
+// The 16 FP32 values of a chunk of a BF16 or FP32 vector (type known at run time).
+__device__ __forceinline__ void load_vector16(const void* base, bool bf16, int64_t off, int n,
+                                              int grain, float* v) {
+  if (bf16) {
+    Chunk<true> c;
+    c.load(base, off, n, grain);
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i) v[i] = c.get(i);
+  } else {
+    Chunk<false> c;
+    c.load(base, off, n, grain);
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i) v[i] = c.get(i);
+  }
+}
+
+// Elements of the chunk that starts at column c of a row of `cols` (0 past its end).
+__device__ __forceinline__ int chunk_len(int64_t c, int64_t cols) {
+  const int64_t left = cols - c;
+  return left >= kChunk ? kChunk : (left > 0 ? (int)left : 0);
+}
+
+}  // namespace nvfp4
