@@ -70,6 +70,41 @@ struct Chunk {
       }
     }
   }
+  // From a row held in shared memory, 16-byte aligned (so n is a whole number of 16-byte
+  // units).  Lanes are 32 or 64 bytes apart; rotating the order of a lane's units spreads
+  // the eight lanes of an access over all banks.
+  __device__ __forceinline__ void load_shared(const uint8_t* p, int n, int lane) {
+    constexpr int kUnits = kWords / 4;
+    const int rot = BF16 ? (lane >> 2) & 1 : (lane >> 1) & 3;
+    uint4 u[kUnits];
+#pragma unroll
+    for (int k = 0; k < kUnits; ++k) {
+      const int at = (k + rot) & (kUnits - 1);
+      u[k] = at * (kChunk / kUnits) < n ? *reinterpret_cast<const uint4*>(p + 16 * at)
+                                        : make_uint4(0, 0, 0, 0);
+    }
+#pragma unroll
+    for (int d = 1; d < kUnits; d *= 2) {  // u[k] holds unit k + rot: rotate back
+      uint4 r[kUnits];
+#pragma unroll
+      for (int k = 0; k < kUnits; ++k) {
+        const uint4 a = u[k], b = u[(k - d) & (kUnits - 1)];
+        r[k].x = (rot & d) ? b.x : a.x;
+        r[k].y = (rot & d) ? b.y : a.y;
+        r[k].z = (rot & d) ? b.z : a.z;
+        r[k].w = (rot & d) ? b.w : a.w;
+      }
+#pragma unroll
+      for (int k = 0; k < kUnits; ++k) u[k] = r[k];
+    }
+#pragma unroll
+    for (int k = 0; k < kUnits; ++k) {
+      w[4 * k] = u[k].x;
+      w[4 * k + 1] = u[k].y;
+      w[4 * k + 2] = u[k].z;
+      w[4 * k + 3] = u[k].w;
+    }
+  }
   __device__ __forceinline__ float get(int i) const {
     if constexpr (BF16) return (i & 1) ? bf16_hi(w[i >> 1]) : bf16_lo(w[i >> 1]);
     else return __uint_as_float(w[i]);
@@ -121,6 +156,17 @@ __device__ __forceinline__ void load_vector16(const void* base, bool bf16, int64
 #pragma unroll
     for (int i = 0; i < kChunk; ++i) v[i] = c.get(i);
   }
+}
+
+// Contiguous bytes to shared memory, completing on `bar` (16-byte aligned addresses, size a
+// multiple of 16).
+__device__ __forceinline__ void bulk_copy_in(void* dst, const void* src, uint32_t bytes,
+                                             uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::
+          "r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_addr(bar))
+      : "memory");
 }
 
 // Elements of the chunk that starts at column c of a row of `cols` (0 past its end).

@@ -42,8 +42,14 @@ def _close(got, want, rel, what):
     assert not bool(bad.any()), f"{what}: {err[bad].max().item()} of {want[bad][:3].tolist()}"
 
 
+# enough rows for every CTA to walk several, at each width of a row's team, with groups of
+# rows cut by the last row
+MANY = [(9001, 24), (7003, 512), (5003, 1000), (3001, 2048), (2777, 4096), (1501, 8192),
+        (1501, 5008), (701, 16384), (701, 12000), (400, 20000)]
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("rows,cols", SHAPES)
+@pytest.mark.parametrize("rows,cols", SHAPES + MANY)
 def test_norm_and_sum(rows, cols, dtype):
     x, r, w = _inputs(rows, cols, dtype, rows * 31 + cols)
     for residual in (None, r):
@@ -64,7 +70,7 @@ def test_norm_and_sum(rows, cols, dtype):
 
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("block", [0, 128])
-@pytest.mark.parametrize("rows,cols", SHAPES)
+@pytest.mark.parametrize("rows,cols", SHAPES + MANY)
 def test_fp8_output(rows, cols, dtype, block):
     x, r, w = _inputs(rows, cols, dtype, rows + cols, torch.float32)
     if rows > 2:
@@ -90,7 +96,7 @@ def test_fp8_output(rows, cols, dtype, block):
 
 @pytest.mark.parametrize("fos", [0, 1])
 @pytest.mark.parametrize("bound", [448.0, 256.0])
-@pytest.mark.parametrize("rows,cols", SHAPES)
+@pytest.mark.parametrize("rows,cols", SHAPES + MANY[1:5])
 def test_nvfp4_output_is_the_quantize_of_y(rows, cols, bound, fos):
     if rows == 0:
         pytest.skip("no codes to compare")
@@ -211,7 +217,7 @@ def test_a_bad_row_leaves_the_others_alone():
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("rows,cols", SHAPES + [(2500, 96), (1300, 2048)])
+@pytest.mark.parametrize("rows,cols", SHAPES + [(2500, 96), (1300, 2048)] + MANY)
 def test_backward(rows, cols, dtype):
     """dx: products of FP32 values and one row mean of at most 48 additions per chain:
     within 2^-18 of the terms' magnitude |g| + |n| mean|g n|; dweight: sums of `rows`
