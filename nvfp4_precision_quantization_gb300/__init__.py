@@ -13,7 +13,9 @@ from __future__ import annotations
 import ctypes as C
 import os
 import platform
+from array import array
 from dataclasses import dataclass
+from itertools import chain
 from typing import Optional
 
 import torch
@@ -193,7 +195,8 @@ def _ptr(t) -> Optional[int]:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+        # the handle alone: a Stream object costs as much as the launch of a small kernel
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -544,17 +547,25 @@ class _CTensor(C.Structure):
                 ("dtype", C.c_int32)]
 
 
-def _like(name: str, t: Optional[torch.Tensor], ref: torch.Tensor) -> None:
-    """An optional tensor of ref's shape and type, contiguous."""
-    if t is not None and (t.shape != ref.shape or t.dtype != ref.dtype or not t.is_contiguous()):
-        raise ValueError(f"{name} must be a contiguous {ref.dtype} tensor of shape "
-                         f"{tuple(ref.shape)}")
+_DTYPE_CODES = {torch.bfloat16: NVFP4_IN_BF16, torch.float32: NVFP4_IN_FP32}
 
 
-def _floats(name: str, t: Optional[torch.Tensor], n: int) -> None:
-    """An optional FP32 vector of n elements (any contiguous shape)."""
-    if t is not None and (t.dtype != torch.float32 or t.numel() != n or not t.is_contiguous()):
+def _like(name: str, t: Optional[torch.Tensor], shape, dtype) -> Optional[int]:
+    """The address of an optional contiguous tensor of the given shape and type."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
+    return t.data_ptr()
+
+
+def _floats(name: str, t: Optional[torch.Tensor], n: int) -> Optional[int]:
+    """The address of an optional FP32 vector of n elements (any contiguous shape)."""
+    if t is None:
+        return None
+    if t.dtype is not torch.float32 or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous float32 with {n} elements")
+    return t.data_ptr()
 
 
 def _vector(name: str, t: torch.Tensor, n: int) -> int:
@@ -579,17 +590,14 @@ def nvfp4_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float,
     (bfloat16 or float32).  Outputs: h, y (x's type), rstd [rows], and one quantized form of
     the FP32 y: fp8 (Fp8Out) or row with cfg (rowwise NVFP4, as nvfp4_quantize_rowwise)."""
     rows, cols = _matrix(x)
-    wd = _vector("weight", weight, cols)
-    for name, t in (("residual", residual), ("h", h), ("y", y)):
-        _like(name, t, x)
-    _floats("rstd", rstd, rows)
+    shape, dtype = x.shape, x.dtype
     cfp8 = crow = None
     if fp8 is not None:
-        if fp8.codes.shape != x.shape or not fp8.codes.is_contiguous() or \
+        if fp8.codes.shape != shape or not fp8.codes.is_contiguous() or \
                 fp8.codes.element_size() != 1:
             raise ValueError("fp8.codes must be a contiguous one-byte tensor of x's shape")
-        _floats("fp8.scale", fp8.scale, rows * (-(-cols // 128) if fp8.block else 1))
-        cfp8 = _CFp8Out(_ptr(fp8.codes), _ptr(fp8.scale), fp8.block)
+        scale = _floats("fp8.scale", fp8.scale, rows * (-(-cols // 128) if fp8.block else 1))
+        cfp8 = C.byref(_CFp8Out(fp8.codes.data_ptr(), scale, fp8.block))
     if row is not None:
         if cfg is None:
             raise ValueError("a row output needs cfg")
@@ -600,12 +608,12 @@ def nvfp4_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float,
         lines = rows if cfg.mode == NVFP4_ROW_SCALED else 1
         _floats("row.amax", row.amax, lines)
         _floats("row.amax_in", row.amax_in, lines)
-        crow = row._c()
+        crow = C.byref(row._c())
     _check(load_library().nvfp4_add_rmsnorm(
-        _ptr(x), _ptr(residual), _in_dtype(x), _ptr(weight), wd, rows, cols, eps, _ptr(h),
-        _ptr(y), _ptr(rstd), C.byref(cfp8) if cfp8 is not None else None,
-        C.byref(cfg) if cfg is not None else None,
-        C.byref(crow) if crow is not None else None, _stream(stream)))
+        x.data_ptr(), _like("residual", residual, shape, dtype), _in_dtype(x),
+        weight.data_ptr(), _vector("weight", weight, cols), rows, cols, eps,
+        _like("h", h, shape, dtype), _like("y", y, shape, dtype), _floats("rstd", rstd, rows),
+        cfp8, C.byref(cfg) if cfg is not None else None, crow, _stream(stream)))
 
 
 def nvfp4_add_rmsnorm_backward_workspace_size(rows: int, cols: int) -> int:
@@ -622,19 +630,17 @@ def nvfp4_add_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.
     """Gradients of nvfp4_add_rmsnorm: dx (of x and of residual; dh, the gradient reaching h
     beside the norm's, is added) and dweight [cols] float32."""
     rows, cols = _matrix(h)
-    for name, t in (("dy", dy), ("dx", dx), ("dh", dh)):
-        _like(name, t, h)
-    wd = _vector("weight", weight, cols)
-    _floats("rstd", rstd, rows)
-    _floats("dweight", dweight, cols)
+    shape, dtype = h.shape, h.dtype
     size = 0
     if dweight is not None:
         need = 0 if workspace is not None else \
             nvfp4_add_rmsnorm_backward_workspace_size(rows, cols)
         workspace, size = _workspace(workspace, need, h.device)
     _check(load_library().nvfp4_add_rmsnorm_backward(
-        _ptr(dy), _ptr(h), _ptr(dh), _in_dtype(h), _ptr(weight), wd, _ptr(rstd), rows, cols,
-        _ptr(dx), _ptr(dweight), _ptr(workspace), size, _stream(stream)))
+        _like("dy", dy, shape, dtype), h.data_ptr(), _like("dh", dh, shape, dtype), _in_dtype(h),
+        weight.data_ptr(), _vector("weight", weight, cols), _floats("rstd", rstd, rows), rows,
+        cols, _like("dx", dx, shape, dtype), _floats("dweight", dweight, cols), _ptr(workspace),
+        size, _stream(stream)))
 
 
 def nvfp4_gemm_bias_act_workspace_size(m: int, n: int, k: int) -> int:
@@ -657,13 +663,13 @@ def nvfp4_gemm_bias_act(a: Operand, b: Operand, d: torch.Tensor,
     k = a.codes.shape[1] * 2
     if a.codes.shape[0] != m or b.codes.shape[0] != n or b.codes.shape[1] * 2 != k:
         raise ValueError("operand shapes do not match d")
-    _like("residual", residual, d)
-    _like("z", z, d)
+    shape, dtype = d.shape, d.dtype
     bd = _vector("bias", bias, n) if bias is not None else NVFP4_IN_FP32
     need = 0 if workspace is not None else nvfp4_gemm_bias_act_workspace_size(m, n, k)
     workspace, size = _workspace(workspace, need, d.device)
     ca, cb = a._c(), b._c()
-    epi = _CEpilogue(_ptr(bias), bd, act, _ptr(residual), _ptr(z))
+    epi = _CEpilogue(_ptr(bias), bd, act, _like("residual", residual, shape, dtype),
+                     _like("z", z, shape, dtype))
     _check(load_library().nvfp4_gemm_bias_act(C.byref(ca), C.byref(cb), m, n, k, C.byref(epi),
                                               _ptr(d), od, _ptr(workspace), size,
                                               _stream(stream)))
@@ -683,18 +689,16 @@ def nvfp4_bias_act_backward(dd: torch.Tensor, z: Optional[torch.Tensor], act: in
     """dz = dd * act'(z), dbias [cols] = its column sums, row_amax [rows] / col_amax [cols] =
     the maxima of |dz|, ready to be the amax_in of the quantization of dz."""
     rows, cols = _matrix(dd)
-    _like("z", z, dd)
-    _like("dz", dz, dd)
-    _floats("dbias", dbias, cols)
-    _floats("row_amax", row_amax, rows)
-    _floats("col_amax", col_amax, cols)
+    shape, dtype = dd.shape, dd.dtype
     size = 0
     if dbias is not None or row_amax is not None or col_amax is not None:
         need = 0 if workspace is not None else nvfp4_bias_act_backward_workspace_size(rows, cols)
         workspace, size = _workspace(workspace, need, dd.device)
     _check(load_library().nvfp4_bias_act_backward(
-        _ptr(dd), _ptr(z), _in_dtype(dd), act, rows, cols, _ptr(dz), _ptr(dbias),
-        _ptr(row_amax), _ptr(col_amax), _ptr(workspace), size, _stream(stream)))
+        dd.data_ptr(), _like("z", z, shape, dtype), _in_dtype(dd), act, rows, cols,
+        _like("dz", dz, shape, dtype), _floats("dbias", dbias, cols),
+        _floats("row_amax", row_amax, rows), _floats("col_amax", col_amax, cols),
+        _ptr(workspace), size, _stream(stream)))
 
 
 def nvfp4_clip_grad_norm_workspace_size() -> int:
@@ -704,17 +708,23 @@ def nvfp4_clip_grad_norm_workspace_size() -> int:
 
 
 def _tensor_list(tensors, out):
-    items = (_CTensor * len(tensors))()
-    for i, t in enumerate(tensors):
-        if not t.is_contiguous():
-            raise ValueError(f"tensor {i} must be contiguous")
-        o = t if out is None else out[i]
-        if o is not t and (o.dtype != t.dtype or o.numel() != t.numel()
-                           or not o.is_contiguous()):
-            raise ValueError(f"out {i} must be contiguous, of its tensor's type and size")
-        e = items[i]
-        e.data, e.out, e.n, e.dtype = t.data_ptr(), o.data_ptr(), t.numel(), _in_dtype(t)
-    return items
+    """The tensors as an array of nvfp4_tensor: four 64-bit words each (data, out, n, and
+    dtype with its padding)."""
+    T = torch.Tensor
+    data, sizes = list(map(T.data_ptr, tensors)), list(map(T.numel, tensors))
+    types = [t.dtype for t in tensors]
+    if not all(map(T.is_contiguous, tensors)):
+        raise ValueError("every tensor must be contiguous")
+    codes = [_DTYPE_CODES.get(t, -1) for t in types]
+    if -1 in codes:
+        raise TypeError(f"tensors must be bfloat16 or float32, got {types[codes.index(-1)]}")
+    to = data
+    if out is not None:
+        if [o.dtype for o in out] != types or list(map(T.numel, out)) != sizes or \
+                not all(map(T.is_contiguous, out)):
+            raise ValueError("out must be contiguous tensors of the tensors' types and sizes")
+        to = list(map(T.data_ptr, out))
+    return array("q", chain.from_iterable(zip(data, to, sizes, codes)))
 
 
 def nvfp4_grad_norm(tensors, norm: torch.Tensor, workspace: Optional[torch.Tensor] = None,
@@ -724,7 +734,8 @@ def nvfp4_grad_norm(tensors, norm: torch.Tensor, workspace: Optional[torch.Tenso
     need = 0 if workspace is not None else nvfp4_clip_grad_norm_workspace_size()
     workspace, size = _workspace(workspace, need, norm.device)
     items = _tensor_list(tensors, None)
-    _check(load_library().nvfp4_grad_norm(items, len(items), _ptr(norm), _ptr(workspace), size,
+    _check(load_library().nvfp4_grad_norm(items.buffer_info()[0], len(tensors), _ptr(norm),
+                                          _ptr(workspace), size,
                                           _stream(stream)))
 
 
@@ -738,8 +749,9 @@ def nvfp4_clip_grad_norm(tensors, max_norm: float, norm: torch.Tensor, out=None,
     need = 0 if workspace is not None else nvfp4_clip_grad_norm_workspace_size()
     workspace, size = _workspace(workspace, need, norm.device)
     items = _tensor_list(tensors, out)
-    _check(load_library().nvfp4_clip_grad_norm(items, len(items), max_norm, _ptr(norm),
-                                               _ptr(workspace), size, _stream(stream)))
+    _check(load_library().nvfp4_clip_grad_norm(items.buffer_info()[0], len(tensors), max_norm,
+                                               _ptr(norm), _ptr(workspace), size,
+                                               _stream(stream)))
 
 
 def alloc_out(lines: int, n: int, amax_len: int, device="cuda", fill=None) -> Out:

@@ -654,8 +654,9 @@ nvfp4_status gemm_impl(const nvfp4_operand* a, const nvfp4_operand* b, const int
     return fail(NVFP4_ERR_UNSUPPORTED, "grouped GEMM: n must be a multiple of 256");
   if (k_grouped && k % 256 != 0)
     return fail(NVFP4_ERR_UNSUPPORTED, "grouped wgrad GEMM: tokens must be a multiple of 256");
-  const GemmLayout L =
-      gemm_layout(m, n, k, group_ends && !k_grouped ? (int64_t)num_groups * n : n);
+  GemmLayout L = gemm_layout(m, n, k, group_ends && !k_grouped ? (int64_t)num_groups * n : n);
+  const bool few = epilogue != nullptr && gemm_few_rows(m);
+  if (few) L.workspace_bytes = gemm_few_workspace(m, n);
   if (L.tiles_m * L.tiles_n >= (1LL << 31)) return fail(NVFP4_ERR_UNSUPPORTED, "too many tiles");
   if (static_ws) {
     if ((uint64_t)L.workspace_bytes > (uint64_t)NVFP4_GEMM_STATIC_WS_BYTES)
@@ -691,7 +692,7 @@ nvfp4_status gemm_impl(const nvfp4_operand* a, const nvfp4_operand* b, const int
   g.num_groups = num_groups;
   g.k_grouped = k_grouped;
   g.epilogue = epilogue;
-  cudaError_t e = launch_gemm(g, dev, stream);
+  cudaError_t e = few ? launch_gemm_few(g, dev, stream) : launch_gemm(g, dev, stream);
   if (e != cudaSuccess) return cuda_fail(e, "gemm launch");
   return NVFP4_OK;
 }
@@ -706,7 +707,10 @@ nvfp4_status nvfp4_gemm(const nvfp4_operand* a, const nvfp4_operand* b, int64_t 
 
 nvfp4_status nvfp4_gemm_bias_act_workspace_size(int64_t m, int64_t n, int64_t k,
                                                 uint64_t* bytes) {
-  return nvfp4_gemm_workspace_size(m, n, k, bytes);
+  const nvfp4_status st = nvfp4_gemm_workspace_size(m, n, k, bytes);
+  if (st == NVFP4_OK && *bytes > 0 && gemm_few_rows(m))
+    *bytes = (uint64_t)gemm_few_workspace(m, n);
+  return st;
 }
 
 nvfp4_status nvfp4_gemm_bias_act(const nvfp4_operand* a, const nvfp4_operand* b, int64_t m,

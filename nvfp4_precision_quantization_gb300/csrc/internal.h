@@ -243,6 +243,11 @@ struct GemmArgs {
   bool k_grouped;
   const Epilogue* epilogue;  // optional, not with groups
 };
+// Few rows of A (kernels_gemm_few.cu), with an epilogue: B streamed once.
+constexpr int64_t kGemmFewRows = 128;
+bool gemm_few_rows(int64_t m);
+int64_t gemm_few_workspace(int64_t m, int64_t n);  // bytes
+cudaError_t launch_gemm_few(const GemmArgs& a, const DeviceInfo& dev, cudaStream_t stream);
 struct GemmLayout {
   int64_t k_tiles, tiles_m, tiles_n;
   int64_t sfa_bytes, sfb_bytes, sfb_offset, workspace_bytes;

@@ -566,25 +566,25 @@ int resident_ctas(K kernel, int threads) {
   return std::max(1, n);
 }
 
-// A ring kernel's limits on this device: CTAs per SM by registers, its static shared memory.
+// A ring kernel's CTAs per SM by registers, and its static shared memory.
+constexpr int kCtaSmem = 227 << 10;  // shared memory that one CTA may have
 struct RingKernel {
   int resident;
   int static_bytes;
 };
 template <typename K>
 RingKernel ring_kernel(K kernel, int threads) {
-  RingKernel r{resident_ctas(kernel, threads), 0};
   cudaFuncAttributes f;
-  constexpr int kMax = 227 << 10;  // per CTA
-  if (cudaFuncGetAttributes(&f, kernel) != cudaSuccess ||
-      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                           kMax - (int)f.sharedSizeBytes) != cudaSuccess) {
+  if (cudaFuncGetAttributes(&f, kernel) != cudaSuccess) {
     cudaGetLastError();
-    r.resident = 0;
-  } else {
-    r.static_bytes = (int)f.sharedSizeBytes;
+    return {0, 0};
   }
-  return r;
+  return {resident_ctas(kernel, threads), (int)f.sharedSizeBytes};
+}
+template <typename K>
+cudaError_t allow_ring(K kernel, const RingKernel& k) {  // on the current device
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              kCtaSmem - k.static_bytes);
 }
 
 // CTAs per SM and the ring of each: as many CTAs as the registers allow while each keeps
@@ -599,7 +599,7 @@ RingPlan plan_ring(const RingKernel& k, int tensors, int64_t group_bytes) {
   for (int c = k.resident; c > 0; --c) {
     // an SM's 228 KB, of which every CTA takes 1 KB beside its own
     const int64_t room =
-        std::min<int64_t>(227 << 10, (228 << 10) / c - (1 << 10)) - k.static_bytes;
+        std::min<int64_t>(kCtaSmem, (228 << 10) / c - (1 << 10)) - k.static_bytes;
     if (room < 2 * stage) continue;
     p.ctas = c;
     p.g.stages = (int)std::min<int64_t>(kRingStages, room / stage);
@@ -624,6 +624,8 @@ cudaError_t run_norm(const NormKernelArgs& k, const DeviceInfo& dev, cudaStream_
                                  (int64_t)kTeams * k.cols * (BF16 ? 2 : 4));
     const int64_t fill = (int64_t)p.ctas * dev.num_sms;
     if (p.ctas > 0 && groups > 2 * fill) {
+      const cudaError_t e = allow_ring(ring, limits);
+      if (e != cudaSuccess) return e;
       ring<<<(unsigned)fill, kThreads, p.g.stages * p.g.stage_bytes, stream>>>(k, p.g);
       return cudaGetLastError();
     }
@@ -664,6 +666,8 @@ cudaError_t run_norm_backward(const NormBackwardKernelArgs& k, int max_parts,
                                  (int64_t)kTeams * k.cols * (BF16 ? 2 : 4));
     const int64_t fill = std::min<int64_t>((int64_t)p.ctas * dev.num_sms, max_parts);
     if (p.ctas > 0 && groups > 2 * fill) {
+      const cudaError_t e = allow_ring(ring, limits);
+      if (e != cudaSuccess) return e;
       *parts = (int)fill;
       ring<<<(unsigned)fill, kThreads, p.g.stages * p.g.stage_bytes, stream>>>(k, p.g);
       return cudaGetLastError();
