@@ -655,7 +655,7 @@ nvfp4_status gemm_impl(const nvfp4_operand* a, const nvfp4_operand* b, const int
   if (k_grouped && k % 256 != 0)
     return fail(NVFP4_ERR_UNSUPPORTED, "grouped wgrad GEMM: tokens must be a multiple of 256");
   GemmLayout L = gemm_layout(m, n, k, group_ends && !k_grouped ? (int64_t)num_groups * n : n);
-  const bool few = epilogue != nullptr && gemm_few_rows(m);
+  const bool few = epilogue != nullptr && gemm_few(m, n);
   if (few) L.workspace_bytes = gemm_few_workspace(m, n);
   if (L.tiles_m * L.tiles_n >= (1LL << 31)) return fail(NVFP4_ERR_UNSUPPORTED, "too many tiles");
   if (static_ws) {
@@ -708,7 +708,7 @@ nvfp4_status nvfp4_gemm(const nvfp4_operand* a, const nvfp4_operand* b, int64_t 
 nvfp4_status nvfp4_gemm_bias_act_workspace_size(int64_t m, int64_t n, int64_t k,
                                                 uint64_t* bytes) {
   const nvfp4_status st = nvfp4_gemm_workspace_size(m, n, k, bytes);
-  if (st == NVFP4_OK && *bytes > 0 && gemm_few_rows(m))
+  if (st == NVFP4_OK && *bytes > 0 && gemm_few(m, n))
     *bytes = (uint64_t)gemm_few_workspace(m, n);
   return st;
 }

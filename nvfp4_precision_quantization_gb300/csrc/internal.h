@@ -243,9 +243,8 @@ struct GemmArgs {
   bool k_grouped;
   const Epilogue* epilogue;  // optional, not with groups
 };
-// Few rows of A (kernels_gemm_few.cu), with an epilogue: B streamed once.
-constexpr int64_t kGemmFewRows = 128;
-bool gemm_few_rows(int64_t m);
+// Few rows of A, or few tiles (kernels_gemm_few.cu), with an epilogue.
+bool gemm_few(int64_t m, int64_t n);
 int64_t gemm_few_workspace(int64_t m, int64_t n);  // bytes
 cudaError_t launch_gemm_few(const GemmArgs& a, const DeviceInfo& dev, cudaStream_t stream);
 struct GemmLayout {

@@ -70,7 +70,9 @@ def _check(m, n, k, dtype, name, bias, residual, keep, seed, modes=(RS, RS),
 SIZES = [(1, 256, 256), (1, 1, 32), (1, 4097, 512), (2, 100, 96), (7, 300, 320), (8, 512, 1024),
          (16, 1000, 544), (17, 129, 64), (31, 64, 800), (33, 640, 256), (64, 255, 288),
          (65, 384, 512), (100, 77, 96), (128, 256, 128), (129, 257, 160), (200, 520, 992),
-         (300, 500, 320)]
+         (300, 500, 320),
+         # past the few-rows kernel: row and tile counts that go to the tiled one
+         (385, 6000, 64), (450, 5000, 96), (1000, 2561, 160)]
 
 
 @pytest.mark.parametrize("m,n,k", SIZES)
@@ -96,6 +98,12 @@ def test_unaligned_outputs(m, offset, dtype):
     _check(m, 264, 128, dtype, "silu", torch.float32, True, True, m, offset=offset)
 
 
+@pytest.mark.parametrize("m,n", [(1, 5000), (40, 20000), (1, 40000), (129, 10100)])
+def test_tiles_cut_along_k(m, n):
+    """More tiles than SMs with a rest that is cut along K, beside whole tiles."""
+    _check(m, n, 2080, torch.bfloat16, "gelu", torch.float32, True, True, m)
+
+
 @pytest.mark.parametrize("m", [1, 20, 130])
 def test_long_k(m):
     """Long sums, every K tile of a split: the bound is still a small part of one term's
@@ -104,9 +112,9 @@ def test_long_k(m):
 
 
 def test_plain_epilogue_is_the_gemm():
-    """Without bias, activation and residual d is nvfp4_gemm's."""
-    (a, b), _, _ = _operands(200, 300, 512, 4)
-    d, e = (torch.empty(200, 300, device=DEV) for _ in range(2))
+    """Without bias, activation and residual d is nvfp4_gemm's (many rows: the same sums)."""
+    (a, b), _, _ = _operands(1100, 2400, 512, 4)
+    d, e = (torch.empty(1100, 2400, device=DEV) for _ in range(2))
     nv.nvfp4_gemm(a, b, d)
     nv.nvfp4_gemm_bias_act(a, b, e)
     assert torch.equal(d, e)
