@@ -31,34 +31,85 @@ __device__ __forceinline__ float act_value(float z) {
   return z;
 }
 
-// p = 1 / (1 + exp(-x)) and q = p (1 - p) from t = exp(-|x|) <= 1: 1 - p is t / (1 + t) for
-// positive x, never the difference of 1 and a rounded p (GELU's slope multiplies q by up
-// to z u' of about 100 before q vanishes).
-__device__ __forceinline__ void sigmoid_pair(float x, float& p, float& q) {
-  const float t = __expf(-fabsf(x));
-  const float r = __fdividef(1.0f, __fadd_rn(1.0f, t));
-  const float tr = __fmul_rn(t, r);
-  p = x >= 0.0f ? r : tr;
-  q = __fmul_rn(r, tr);
+// Two FP32 values side by side: one packed instruction each (sm_100+).
+struct Pair {
+  float x, y;
+};
+__device__ __forceinline__ Pair pair_fma(Pair a, Pair b, Pair c) {
+  Pair d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ Pair pair_mul(Pair a, Pair b) {
+  Pair d;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "mul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ Pair pair_add(Pair a, Pair b) {
+  Pair d;
+  asm("{\n\t.reg .b64 a, b, d;\n\t"
+      "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+__device__ __forceinline__ float ex2_approx(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float rcp_approx(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// m with the sign of z (m >= 0)
+__device__ __forceinline__ float with_sign(float m, float z) {
+  return __uint_as_float(__float_as_uint(m) | (__float_as_uint(z) & 0x80000000u));
 }
 
-// d act / d z = p + z p (1 - p) u' with u' bounded: where z^2 > 10^4 the factor p (1 - p) is
-// 0 and must not meet an infinite u'.
+// act'(z) of a pair.  GELU and SILU are z p(u), p = 1 / (1 + exp(-u)), u odd in z, so with
+// a = |z|, t = exp(-u(a)) <= 1 and r = 1 / (1 + t) = p(u(a)):
+//   act' = 1/2 + sgn(z) (r - 1/2 + a t r^2 u'(a)),
+// where p (1 - p) = t r^2 is never the difference of 1 and a rounded p (it is multiplied by
+// a u' of up to 100 before it vanishes).  a is cut at 64, where t is 0 or below 2^-92, so that
+// 0 never meets an infinite u'; a NaN stays one.
 template <int ACT>
-__device__ __forceinline__ float act_slope(float z) {
-  if constexpr (ACT == kActRelu) return z > 0.0f ? 1.0f : 0.0f;
-  float p, q;
+__device__ __forceinline__ Pair act_slope(Pair z) {
+  if constexpr (ACT == kActRelu) return {z.x > 0.0f ? 1.0f : 0.0f, z.y > 0.0f ? 1.0f : 0.0f};
+  if constexpr (ACT != kActGelu && ACT != kActSilu) return {1.0f, 1.0f};
+  constexpr float kLog2e = 1.4426950408889634f;
+  Pair a;
+  asm("min.NaN.f32 %0, %1, 0f42800000;" : "=f"(a.x) : "f"(fabsf(z.x)));
+  asm("min.NaN.f32 %0, %1, 0f42800000;" : "=f"(a.y) : "f"(fabsf(z.y)));
+  Pair w, du;  // u(a) log2(e), u'(a)
   if constexpr (ACT == kActGelu) {
-    const float z2 = fminf(__fmul_rn(z, z), 1e4f);
-    sigmoid_pair(__fmul_rn(z, __fmaf_rn(kGelu2C * kGeluA, z2, kGelu2C)), p, q);
-    const float du = __fmaf_rn(3.0f * kGelu2C * kGeluA, z2, kGelu2C);
-    return __fmaf_rn(__fmul_rn(z, q), du, p);
+    constexpr float c0 = kGelu2C * kLog2e, c1 = kGelu2C * kGeluA * kLog2e;
+    constexpr float d1 = 3.0f * kGelu2C * kGeluA;
+    const Pair a2 = pair_mul(a, a);
+    w = pair_mul(a, pair_fma({c1, c1}, a2, {c0, c0}));
+    du = pair_fma({d1, d1}, a2, {kGelu2C, kGelu2C});
+  } else {
+    w = pair_mul(a, {kLog2e, kLog2e});
+    du = {1.0f, 1.0f};
   }
-  if constexpr (ACT == kActSilu) {
-    sigmoid_pair(z, p, q);
-    return __fmaf_rn(z, q, p);
-  }
-  return 1.0f;
+  const Pair t = {ex2_approx(-w.x), ex2_approx(-w.y)};
+  const Pair one_t = pair_add(t, {1.0f, 1.0f});
+  const Pair r = {rcp_approx(one_t.x), rcp_approx(one_t.y)};
+  const Pair q = pair_mul(pair_mul(t, r), r);
+  Pair aq = pair_mul(a, q);
+  if constexpr (ACT == kActGelu) aq = pair_mul(aq, du);
+  const Pair m = pair_add(pair_add(r, {-0.5f, -0.5f}), aq);
+  return pair_add({with_sign(m.x, z.x), with_sign(m.y, z.y)}, {0.5f, 0.5f});
 }
 
 }  // namespace nvfp4

@@ -21,7 +21,6 @@ namespace {
 constexpr int kActThreads = 256;
 constexpr int kActWarps = kActThreads / 32;
 constexpr int kActMaxCtas = 1024;  // bound of the main kernel's grid, for the workspace
-constexpr int kStrip = 32 * kChunk;  // columns of one warp
 
 struct ActKernelArgs {
   const void* dd;
@@ -36,65 +35,162 @@ struct ActKernelArgs {
   int g_dd, g_z, g_dz;
 };
 
+// 32 bytes of a row, one lane's columns: 16 BF16 or 8 FP32.
+template <bool BF16>
+struct Sector {
+  static constexpr int kCols = BF16 ? 16 : 8;
+  uint32_t w[8];
+  __device__ __forceinline__ void load(const void* base, int64_t off, int n, int grain) {
+    const char* p = static_cast<const char*>(base) + off * (BF16 ? 2 : 4);
+    if (n == kCols && grain == 32) {
+      ldg_v8(p, w);
+    } else if (n == kCols && grain == 16) {
+      ldg_v4(p, w);
+      ldg_v4(p + 16, w + 4);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) w[i] = 0;
+#pragma unroll
+      for (int i = 0; i < kCols; ++i)
+        if (i < n) {
+          if constexpr (BF16)
+            w[i >> 1] |= (uint32_t) reinterpret_cast<const uint16_t*>(p)[i] << (16 * (i & 1));
+          else
+            w[i] = reinterpret_cast<const uint32_t*>(p)[i];
+        }
+    }
+  }
+  __device__ __forceinline__ void store(void* base, int64_t off, int n, int grain) const {
+    char* p = static_cast<char*>(base) + off * (BF16 ? 2 : 4);
+    if (n == kCols && grain == 32) {
+      stg_v8(p, w);
+    } else if (n == kCols && grain == 16) {
+      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(p + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kCols; ++i)
+        if (i < n) {
+          if constexpr (BF16)
+            reinterpret_cast<uint16_t*>(p)[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+          else
+            reinterpret_cast<uint32_t*>(p)[i] = w[i];
+        }
+    }
+  }
+  // columns 2k and 2k + 1
+  __device__ __forceinline__ Pair get(int k) const {
+    if constexpr (BF16) return {bf16_lo(w[k]), bf16_hi(w[k])};
+    else return {__uint_as_float(w[2 * k]), __uint_as_float(w[2 * k + 1])};
+  }
+  __device__ __forceinline__ void set(int k, Pair v) {
+    if constexpr (BF16) {
+      w[k] = bf16x2_bits(v.x, v.y);
+    } else {
+      w[2 * k] = __float_as_uint(v.x);
+      w[2 * k + 1] = __float_as_uint(v.y);
+    }
+  }
+};
+
+// max |a|, |b| of the values in a word (one FP32 or a pair of BF16), NaN skipped; the sign
+// bits of the result mean nothing.
+template <bool BF16>
+__device__ __forceinline__ uint32_t word_absmax(uint32_t a, uint32_t b) {
+  if constexpr (BF16) return absmax_bf16x2(a, b);
+  return __float_as_uint(fmaxf(fabsf(__uint_as_float(a)), fabsf(__uint_as_float(b))));
+}
+template <bool BF16>
+__device__ __forceinline__ float word_value(uint32_t a) {
+  if constexpr (BF16) return bf16x2_hmax_f32(a);
+  return __uint_as_float(a);
+}
+
 template <bool BF16, int ACT>
-__global__ void __launch_bounds__(kActThreads, 2) k_bias_act_backward(const ActKernelArgs a) {
+__global__ void __launch_bounds__(kActThreads, 3) k_bias_act_backward(const ActKernelArgs a) {
+  using S = Sector<BF16>;
+  constexpr int kCols = S::kCols, kStrip = 32 * kCols;
   __shared__ float s_sum[kStrip], s_max[kStrip];
+  pdl_launch_dependents();  // the join may be set up meanwhile
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int strip = blockIdx.x % a.strips, part = blockIdx.x / a.strips;
   const int sub = lane / a.lanes, step = 32 / a.lanes;  // rows side by side in the warp
-  const int64_t col = (int64_t)strip * kStrip + (lane % a.lanes) * kChunk;
-  const int n_col = chunk_len(col, a.cols);
+  const int64_t col = (int64_t)strip * kStrip + (lane % a.lanes) * kCols;
+  const int n_col = (int)max((int64_t)0, min((int64_t)kCols, a.cols - col));
   // this warp's rows
   const int64_t warps = (int64_t)a.row_parts * kActWarps, w = (int64_t)part * kActWarps + warp;
   const int64_t r0 = a.rows * w / warps, r1 = a.rows * (w + 1) / warps;
-  float sum[kChunk], mx[kChunk];
+  Pair sum[kCols / 2];
+  uint32_t mx[8];  // word by word, as dz is stored
 #pragma unroll
-  for (int i = 0; i < kChunk; ++i) sum[i] = mx[i] = 0.0f;
+  for (int i = 0; i < kCols / 2; ++i) sum[i] = {0.0f, 0.0f};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) mx[i] = 0;
+  // the next row's words are loaded before this row's are used
+  S nd, nz;
+  auto fetch = [&](int64_t r) {
+    const int n = r < r1 ? n_col : 0;
+    nd.load(a.dd, r * a.cols + col, n, a.g_dd);
+    if constexpr (ACT != kActNone) nz.load(a.z, r * a.cols + col, n, a.g_z);
+  };
+  fetch(r0 + sub);
   for (int64_t rb = r0; rb < r1; rb += step) {
     const int64_t r = rb + sub;
-    const int n = r < r1 ? n_col : 0;
-    const int64_t off = r * a.cols + col;
-    Chunk<BF16> cd, cz;
-    cd.load(a.dd, off, n, a.g_dd);
-    if constexpr (ACT != kActNone) cz.load(a.z, off, n, a.g_z);
-    float v[kChunk];
+    S d = nd, z;
+    if constexpr (ACT != kActNone) z = nz;
+    if (rb + step < r1) fetch(r + step);
 #pragma unroll
-    for (int i = 0; i < kChunk; ++i) {
-      v[i] = cd.get(i);
-      if constexpr (ACT != kActNone) v[i] = __fmul_rn(v[i], act_slope<ACT>(cz.get(i)));
-      sum[i] = __fadd_rn(sum[i], v[i]);
+    for (int i = 0; i < kCols / 2; ++i) {
+      Pair v = d.get(i);
+      if constexpr (ACT != kActNone) v = pair_mul(v, act_slope<ACT>(z.get(i)));
+      sum[i] = pair_add(sum[i], v);
+      d.set(i, v);
     }
-    cd.set(v);
-    cd.store(a.dz, off, n, a.g_dz);
-    float rm = 0.0f;
+    d.store(a.dz, r * a.cols + col, r < r1 ? n_col : 0, a.g_dz);
 #pragma unroll
-    for (int i = 0; i < kChunk; ++i) {
-      const float m = fabsf(cd.get(i));
-      mx[i] = fmaxf(mx[i], m);
-      rm = fmaxf(rm, m);
-    }
+    for (int i = 0; i < 8; ++i) mx[i] = word_absmax<BF16>(mx[i], d.w[i]);
     if (a.row_max != nullptr) {
-      for (int d = a.lanes >> 1; d > 0; d >>= 1)
-        rm = fmaxf(rm, __shfl_xor_sync(0xffffffffu, rm, d));
-      if (r < r1 && lane % a.lanes == 0) a.row_max[(int64_t)strip * a.rows + r] = rm;
+      uint32_t m = 0;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) m = word_absmax<BF16>(m, d.w[i]);
+      // as bits: non-negative values are ordered like them
+      uint32_t bits = __float_as_uint(word_value<BF16>(m));
+      if (a.lanes == 32) {
+        bits = __reduce_max_sync(0xffffffffu, bits);
+      } else {
+        for (int k = a.lanes >> 1; k > 0; k >>= 1)
+          bits = max(bits, __shfl_xor_sync(0xffffffffu, bits, k));
+      }
+      if (r < r1 && lane % a.lanes == 0)
+        a.row_max[(int64_t)strip * a.rows + r] = __uint_as_float(bits);
     }
   }
   if (a.col_sum == nullptr && a.col_max == nullptr) return;
-  // rows side by side, then the CTA's warps in their order
-  for (int d = 16; d >= a.lanes; d >>= 1) {
+  // rows side by side, then the CTA's warps in their order; column c of the strip is kept at
+  // (c % kCols) * 32 + c / kCols (no bank conflicts)
+  float cmax[kCols], csum[kCols];
 #pragma unroll
-    for (int i = 0; i < kChunk; ++i) {
-      sum[i] = __fadd_rn(sum[i], __shfl_xor_sync(0xffffffffu, sum[i], d));
-      mx[i] = fmaxf(mx[i], __shfl_xor_sync(0xffffffffu, mx[i], d));
+  for (int i = 0; i < kCols; ++i) {
+    csum[i] = (i & 1) ? sum[i / 2].y : sum[i / 2].x;
+    if constexpr (BF16)
+      cmax[i] = __uint_as_float(((i & 1) ? mx[i / 2] & 0xffff0000u : mx[i / 2] << 16) & 0x7fffffffu);
+    else
+      cmax[i] = __uint_as_float(mx[i]);
+  }
+  for (int k = 16; k >= a.lanes; k >>= 1) {
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) {
+      csum[i] = __fadd_rn(csum[i], __shfl_xor_sync(0xffffffffu, csum[i], k));
+      cmax[i] = fmaxf(cmax[i], __shfl_xor_sync(0xffffffffu, cmax[i], k));
     }
   }
   for (int k = 0; k < kActWarps; ++k) {
     if (warp == k && lane < a.lanes) {
 #pragma unroll
-      for (int i = 0; i < kChunk; ++i) {
-        const int c = i * 32 + lane;  // lane-major columns: no bank conflicts
-        s_sum[c] = k == 0 ? sum[i] : __fadd_rn(s_sum[c], sum[i]);
-        s_max[c] = k == 0 ? mx[i] : fmaxf(s_max[c], mx[i]);
+      for (int i = 0; i < kCols; ++i) {
+        const int c = i * 32 + lane;
+        s_sum[c] = k == 0 ? csum[i] : __fadd_rn(s_sum[c], csum[i]);
+        s_max[c] = k == 0 ? cmax[i] : fmaxf(s_max[c], cmax[i]);
       }
     }
     __syncthreads();
@@ -102,7 +198,7 @@ __global__ void __launch_bounds__(kActThreads, 2) k_bias_act_backward(const ActK
   for (int c = threadIdx.x; c < kStrip; c += kActThreads) {
     const int64_t gc = (int64_t)strip * kStrip + c;
     if (gc >= a.cols) break;
-    const int at = (c % kChunk) * 32 + c / kChunk;
+    const int at = (c % kCols) * 32 + c / kCols;
     if (a.col_sum != nullptr) a.col_sum[(int64_t)part * a.cols + gc] = s_sum[at];
     if (a.col_max != nullptr) a.col_max[(int64_t)part * a.cols + gc] = s_max[at];
   }
@@ -123,12 +219,14 @@ struct ActReduceArgs {
 // The first col_ctas CTAs join 32 columns each (warp w the parts w, w + 8, ..., then the
 // warps in turn), the others 256 rows each.
 __global__ void __launch_bounds__(256) k_act_join(const ActReduceArgs a) {
+  pdl_wait();
   if ((int)blockIdx.x < a.col_ctas) {
     __shared__ float s_sum[8][32], s_max[8][32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t c = (int64_t)blockIdx.x * 32 + lane;
     float sum = 0.0f, mx = 0.0f;
     if (c < a.cols) {
+#pragma unroll 4
       for (int p = warp; p < a.row_parts; p += 8) {
         if (a.dbias != nullptr) sum = __fadd_rn(sum, a.col_sum[(int64_t)p * a.cols + c]);
         if (a.col_amax != nullptr) mx = fmaxf(mx, a.col_max[(int64_t)p * a.cols + c]);
@@ -150,14 +248,19 @@ __global__ void __launch_bounds__(256) k_act_join(const ActReduceArgs a) {
     const int64_t r = (int64_t)(blockIdx.x - a.col_ctas) * 256 + threadIdx.x;
     if (r >= a.rows) return;
     float mx = 0.0f;
+#pragma unroll 8
     for (int s = 0; s < a.strips; ++s) mx = fmaxf(mx, a.row_max[(int64_t)s * a.rows + r]);
     a.row_amax[r] = mx;
   }
 }
 
-int64_t strips_of(int64_t cols) { return (cols + kStrip - 1) / kStrip; }
-int64_t max_row_parts(int64_t cols) {
-  return std::max<int64_t>(1, kActMaxCtas / strips_of(cols));
+// strips of 32 lanes: 512 BF16 or 256 FP32 columns
+int64_t strips_of(int64_t cols, bool bf16) {
+  const int strip = bf16 ? 32 * Sector<true>::kCols : 32 * Sector<false>::kCols;
+  return (cols + strip - 1) / strip;
+}
+int64_t max_row_parts(int64_t cols, bool bf16) {
+  return std::max<int64_t>(1, kActMaxCtas / strips_of(cols, bf16));
 }
 int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
 
@@ -195,7 +298,9 @@ cudaError_t pick_act(int act, ActKernelArgs& k, const DeviceInfo& dev, cudaStrea
 }  // namespace
 
 int64_t bias_act_backward_workspace(int64_t rows, int64_t cols) {
-  return 2 * round16(4 * max_row_parts(cols) * cols) + round16(4 * strips_of(cols) * rows);
+  // the larger of the two types' needs, part by part
+  return 2 * round16(4 * max_row_parts(cols, true) * cols) +
+         round16(4 * strips_of(cols, false) * rows);
 }
 
 cudaError_t launch_bias_act_backward(const ActBackwardArgs& a, const DeviceInfo& dev,
@@ -211,7 +316,8 @@ cudaError_t launch_bias_act_backward(const ActBackwardArgs& a, const DeviceInfo&
   }
   const int e = a.in == InType::BF16 ? 2 : 4;
   char* ws = static_cast<char*>(a.workspace);
-  const int64_t col_bytes = round16(4 * max_row_parts(a.cols) * a.cols);
+  const bool bf16 = a.in == InType::BF16;
+  const int64_t col_bytes = round16(4 * max_row_parts(a.cols, bf16) * a.cols);
   ActKernelArgs k{};
   k.dd = a.dd;
   k.z = a.z;
@@ -221,9 +327,9 @@ cudaError_t launch_bias_act_backward(const ActBackwardArgs& a, const DeviceInfo&
   k.row_max = a.row_amax ? reinterpret_cast<float*>(ws + 2 * col_bytes) : nullptr;
   k.rows = a.rows;
   k.cols = a.cols;
-  k.strips = (int)strips_of(a.cols);
+  k.strips = (int)strips_of(a.cols, bf16);
   k.lanes = 32;
-  while (k.lanes > 1 && (int64_t)(k.lanes / 2) * kChunk >= a.cols) k.lanes /= 2;
+  while (k.lanes > 1 && (int64_t)(k.lanes / 2) * (bf16 ? 16 : 8) >= a.cols) k.lanes /= 2;
   k.g_dd = row_grain(a.dd, a.cols, e);
   k.g_z = row_grain(a.z, a.cols, e);
   k.g_dz = row_grain(a.dz, a.cols, e);
@@ -243,8 +349,7 @@ cudaError_t launch_bias_act_backward(const ActBackwardArgs& a, const DeviceInfo&
   r.row_parts = k.row_parts;
   r.col_ctas = a.dbias || a.col_amax ? (int)((a.cols + 31) / 32) : 0;
   const int64_t row_ctas = a.row_amax ? (a.rows + 255) / 256 : 0;
-  k_act_join<<<(unsigned)(r.col_ctas + row_ctas), 256, 0, stream>>>(r);
-  return cudaGetLastError();
+  return launch_after(k_act_join, (unsigned)(r.col_ctas + row_ctas), 256, stream, r);
 }
 
 }  // namespace nvfp4

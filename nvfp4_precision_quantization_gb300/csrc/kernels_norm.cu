@@ -452,6 +452,7 @@ __device__ __forceinline__ void backward_partials(const NormBackwardKernelArgs& 
 template <bool BF16, int TPR, int NCH>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
     k_add_rmsnorm_backward(const NormBackwardKernelArgs a) {
+  pdl_launch_dependents();  // the columns' sum may be set up meanwhile
   constexpr int kThreads = TPR < 256 ? 256 : TPR;
   constexpr int kTeams = kThreads / TPR;
   __shared__ float2 red[2][kThreads / 32];
@@ -488,6 +489,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
 template <bool BF16, int TPR, int NCH>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
     k_add_rmsnorm_backward_ring(const NormBackwardKernelArgs a, const RingArgs g) {
+  pdl_launch_dependents();  // the columns' sum may be set up meanwhile
   constexpr int kThreads = TPR < 256 ? 256 : TPR;
   constexpr int kTeams = kThreads / TPR;
   constexpr int kElem = BF16 ? 2 : 4;
@@ -542,10 +544,12 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
 __global__ void __launch_bounds__(256) k_column_sum(const float* part, int n, int64_t cols,
                                                     float* out) {
   __shared__ float s[8][32];
+  pdl_wait();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t col = (int64_t)blockIdx.x * 32 + lane;
   float sum = 0.0f;
   if (col < cols)
+#pragma unroll 4
     for (int r = warp; r < n; r += 8) sum = __fadd_rn(sum, part[(int64_t)r * cols + col]);
   s[warp][lane] = sum;
   __syncthreads();
@@ -694,8 +698,7 @@ cudaError_t pick_norm_backward(const NormBackwardKernelArgs& k, int max_parts,
 
 cudaError_t launch_column_sum(const float* part, int n, int64_t cols, float* out,
                               cudaStream_t stream) {
-  k_column_sum<<<(unsigned)((cols + 31) / 32), 256, 0, stream>>>(part, n, cols, out);
-  return cudaGetLastError();
+  return launch_after(k_column_sum, (unsigned)((cols + 31) / 32), 256, stream, part, n, cols, out);
 }
 
 cudaError_t launch_add_rmsnorm(const NormArgs& a, const DeviceInfo& dev, cudaStream_t stream) {

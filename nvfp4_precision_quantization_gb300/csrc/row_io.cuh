@@ -16,6 +16,23 @@ namespace nvfp4 {
 
 constexpr int kChunk = 16;  // elements per thread and access group
 
+// Launch a kernel whose set-up may overlap the end of the one before it in the stream; it
+// begins with pdl_wait().
+template <typename... P>
+inline cudaError_t launch_after(void (*kernel)(P...), unsigned grid, unsigned threads,
+                                cudaStream_t stream, const P&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.stream = stream;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // The grain of rows of `cols` elements of `elem` bytes at p.
 inline int row_grain(const void* p, int64_t cols, int elem) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(p) | (uintptr_t)(cols * elem);
