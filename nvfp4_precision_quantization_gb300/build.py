@@ -20,8 +20,10 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD_DIR = os.path.join(HERE, "_build", platform.machine())
 SOURCES = ["api.cu", "kernels_amax.cu", "kernels_quantize.cu", "kernels_misc.cu",
            "kernels_gemm.cu", "kernels_rht.cu", "api_layer.cu", "kernels_norm.cu",
+           "kernels_norm_backward.cu",
            "kernels_act.cu", "kernels_clip.cu", "kernels_gemm_few.cu"]
 HEADERS = ["device_common.cuh", "internal.h", "tile_pipeline.cuh", "api_common.h", "row_io.cuh",
+           "row_ring.cuh",
            "activation.cuh", "tcgen05.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]

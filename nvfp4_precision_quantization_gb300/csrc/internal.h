@@ -299,9 +299,6 @@ constexpr int64_t kNormBackwardParts = 608;  // at most this many CTAs, one part
 int64_t add_rmsnorm_backward_workspace(int64_t rows, int64_t cols);
 cudaError_t launch_add_rmsnorm_backward(const NormBackwardArgs& a, const DeviceInfo& dev,
                                         cudaStream_t stream);
-// out[c] = sum of the n rows of part [n][cols], in a fixed order
-cudaError_t launch_column_sum(const float* part, int n, int64_t cols, float* out,
-                              cudaStream_t stream);
 
 // Gradients of bias and activation (kernels_act.cu).
 struct ActBackwardArgs {

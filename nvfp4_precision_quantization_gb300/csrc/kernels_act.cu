@@ -78,6 +78,19 @@ struct Sector {
         }
     }
   }
+  // The store of a warp whose lanes hold consecutive sectors (`run` columns exist from lane
+  // 0's on), in rows whose grain does not allow 16-byte accesses.
+  template <bool STAGED>
+  __device__ __forceinline__ void store_warp(void* base, int64_t off, int n, int64_t run,
+                                             int grain, uint8_t* smem, int lane) const {
+    constexpr int kElem = BF16 ? 2 : 4;
+    if (!STAGED || grain >= 16 || smem == nullptr) {
+      store(base, off, n, grain);
+      return;
+    }
+    staged_store<8, 32>(static_cast<char*>(base) + (off - (int64_t)kCols * lane) * kElem,
+                        (int)run * kElem, grain, smem, lane, w);
+  }
   // columns 2k and 2k + 1
   __device__ __forceinline__ Pair get(int k) const {
     if constexpr (BF16) return {bf16_lo(w[k]), bf16_hi(w[k])};
@@ -90,6 +103,27 @@ struct Sector {
       w[2 * k] = __float_as_uint(v.x);
       w[2 * k + 1] = __float_as_uint(v.y);
     }
+  }
+};
+
+// The load of such a warp: issue() for every tensor, settle() when the values are needed.
+template <bool BF16, bool STAGED>
+struct SectorLoad {
+  Sector<BF16> s;
+  StagedLoad<8, 32> raw;
+  __device__ __forceinline__ void issue(const void* base, int64_t off, int n, int64_t run,
+                                        int grain, const uint8_t* smem, int lane) {
+    constexpr int kElem = BF16 ? 2 : 4;
+    if (!STAGED || grain >= 16 || smem == nullptr) s.load(base, off, n, grain);
+    else
+      raw.issue(static_cast<const char*>(base) + (off - (int64_t)Sector<BF16>::kCols * lane) * kElem,
+                (int)run * kElem, grain, lane);
+  }
+  __device__ __forceinline__ const Sector<BF16>& settle(int grain, uint8_t* smem, int lane) {
+    if constexpr (STAGED) {
+      if (grain < 16 && smem != nullptr) raw.settle(grain, smem, lane, s.w);
+    }
+    return s;
   }
 };
 
@@ -106,17 +140,22 @@ __device__ __forceinline__ float word_value(uint32_t a) {
   return __uint_as_float(a);
 }
 
-template <bool BF16, int ACT>
-__global__ void __launch_bounds__(kActThreads, 3) k_bias_act_backward(const ActKernelArgs a) {
+template <bool BF16, int ACT, bool STAGED>
+__global__ void __launch_bounds__(kActThreads, STAGED ? 2 : 3)
+    k_bias_act_backward(const ActKernelArgs a) {
   using S = Sector<BF16>;
   constexpr int kCols = S::kCols, kStrip = 32 * kCols;
   __shared__ float s_sum[kStrip], s_max[kStrip];
+  __shared__ __align__(16) uint8_t stages[STAGED ? kActWarps : 1][kStageBytes];
   pdl_launch_dependents();  // the join may be set up meanwhile
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int strip = blockIdx.x % a.strips, part = blockIdx.x / a.strips;
   const int sub = lane / a.lanes, step = 32 / a.lanes;  // rows side by side in the warp
   const int64_t col = (int64_t)strip * kStrip + (lane % a.lanes) * kCols;
   const int n_col = (int)max((int64_t)0, min((int64_t)kCols, a.cols - col));
+  // a warp that spans several rows has no run of its own to stage
+  uint8_t* stage = STAGED && a.lanes == 32 ? stages[STAGED ? warp : 0] : nullptr;
+  const int64_t left = a.cols - (int64_t)strip * kStrip, run = left < kStrip ? left : kStrip;
   // this warp's rows
   const int64_t warps = (int64_t)a.row_parts * kActWarps, w = (int64_t)part * kActWarps + warp;
   const int64_t r0 = a.rows * w / warps, r1 = a.rows * (w + 1) / warps;
@@ -127,17 +166,19 @@ __global__ void __launch_bounds__(kActThreads, 3) k_bias_act_backward(const ActK
 #pragma unroll
   for (int i = 0; i < 8; ++i) mx[i] = 0;
   // the next row's words are loaded before this row's are used
-  S nd, nz;
+  SectorLoad<BF16, STAGED> nd, nz;
   auto fetch = [&](int64_t r) {
     const int n = r < r1 ? n_col : 0;
-    nd.load(a.dd, r * a.cols + col, n, a.g_dd);
-    if constexpr (ACT != kActNone) nz.load(a.z, r * a.cols + col, n, a.g_z);
+    const int64_t have = r < r1 ? run : 0;
+    nd.issue(a.dd, r * a.cols + col, n, have, a.g_dd, stage, lane);
+    if constexpr (ACT != kActNone)
+      nz.issue(a.z, r * a.cols + col, n, have, a.g_z, stage, lane);
   };
   fetch(r0 + sub);
   for (int64_t rb = r0; rb < r1; rb += step) {
     const int64_t r = rb + sub;
-    S d = nd, z;
-    if constexpr (ACT != kActNone) z = nz;
+    S d = nd.settle(a.g_dd, stage, lane), z;
+    if constexpr (ACT != kActNone) z = nz.settle(a.g_z, stage, lane);
     if (rb + step < r1) fetch(r + step);
 #pragma unroll
     for (int i = 0; i < kCols / 2; ++i) {
@@ -146,7 +187,7 @@ __global__ void __launch_bounds__(kActThreads, 3) k_bias_act_backward(const ActK
       sum[i] = pair_add(sum[i], v);
       d.set(i, v);
     }
-    d.store(a.dz, r * a.cols + col, r < r1 ? n_col : 0, a.g_dz);
+    d.store_warp<STAGED>(a.dz, r * a.cols + col, r < r1 ? n_col : 0, r < r1 ? run : 0, a.g_dz, stage, lane);
 #pragma unroll
     for (int i = 0; i < 8; ++i) mx[i] = word_absmax<BF16>(mx[i], d.w[i]);
     if (a.row_max != nullptr) {
@@ -264,12 +305,12 @@ int64_t max_row_parts(int64_t cols, bool bf16) {
 }
 int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
 
-template <bool BF16, int ACT>
-cudaError_t run_act(ActKernelArgs& k, const DeviceInfo& dev, cudaStream_t stream) {
+template <bool BF16, int ACT, bool STAGED>
+cudaError_t run_act_as(ActKernelArgs& k, const DeviceInfo& dev, cudaStream_t stream) {
   static const int resident = [] {
     int n = 0;
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, k_bias_act_backward<BF16, ACT>,
-                                                      kActThreads, 0) != cudaSuccess) {
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+            &n, k_bias_act_backward<BF16, ACT, STAGED>, kActThreads, 0) != cudaSuccess) {
       cudaGetLastError();
       n = 2;
     }
@@ -280,9 +321,17 @@ cudaError_t run_act(ActKernelArgs& k, const DeviceInfo& dev, cudaStream_t stream
   const int64_t rows_per_cta = (int64_t)kActWarps * (32 / k.lanes);
   k.row_parts = (int)std::max<int64_t>(
       1, std::min(fill / k.strips, (k.rows + rows_per_cta - 1) / rows_per_cta));
-  k_bias_act_backward<BF16, ACT>
+  k_bias_act_backward<BF16, ACT, STAGED>
       <<<(unsigned)(k.strips * (int64_t)k.row_parts), kActThreads, 0, stream>>>(k);
   return cudaGetLastError();
+}
+
+template <bool BF16, int ACT>
+cudaError_t run_act(ActKernelArgs& k, const DeviceInfo& dev, cudaStream_t stream) {
+  int grain = std::min(k.g_dd, k.g_dz);
+  if (ACT != kActNone) grain = std::min(grain, k.g_z);
+  return grain >= 16 ? run_act_as<BF16, ACT, false>(k, dev, stream)
+                     : run_act_as<BF16, ACT, true>(k, dev, stream);
 }
 
 template <bool BF16>
@@ -330,9 +379,9 @@ cudaError_t launch_bias_act_backward(const ActBackwardArgs& a, const DeviceInfo&
   k.strips = (int)strips_of(a.cols, bf16);
   k.lanes = 32;
   while (k.lanes > 1 && (int64_t)(k.lanes / 2) * (bf16 ? 16 : 8) >= a.cols) k.lanes /= 2;
-  k.g_dd = row_grain(a.dd, a.cols, e);
-  k.g_z = row_grain(a.z, a.cols, e);
-  k.g_dz = row_grain(a.dz, a.cols, e);
+  k.g_dd = row_grain(a.dd, a.cols * e);
+  k.g_z = row_grain(a.z, a.cols * e);
+  k.g_dz = row_grain(a.dz, a.cols * e);
   cudaError_t err = a.in == InType::BF16 ? pick_act<true>(a.act, k, dev, stream)
                                          : pick_act<false>(a.act, k, dev, stream);
   if (err != cudaSuccess || !(a.dbias || a.col_amax || a.row_amax)) return err;

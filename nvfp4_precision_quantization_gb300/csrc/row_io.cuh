@@ -1,11 +1,14 @@
 // row_io.cuh -- 16 consecutive row elements per thread: loads and stores shared by the
 // layer operators' kernels (BF16 or FP32 rows, widened to FP32).
 //
-// A row may start at any element.  `grain` is the widest access that every full
-// 16-element chunk of the tensor allows (32 or 16 bytes, 0 for element accesses), the
-// same for the whole tensor, so the choice is one uniform branch: 32-byte accesses move
-// whole sectors (one request of a warp covers 1 KB), and an odd row length falls back
-// to elements.  A chunk cut by the row's end is always moved element by element.
+// A row may start at any element.  `grain` is the widest access that every row of the tensor
+// allows, the same for the whole tensor, so the choice is one uniform branch.  32- and
+// 16-byte accesses are made by each lane on its own chunk (a row's last chunk, cut by its
+// end, element by element).  Narrower ones would make every request of a warp touch 32
+// sectors, so there the warp moves its 32 chunks together: neighbouring lanes access
+// neighbouring units of 8, 4, 2 or 1 bytes, and 1 KB of shared memory per warp turns that
+// into whole chunks per lane and back (5001 columns instead of 5000 measured 7 times slower
+// without it).
 #pragma once
 
 #include <cuda_bf16.h>
@@ -33,10 +36,149 @@ inline cudaError_t launch_after(void (*kernel)(P...), unsigned grid, unsigned th
   return cudaLaunchKernelEx(&cfg, kernel, args...);
 }
 
-// The grain of rows of `cols` elements of `elem` bytes at p.
-inline int row_grain(const void* p, int64_t cols, int elem) {
-  const uintptr_t a = reinterpret_cast<uintptr_t>(p) | (uintptr_t)(cols * elem);
-  return a % 32 == 0 ? 32 : (a % 16 == 0 ? 16 : 0);
+// The grain of rows of `bytes` bytes at p: 32, 16, 8, 4, 2 or 1.
+inline int row_grain(const void* p, int64_t bytes) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p) | (uintptr_t)bytes;
+  int g = 32;
+  while (a % g != 0) g /= 2;
+  return g;
+}
+
+constexpr int kStageBytes = 1024;  // of shared memory per warp
+
+// Staged accesses of a warp: W words per lane (at most 8), lanes PITCH bytes apart from lane
+// 0's first byte, of which the first `bytes` bytes of the whole run exist.  Unit i of the
+// warp's 32 W / unit is byte i * unit % (4 W) of lane i * unit / (4 W).
+template <int W, int PITCH, int UNIT>
+struct StagedUnits {
+  static constexpr int kPer = 4 * W / UNIT;  // units per lane
+  static constexpr int kAll = 31 * PITCH + 4 * W;  // the bytes of a whole run
+  static_assert(W <= 8 && 4 * W * 32 <= kStageBytes, "one pass");
+  __device__ __forceinline__ static int at(int i, int lane) { return (32 * i + lane) * UNIT; }
+  __device__ __forceinline__ static int offset(int i, int lane) {
+    if constexpr (PITCH == 4 * W) return at(i, lane);
+    // a step of i is 32 units: a whole number of lanes
+    static_assert(32 * UNIT % (4 * W) == 0, "units of a step");
+    return (lane * UNIT) / (4 * W) * PITCH + (lane * UNIT) % (4 * W) +
+           i * (32 * UNIT / (4 * W)) * PITCH;
+  }
+};
+template <int UNIT>
+struct UnitType;
+template <>
+struct UnitType<8> {
+  using type = uint2;
+};
+template <>
+struct UnitType<4> {
+  using type = uint32_t;
+};
+template <>
+struct UnitType<2> {
+  using type = uint16_t;
+};
+template <>
+struct UnitType<1> {
+  using type = uint8_t;
+};
+
+// A staged load in two steps, so that several can be in flight: the warp's units into
+// registers, then through shared memory into each lane's W words.
+template <int W, int PITCH>
+struct StagedLoad {
+  uint32_t v[2 * W];  // units of 2 bytes take a register each, wider ones W words in all
+
+  template <int UNIT, bool WHOLE>
+  __device__ __forceinline__ void issue_units(const char* p, int bytes, int lane) {
+    using U = StagedUnits<W, PITCH, UNIT>;
+    using T = typename UnitType<UNIT>::type;
+#pragma unroll
+    for (int i = 0; i < U::kPer; ++i) {
+      const int off = U::offset(i, lane);
+      const T t = WHOLE || off < bytes ? *reinterpret_cast<const T*>(p + off) : T{};
+      if constexpr (UNIT == 8) {
+        v[2 * i] = t.x;
+        v[2 * i + 1] = t.y;
+      } else {
+        v[i] = t;
+      }
+    }
+  }
+  template <int UNIT>
+  __device__ __forceinline__ void issue_units(const char* p, int bytes, int lane) {
+    if (bytes >= StagedUnits<W, PITCH, UNIT>::kAll) issue_units<UNIT, true>(p, bytes, lane);
+    else issue_units<UNIT, false>(p, bytes, lane);
+  }
+  template <int UNIT>
+  __device__ __forceinline__ void settle_units(uint8_t* smem, int lane) const {
+    using U = StagedUnits<W, PITCH, UNIT>;
+    using T = typename UnitType<UNIT>::type;
+#pragma unroll
+    for (int i = 0; i < U::kPer; ++i) {
+      T* to = reinterpret_cast<T*>(smem + U::at(i, lane));
+      if constexpr (UNIT == 8) *to = make_uint2(v[2 * i], v[2 * i + 1]);
+      else *to = (T)v[i];
+    }
+  }
+  __device__ __forceinline__ void issue(const char* p, int bytes, int unit, int lane) {
+    if (unit == 8) issue_units<8>(p, bytes, lane);
+    else if (unit == 4) issue_units<4>(p, bytes, lane);
+    else issue_units<2>(p, bytes, lane);
+  }
+  __device__ __forceinline__ void settle(int unit, uint8_t* smem, int lane, uint32_t* w) const {
+    if (unit == 8) settle_units<8>(smem, lane);
+    else if (unit == 4) settle_units<4>(smem, lane);
+    else settle_units<2>(smem, lane);
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < W; k += 4) {
+      const uint4 u = *reinterpret_cast<const uint4*>(smem + 4 * W * lane + 4 * k);
+      w[k] = u.x, w[k + 1] = u.y, w[k + 2] = u.z, w[k + 3] = u.w;
+    }
+    __syncwarp();
+  }
+};
+
+template <int W, int PITCH, int UNIT, bool WHOLE>
+__device__ __forceinline__ void staged_store_units(char* p, int bytes, const uint8_t* smem,
+                                                   int lane) {
+  using U = StagedUnits<W, PITCH, UNIT>;
+  using T = typename UnitType<UNIT>::type;
+#pragma unroll
+  for (int i = 0; i < U::kPer; ++i) {
+    const int off = U::offset(i, lane);
+    if (WHOLE || off < bytes)
+      *reinterpret_cast<T*>(p + off) = *reinterpret_cast<const T*>(smem + U::at(i, lane));
+  }
+}
+template <int W, int PITCH, int UNIT>
+__device__ __forceinline__ void staged_store_units(char* p, int bytes, const uint8_t* smem,
+                                                   int lane) {
+  if (bytes >= StagedUnits<W, PITCH, UNIT>::kAll)
+    staged_store_units<W, PITCH, UNIT, true>(p, bytes, smem, lane);
+  else
+    staged_store_units<W, PITCH, UNIT, false>(p, bytes, smem, lane);
+}
+// Words of every lane to memory through shared memory (see StagedUnits).
+template <int W, int PITCH>
+__device__ __forceinline__ void staged_store(char* p, int bytes, int unit, uint8_t* smem,
+                                             int lane, const uint32_t* w) {
+  if constexpr (W % 4 == 0) {
+#pragma unroll
+    for (int k = 0; k < W; k += 4)
+      *reinterpret_cast<uint4*>(smem + 4 * W * lane + 4 * k) =
+          make_uint4(w[k], w[k + 1], w[k + 2], w[k + 3]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < W; ++k)
+      *reinterpret_cast<uint32_t*>(smem + 4 * W * lane + 4 * k) = w[k];
+  }
+  __syncwarp();
+  if (unit == 8) staged_store_units<W, PITCH, 8>(p, bytes, smem, lane);
+  else if (unit == 4) staged_store_units<W, PITCH, 4>(p, bytes, smem, lane);
+  else if (unit == 2) staged_store_units<W, PITCH, 2>(p, bytes, smem, lane);
+  else staged_store_units<W, PITCH, 1>(p, bytes, smem, lane);
+  __syncwarp();
 }
 
 __device__ __forceinline__ void ldg_v8(const void* p, uint32_t* w) {
@@ -86,6 +228,21 @@ struct Chunk {
           if (i < n) w[i] = q[i];
       }
     }
+  }
+  // The same for a warp whose lanes hold consecutive chunks (`run` elements exist from lane
+  // 0's on); smem: the warp's kStageBytes.  STAGED false: every grain is at least 16.
+  template <bool STAGED>
+  __device__ __forceinline__ void store_warp(void* base, int64_t off, int n, int64_t run,
+                                             int grain, uint8_t* smem, int lane) const {
+    if (!STAGED || grain >= 16) {
+      store(base, off, n, grain);
+      return;
+    }
+    constexpr int kElem = BF16 ? 2 : 4;
+    char* p = static_cast<char*>(base) + (off - (int64_t)kChunk * lane) * kElem;
+#pragma unroll
+    for (int h = 0; h < kWords; h += 8)
+      staged_store<8, 4 * kWords>(p + 4 * h, (int)run * kElem - 4 * h, grain, smem, lane, w + h);
   }
   // From a row held in shared memory, 16-byte aligned (so n is a whole number of 16-byte
   // units).  Lanes are 32 or 64 bytes apart; rotating the order of a lane's units spreads
@@ -159,6 +316,38 @@ struct Chunk {
   }
 };
 
+// A chunk's load by a warp whose lanes hold consecutive chunks, in two steps: issue() for
+// every tensor first, then settle() one after the other.  STAGED false: every grain is at
+// least 16, and settle has nothing to do.
+template <bool BF16, bool STAGED>
+struct ChunkLoad {
+  Chunk<BF16> c;
+  StagedLoad<8, 4 * Chunk<BF16>::kWords> raw[STAGED ? Chunk<BF16>::kWords / 8 : 1];
+
+  __device__ __forceinline__ void issue(const void* base, int64_t off, int n, int64_t run,
+                                        int grain, int lane) {
+    if (!STAGED || grain >= 16) {
+      c.load(base, off, n, grain);
+      return;
+    }
+    constexpr int kElem = BF16 ? 2 : 4;
+    const char* p = static_cast<const char*>(base) + (off - (int64_t)kChunk * lane) * kElem;
+#pragma unroll
+    for (int h = 0; h < Chunk<BF16>::kWords / 8; ++h)
+      raw[h].issue(p + 32 * h, (int)run * kElem - 32 * h, grain, lane);
+  }
+  __device__ __forceinline__ const Chunk<BF16>& settle(int grain, uint8_t* smem, int lane) {
+    if constexpr (STAGED) {
+      if (grain < 16) {
+#pragma unroll
+        for (int h = 0; h < Chunk<BF16>::kWords / 8; ++h)
+          raw[h].settle(grain, smem, lane, c.w + 8 * h);
+      }
+    }
+    return c;
+  }
+};
+
 // The 16 FP32 values of a chunk of a BF16 or FP32 vector (type known at run time).
 __device__ __forceinline__ void load_vector16(const void* base, bool bf16, int64_t off, int n,
                                               int grain, float* v) {
@@ -184,6 +373,12 @@ __device__ __forceinline__ void bulk_copy_in(void* dst, const void* src, uint32_
           "r"(smem_addr(dst)),
       "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_addr(bar))
       : "memory");
+}
+
+// Elements from column c on of a row of `cols`, for a warp (at most its 32 chunks).
+__device__ __forceinline__ int64_t warp_run(int64_t c, int64_t cols) {
+  const int64_t left = cols - c;
+  return left < 0 ? 0 : (left < 32 * kChunk ? left : 32 * kChunk);
 }
 
 // Elements of the chunk that starts at column c of a row of `cols` (0 past its end).

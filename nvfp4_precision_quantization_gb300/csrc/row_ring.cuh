@@ -1,0 +1,167 @@
+// row_ring.cuh -- what the norm's forward and backward kernels share: the reduction over a
+// row's team of threads, and the shared-memory ring that rows run through.
+#pragma once
+
+#include <algorithm>
+
+#include "internal.h"
+#include "row_io.cuh"
+
+namespace nvfp4 {
+namespace {
+
+// Sum and maximum over the TPR threads of a row's team; every thread gets both.  The
+// order of the sum depends on TPR alone.  red: one pair per warp, in two buffers used in
+// turn, so that one barrier per row is enough.  BARRIER: with the CTA's barrier also where
+// a team is one warp.
+template <int TPR, bool BARRIER = false>
+__device__ __forceinline__ float2 team_sum_max(float s, float m, float2* red) {
+#pragma unroll
+  for (int d = 16; d > 0; d >>= 1) {
+    s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, d));
+    m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+  }
+  if constexpr (TPR > 32) {
+    constexpr int kWarps = TPR / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (lane == 0) red[warp] = make_float2(s, m);
+    __syncthreads();
+    const float2 v = red[warp - warp % kWarps + lane % kWarps];
+    s = v.x;
+    m = v.y;
+#pragma unroll
+    for (int d = kWarps / 2; d > 0; d >>= 1) {
+      s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, d));
+      m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+    }
+  } else if constexpr (BARRIER) {
+    __syncthreads();
+  }
+  return make_float2(s, m);
+}
+
+// ---------------------------------------------------------------- a ring of rows
+
+// Many aligned rows: they run through a ring in shared memory, filled by bulk copies that
+// thread 0 issues several rows ahead, so that the row's barrier and its arithmetic never
+// leave the memory idle, whatever the registers allow to be resident.  A stage holds one
+// group of kTeams consecutive rows of each tensor (consecutive in memory: one copy each).
+// The row's reduction barrier is also what frees its stage: by then every thread has the
+// stage's values in registers.
+constexpr int kRingStages = 8;
+
+struct RingArgs {
+  int stages;
+  int tensor_bytes;  // stride of a stage's tensors
+  int stage_bytes;
+};
+
+template <int NT>
+struct RowRing {
+  uint64_t* full;
+  int* err;
+  uint8_t* smem;
+  const void* src[NT];
+  int64_t rows, row_bytes;
+  int teams;
+  RingArgs g;
+
+  __device__ __forceinline__ uint8_t* stage(int s) const { return smem + s * g.stage_bytes; }
+  // thread 0: start the copies of the group of rows that begins at row0
+  __device__ __forceinline__ void fetch(int s, int64_t row0) const {
+    const int64_t left = rows - row0;
+    const uint32_t bytes = (uint32_t)((left < teams ? left : teams) * row_bytes);
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < NT; ++i) n += src[i] != nullptr;
+    mbar_expect_tx(&full[s], bytes * n);
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+      if (src[i] != nullptr)
+        bulk_copy_in(stage(s) + i * g.tensor_bytes,
+                     static_cast<const char*>(src[i]) + row0 * row_bytes, bytes, &full[s]);
+  }
+  __device__ __forceinline__ void start(int64_t step) const {
+    if (threadIdx.x == 0) {
+      for (int s = 0; s < g.stages; ++s) mbar_init(&full[s], 1);
+      *err = 0;
+      fence_mbar_init();
+      for (int s = 0; s < g.stages; ++s) {
+        const int64_t row0 = (int64_t)blockIdx.x * teams + s * step;
+        if (row0 < rows) fetch(s, row0);
+      }
+    }
+    __syncthreads();
+  }
+  // Wait for use `it` of the ring; false (with the error noted) if it gave up.
+  __device__ __forceinline__ bool wait(int s, int it) const {
+    const bool ok = mbar_wait_bounded(&full[s], (it / g.stages) & 1);
+    if (!ok) *err = 1;
+    return ok;
+  }
+  // After a timeout: thread 0 waits (bounded) for the copies still in flight.
+  __device__ __forceinline__ void give_up(int it, int64_t row0, int64_t step, int* status) const {
+    if (threadIdx.x != 0) return;
+    raise_status(status, kStatusTimeout);
+    for (int k = 0; k < g.stages; ++k)
+      if (row0 + k * step < rows)
+        mbar_wait_bounded(&full[(it + k) % g.stages], ((it + k) / g.stages) & 1);
+  }
+};
+
+template <typename K>
+int resident_ctas(K kernel, int threads) {
+  int n = 0;
+  if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, threads, 0) != cudaSuccess) {
+    cudaGetLastError();
+    n = 1;
+  }
+  return std::max(1, n);
+}
+
+// A ring kernel's CTAs per SM by registers, and its static shared memory.
+constexpr int kCtaSmem = 227 << 10;  // shared memory that one CTA may have
+struct RingKernel {
+  int resident;
+  int static_bytes;
+};
+template <typename K>
+RingKernel ring_kernel(K kernel, int threads) {
+  cudaFuncAttributes f;
+  if (cudaFuncGetAttributes(&f, kernel) != cudaSuccess) {
+    cudaGetLastError();
+    return {0, 0};
+  }
+  return {resident_ctas(kernel, threads), (int)f.sharedSizeBytes};
+}
+template <typename K>
+cudaError_t allow_ring(K kernel, const RingKernel& k) {  // on the current device
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              kCtaSmem - k.static_bytes);
+}
+
+// CTAs per SM and the ring of each: as many CTAs as the registers allow while each keeps
+// at least two stages.  ctas == 0: two stages do not fit.
+struct RingPlan {
+  int ctas;
+  RingArgs g;
+};
+RingPlan plan_ring(const RingKernel& k, int tensors, int64_t group_bytes) {
+  RingPlan p{};
+  const int64_t tensor = (group_bytes + 127) / 128 * 128, stage = tensors * tensor;
+  for (int c = k.resident; c > 0; --c) {
+    // an SM's 228 KB, of which every CTA takes 1 KB beside its own
+    const int64_t room =
+        std::min<int64_t>(kCtaSmem, (228 << 10) / c - (1 << 10)) - k.static_bytes;
+    if (room < 2 * stage) continue;
+    p.ctas = c;
+    p.g.stages = (int)std::min<int64_t>(kRingStages, room / stage);
+    p.g.tensor_bytes = (int)tensor;
+    p.g.stage_bytes = (int)stage;
+    break;
+  }
+  return p;
+}
+
+}  // namespace
+}  // namespace nvfp4

@@ -171,7 +171,8 @@ def test_workspace_and_stream(m):
 # ---------------------------------------------------------------- backward
 
 BACK = [(1, 1), (1, 4096), (3, 16), (5, 17), (40, 64), (1000, 8), (129, 100), (300, 512),
-        (77, 513), (64, 5000), (2000, 1024), (5, 28672), (700, 2056), (0, 8), (8, 0)]
+        (77, 513), (64, 5000), (2000, 1024), (5, 28672), (700, 2056), (0, 8), (8, 0),
+        (3000, 1001), (999, 515), (1200, 2050)]
 
 
 def _backward_inputs(rows, cols, dtype, seed, spread=3.0):

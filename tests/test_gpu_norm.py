@@ -45,7 +45,8 @@ def _close(got, want, rel, what):
 # enough rows for every CTA to walk several, at each width of a row's team, with groups of
 # rows cut by the last row
 MANY = [(9001, 24), (7003, 512), (5003, 1000), (3001, 2048), (2777, 4096), (1501, 8192),
-        (1501, 5008), (701, 16384), (701, 12000), (400, 20000)]
+        (1501, 5008), (701, 16384), (701, 12000), (400, 20000), (9001, 25), (3001, 1001),
+        (2501, 1002), (1501, 4097), (1001, 5004), (601, 9001), (401, 17001)]
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
@@ -96,7 +97,7 @@ def test_fp8_output(rows, cols, dtype, block):
 
 @pytest.mark.parametrize("fos", [0, 1])
 @pytest.mark.parametrize("bound", [448.0, 256.0])
-@pytest.mark.parametrize("rows,cols", SHAPES + MANY[1:5])
+@pytest.mark.parametrize("rows,cols", SHAPES + MANY[1:5] + MANY[10:16])
 def test_nvfp4_output_is_the_quantize_of_y(rows, cols, bound, fos):
     if rows == 0:
         pytest.skip("no codes to compare")
