@@ -112,4 +112,40 @@ __device__ __forceinline__ Pair act_slope(Pair z) {
   return pair_add({with_sign(m.x, z.x), with_sign(m.y, z.y)}, {0.5f, 0.5f});
 }
 
+// act(z) of a pair: z p with p = 1 / (1 + 2^-w), w = u log2(e).
+template <int ACT>
+__device__ __forceinline__ Pair act_value(Pair z) {
+  if constexpr (ACT == kActGelu || ACT == kActSilu) {
+    constexpr float kLog2e = 1.4426950408889634f;
+    Pair w;
+    if constexpr (ACT == kActGelu) {
+      constexpr float c0 = kGelu2C * kLog2e, c1 = kGelu2C * kGeluA * kLog2e;
+      w = pair_mul(z, pair_fma({c1, c1}, pair_mul(z, z), {c0, c0}));
+    } else {
+      w = pair_mul(z, {kLog2e, kLog2e});
+    }
+    const Pair t = pair_add({ex2_approx(-w.x), ex2_approx(-w.y)}, {1.0f, 1.0f});
+    return pair_mul(z, {rcp_approx(t.x), rcp_approx(t.y)});
+  } else {
+    return {act_value<ACT>(z.x), act_value<ACT>(z.y)};
+  }
+}
+
+// v[0 .. N) = act(v), the activation known at run time.
+template <int ACT, int N>
+__device__ __forceinline__ void apply_act_as(float* v) {
+#pragma unroll
+  for (int j = 0; j < N; j += 2) {
+    const Pair r = act_value<ACT>(Pair{v[j], v[j + 1]});
+    v[j] = r.x;
+    v[j + 1] = r.y;
+  }
+}
+template <int N>
+__device__ __forceinline__ void apply_act(int act, float* v) {
+  if (act == kActRelu) apply_act_as<kActRelu, N>(v);
+  else if (act == kActGelu) apply_act_as<kActGelu, N>(v);
+  else if (act == kActSilu) apply_act_as<kActSilu, N>(v);
+}
+
 }  // namespace nvfp4

@@ -248,89 +248,110 @@ __device__ __forceinline__ void tile_coords(int idx, int tiles_m, int tiles_n, i
   tn = rem / gm;
 }
 
-// 32 consecutive output columns of one row, FP32 -> D's type.  whole32 / whole16: all
-// of them inside the row, the run 32- / 16-byte aligned; else element stores of the
-// first n.
+// 32 consecutive output columns of one row, FP32 -> D's type, in 32-byte (v8) or 16-byte
+// stores.
 __device__ __forceinline__ void store_run32(void* base, bool bf16, int64_t off, const float* v,
-                                            bool whole32, bool whole16, int n) {
-  if (bf16) {
-    uint16_t* dst = static_cast<uint16_t*>(base) + off;
-    uint32_t w[16];
+                                            bool v8) {
+  const int step = bf16 ? 16 : 8;  // values of a 32-byte sector
 #pragma unroll
-    for (int j = 0; j < 16; ++j) w[j] = bf16x2_bits(v[2 * j], v[2 * j + 1]);
-    if (whole32) {
+  for (int g = 0; g < 4; ++g) {
+    uint32_t w[8];
+    if (bf16) {
+      if (g >= 2) break;
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+        w[j] = bf16x2_bits(v[(16 * g + 2 * j) & 31], v[(16 * g + 2 * j + 1) & 31]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[j] = __float_as_uint(v[8 * g + j]);
+    }
+    char* dst = static_cast<char*>(base) + (off + g * step) * (bf16 ? 2 : 4);
+    if (v8) {
       stg_v8(dst, w);
-      stg_v8(dst + 16, w + 8);
-    } else if (whole16) {
-#pragma unroll
-      for (int g = 0; g < 4; ++g)
-        *reinterpret_cast<uint4*>(dst + 8 * g) =
-            make_uint4(w[4 * g], w[4 * g + 1], w[4 * g + 2], w[4 * g + 3]);
     } else {
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (j < n) dst[j] = (uint16_t)(w[j >> 1] >> (16 * (j & 1)));
-    }
-  } else {
-    uint32_t* dst = static_cast<uint32_t*>(base) + off;
-    uint32_t w[32];
-#pragma unroll
-    for (int j = 0; j < 32; ++j) w[j] = __float_as_uint(v[j]);
-    if (whole32) {
-#pragma unroll
-      for (int g = 0; g < 4; ++g) stg_v8(dst + 8 * g, w + 8 * g);
-    } else if (whole16) {
-#pragma unroll
-      for (int g = 0; g < 8; ++g)
-        *reinterpret_cast<uint4*>(dst + 4 * g) =
-            make_uint4(w[4 * g], w[4 * g + 1], w[4 * g + 2], w[4 * g + 3]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < 32; ++j)
-        if (j < n) dst[j] = w[j];
+      *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
+      *reinterpret_cast<uint4*>(dst + 16) = make_uint4(w[4], w[5], w[6], w[7]);
     }
   }
 }
 
-// The epilogue of 32 columns of one row: v (the product) plus bias becomes z, kept if
-// asked for, then act(z) + residual, stored.  bias: 32 FP32 values in shared memory.
-__device__ __forceinline__ void epilogue_run32(const Epilogue& e, void* d, bool bf16, int64_t off,
-                                               float* v, const float* bias, bool vec32,
-                                               bool vec16, int n) {
+// v[i] of lane l <- v[l] of lane i: a 32 x 32 transposition between the lanes of a warp.
+__device__ __forceinline__ void transpose32(float* v, int lane) {
 #pragma unroll
-  for (int j4 = 0; j4 < 8; ++j4) {
-    const float4 b = *reinterpret_cast<const float4*>(bias + 4 * j4);
-    v[4 * j4] = __fadd_rn(v[4 * j4], b.x);
-    v[4 * j4 + 1] = __fadd_rn(v[4 * j4 + 1], b.y);
-    v[4 * j4 + 2] = __fadd_rn(v[4 * j4 + 2], b.z);
-    v[4 * j4 + 3] = __fadd_rn(v[4 * j4 + 3], b.w);
+  for (int d = 16; d > 0; d >>= 1) {
+    const bool upper = lane & d;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      if (i & d) continue;
+      const float got = __shfl_xor_sync(0xffffffffu, upper ? v[i] : v[i | d], d);
+      if (upper) v[i] = got;
+      else v[i | d] = got;
+    }
   }
-  if (e.z != nullptr) store_run32(e.z, bf16, off, v, vec32, vec16, n);
-  if (e.act == kActRelu) {
+}
+
+// The epilogue of a warp's 32 rows (one per lane) x 32 columns: v, the product plus bias, is
+// z, kept if asked for; then act(z) + residual, stored.  Whole, aligned runs (v16) are moved
+// by each lane in its own row.  Otherwise every lane's
+// accesses would start and end anywhere (an odd N measured four times slower), so the block
+// is transposed and a request covers 32 neighbouring columns of a row.
+struct EpilogueBlock {
+  int row0, col0;  // of the block
+  int rows, cols;  // of it, inside D
+};
+__device__ __forceinline__ void epilogue_block32(const GemmParams& p, const EpilogueBlock& b,
+                                                 float* v, bool v16, bool v8, int lane) {
+  const Epilogue& e = p.epi;
+  if (v16) {
+    const int64_t off = (int64_t)(b.row0 + lane) * p.N + b.col0;
+    const bool live = lane < b.rows;
+    if (e.z != nullptr && live) store_run32(e.z, p.d_bf16, off, v, v8);
+    apply_act<32>(e.act, v);
+    if (e.residual != nullptr) {
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = act_value<kActRelu>(v[j]);
-  } else if (e.act == kActGelu) {
+      for (int c = 0; c < 32; c += kChunk) {
+        float r[kChunk];
+        load_vector16(e.residual, p.d_bf16, off + c, live ? kChunk : 0, v8 ? 32 : 16, r);
 #pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = act_value<kActGelu>(v[j]);
-  } else if (e.act == kActSilu) {
-#pragma unroll
-    for (int j = 0; j < 32; ++j) v[j] = act_value<kActSilu>(v[j]);
+        for (int j = 0; j < kChunk; ++j) v[c + j] = __fadd_rn(v[c + j], r[j]);
+      }
+    }
+    if (live) store_run32(p.d, p.d_bf16, off, v, v8);
+    return;
   }
+  transpose32(v, lane);  // v[i]: row row0 + i, column col0 + lane
+  const bool live = lane < b.cols;
+  const int64_t off = (int64_t)b.row0 * p.N + b.col0 + lane;
+  auto store = [&](void* base) {
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+      if (!live || i >= b.rows) continue;
+      if (p.d_bf16)
+        static_cast<__nv_bfloat16*>(base)[off + (int64_t)i * p.N] = __float2bfloat16_rn(v[i]);
+      else
+        static_cast<float*>(base)[off + (int64_t)i * p.N] = v[i];
+    }
+  };
+  if (e.z != nullptr) store(e.z);
+  apply_act<32>(e.act, v);
   if (e.residual != nullptr) {
-    const int grain = vec32 ? 32 : (vec16 ? 16 : 0);
 #pragma unroll
-    for (int c = 0; c < 2; ++c) {
-      const int left = n - kChunk * c;
-      float r[kChunk];
-      load_vector16(e.residual, bf16, off + kChunk * c,
-                    left < 0 ? 0 : (left < kChunk ? left : kChunk), grain, r);
+    for (int g = 0; g < 32; g += 8) {
+      float r[8];
 #pragma unroll
-      for (int j = 0; j < kChunk; ++j) v[kChunk * c + j] = __fadd_rn(v[kChunk * c + j], r[j]);
+      for (int i = 0; i < 8; ++i) {
+        r[i] = 0.0f;
+        if (!live || g + i >= b.rows) continue;
+        const int64_t at = off + (int64_t)(g + i) * p.N;
+        r[i] = p.d_bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(e.residual)[at])
+                        : static_cast<const float*>(e.residual)[at];
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[g + i] = __fadd_rn(v[g + i], r[i]);
     }
   }
-  store_run32(d, bf16, off, v, vec32, vec16, n);
+  store(p.d);
 }
-
 // Persistent: CTA c computes tiles c, c + gridDim.x, ...  The load ring runs on
 // across tile boundaries; the epilogue copies the accumulator to registers,
 // hands TMEM back (acc_empty) and stores while the MMAs of the next tile run.
@@ -533,6 +554,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         __syncwarp();
       }
+      if constexpr (EPI) {
+        // the warp's part of the residual into L2 while the MMAs run: 128-byte lines, each
+        // lane those of its row
+        if (live && p.epi.residual != nullptr) {
+          const int esize = p.d_bf16 ? 2 : 4;
+          const char* from = static_cast<const char*>(p.epi.residual) +
+                             ((int64_t)row * p.N + col_base) * esize;
+          const int bytes = min(kEpiCols, p.N - col_base) * esize;
+          for (int b = 0; b < bytes; b += 128)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(from + b));
+        }
+      }
       const bool ready = mbar_wait_bounded(acc_full, t & 1);
       if (!ready) *err = 1;
       tc_fence_after();
@@ -549,6 +582,37 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < kEpiCols; ++i) v[i] = 0u;
       }
+      if constexpr (EPI) {
+        // the warp's rows and columns inside D; every lane takes part
+        const int rows = min(32, p.M - (tm * kBM + q * 32));
+        const int cols = min(kEpiCols, p.N - col_base);
+        if (rows <= 0 || cols <= 0) continue;
+        const int esize = p.d_bf16 ? 2 : 4;
+        uintptr_t align = reinterpret_cast<uintptr_t>(p.d) | (uintptr_t)p.N * esize;
+        if (p.epi.residual) align |= reinterpret_cast<uintptr_t>(p.epi.residual);
+        if (p.epi.z) align |= reinterpret_cast<uintptr_t>(p.epi.z);
+        const bool v16 = cols == kEpiCols && (align & 15) == 0, v8 = (align & 31) == 0;
+#pragma unroll
+        for (int c = 0; c < kEpiCols / 32; ++c) {
+          if (c * 32 >= cols) break;
+          float f[32];
+          // d = fl(fl(acc * alpha) * beta) + bias
+#pragma unroll
+          for (int j4 = 0; j4 < 8; ++j4) {
+            const float4 b4 = *reinterpret_cast<const float4*>(beta + c * 32 + 4 * j4);
+            const float4 a4 = *reinterpret_cast<const float4*>(bias + c * 32 + 4 * j4);
+            const float bj[4] = {b4.x, b4.y, b4.z, b4.w}, aj[4] = {a4.x, a4.y, a4.z, a4.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              f[4 * j4 + j] = __fadd_rn(
+                  __fmul_rn(__fmul_rn(__uint_as_float(v[c * 32 + 4 * j4 + j]), alpha), bj[j]),
+                  aj[j]);
+          }
+          epilogue_block32(p, {tm * kBM + q * 32, col_base + c * 32, rows, min(32, cols - c * 32)},
+                           f, v16, v8, lane);
+        }
+        continue;
+      }
       if (!live) continue;
       const int nvalid = min(kEpiCols, p.N - col_base);
       const int64_t off = (p.k_grouped ? (int64_t)job.g * p.M * p.N : 0) +
@@ -556,14 +620,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       // whole 32-byte sectors per store where the row's run is 32-byte aligned,
       // else 16-byte stores, else (ragged N or odd alignment) element stores
       const uintptr_t d_addr = reinterpret_cast<uintptr_t>(p.d) + off * (p.d_bf16 ? 2 : 4);
-      uintptr_t run_addr = d_addr;
-      if constexpr (EPI) {  // the residual and z take D's accesses
-        const int64_t at = off * (p.d_bf16 ? 2 : 4);
-        if (p.epi.residual) run_addr |= reinterpret_cast<uintptr_t>(p.epi.residual) + at;
-        if (p.epi.z) run_addr |= reinterpret_cast<uintptr_t>(p.epi.z) + at;
-      }
-      const bool vec = nvalid == kEpiCols && (run_addr & 15) == 0;
-      const bool vec32 = vec && (run_addr & 31) == 0;
+      const bool vec = nvalid == kEpiCols && (d_addr & 15) == 0;
+      const bool vec32 = vec && (d_addr & 31) == 0;
 #pragma unroll
       for (int c = 0; c < kEpiCols / 32; ++c) {
         uint32_t* vc = v + c * 32;
@@ -576,14 +634,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int j = 0; j < 4; ++j)
             vc[4 * j4 + j] =
                 __float_as_uint(__fmul_rn(__fmul_rn(__uint_as_float(vc[4 * j4 + j]), alpha), bj[j]));
-        }
-        if constexpr (EPI) {
-          float f[32];
-#pragma unroll
-          for (int j = 0; j < 32; ++j) f[j] = __uint_as_float(vc[j]);
-          epilogue_run32(p.epi, p.d, p.d_bf16, off + c * 32, f, bias + c * 32, vec32, vec,
-                         nvalid - c * 32);
-          continue;
         }
         if (p.d_bf16) {
           uint16_t* dst = static_cast<uint16_t*>(p.d) + off + c * 32;

@@ -46,7 +46,7 @@ constexpr int kMaxCtas = 160;   // bound of the grid, for the workspace
 struct FewParams {
   const uint8_t* x_scales;
   const uint8_t* w_scales;
-  int x_grain, w_grain;  // accesses of the scale rows: 16 or 4 bytes (see copy_lines), or 1
+  int x_grain, w_grain;  // how the scale rows are copied: 16, 2 or 1 (see copy_lines)
   const float* x_amax;
   const float* w_amax;
   int x_amax_stride, w_amax_stride;
@@ -74,13 +74,9 @@ struct ScaleRows {
   static constexpr int kPitch = kRowBytes + 16;
 };
 
-__device__ __forceinline__ void cp_async16(void* dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src)
-               : "memory");
-}
-// 4 bytes, of which the last 4 - bytes become zero and are not read.
-__device__ __forceinline__ void cp_async4(void* dst, const void* src, int bytes) {
-  asm volatile("cp.async.ca.shared.global.L2::128B [%0], [%1], 4, %2;" ::"r"(smem_addr(dst)),
+// 16 bytes, of which those from `bytes` on become zero and are not read.
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, int bytes = 16) {
+  asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)),
                "l"(src), "r"(bytes)
                : "memory");
 }
@@ -90,9 +86,9 @@ __device__ __forceinline__ void cp_async_wait_all() {
 
 // Start copying bytes [b0, b0 + kRowBytes) of the scale rows [first, first + lines) of
 // sc [total][k16] (rows from total on are left alone) to rows of dst; t of 128 threads.
-//   grain 16: rows and base are 16-byte aligned; 4: the base is 4-byte aligned, and the
-//   words that cover a row's part are copied (k16 is even, so a part may start 2 bytes into
-//   its first word; no byte past the tensor is read); 1: bytes, not asynchronously.
+//   grain 16: rows and base are 16-byte aligned; 2: the base is, and the 16-byte units that
+//   cover a row's part are copied, so that it starts 0 to 14 bytes (k16 is even) into its row
+//   of dst; no byte outside the tensor is read; 1: bytes, not asynchronously.
 template <int kGroup>
 __device__ __forceinline__ void copy_lines(const uint8_t* sc, int64_t k16, int64_t total,
                                            int64_t first, int lines, int64_t b0, int grain,
@@ -110,25 +106,15 @@ __device__ __forceinline__ void copy_lines(const uint8_t* sc, int64_t k16, int64
 #pragma unroll 4
     for (int r = t / kParts; r < rows; r += kStep, from += kStep * k16, dst += kStep * kPitch)
       cp_async16(dst, from);
-  } else if (grain == 4) {
-    // a warp takes a row at a time, 32 words of it at a time, and its last word in a pass of
-    // its own
-    const int lane = t & 31;
+  } else if (grain == 2) {
     const int64_t end = total * k16;
-    int64_t at = (first + (t >> 5)) * k16 + b0;
-    uint8_t* row = dst + (t >> 5) * kPitch;
-    for (int r = t >> 5; r < rows; r += 4, at += 4 * k16, row += 4 * kPitch) {
-      const int64_t word = (at & ~(int64_t)3) + 4 * lane;
-#pragma unroll
-      for (int w = 0; w < kRow / 4; w += 32)
-        if (w + lane < kRow / 4 && word + 4 * w < at + bytes)
-          cp_async4(row + 4 * (w + lane), sc + word + 4 * w,
-                    (int)min((int64_t)4, end - word - 4 * w));
-    }
     for (int r = t; r < rows; r += 128) {
-      const int64_t from = (first + r) * k16 + b0, word = (from & ~(int64_t)3) + kRow;
-      if (word < from + bytes)
-        cp_async4(dst + r * kPitch + kRow, sc + word, (int)min((int64_t)4, end - word));
+      const int64_t from = (first + r) * k16 + b0, to = from + bytes;
+      int64_t at = from & ~(int64_t)15;
+      uint8_t* row = dst + r * kPitch;
+#pragma unroll
+      for (int c = 0; c <= kRow / 16; ++c, at += 16, row += 16)
+        if (at < to) cp_async16(row, sc + at, (int)min((int64_t)16, end - at));
     }
   } else {
     for (int i = t; i < rows * kRow; i += 128) {
@@ -139,20 +125,24 @@ __device__ __forceinline__ void copy_lines(const uint8_t* sc, int64_t k16, int64
 }
 
 // The scales of unit e of the group, of the line at src, as words (one per MMA); those from n
-// on zero (they belong to the next line).  odd: the row starts 2 bytes into its first word.
-__device__ __forceinline__ void read_scales(const uint8_t* src, int e, bool odd, int n,
+// on zero (they belong to the next line).  shift: where in its first 16 bytes the row starts.
+__device__ __forceinline__ void read_scales(const uint8_t* src, int e, int shift, int n,
                                             uint32_t* w) {
   const uint8_t* p = src + kUnitScales * e;
+  if (shift == 0) {
 #pragma unroll
-  for (int j = 0; j < kMmas; j += 4) {
-    const uint4 v = *reinterpret_cast<const uint4*>(p + 4 * j);
-    w[j] = v.x, w[j + 1] = v.y, w[j + 2] = v.z, w[j + 3] = v.w;
-  }
-  if (odd) {
-    const uint32_t after = *reinterpret_cast<const uint32_t*>(p + 4 * kMmas);
+    for (int j = 0; j < kMmas; j += 4) {
+      const uint4 v = *reinterpret_cast<const uint4*>(p + 4 * j);
+      w[j] = v.x, w[j + 1] = v.y, w[j + 2] = v.z, w[j + 3] = v.w;
+    }
+  } else {
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(p + (shift & ~3));
+    uint32_t v[kMmas + 1];
 #pragma unroll
-    for (int j = 0; j < kMmas; ++j)
-      w[j] = __funnelshift_r(w[j], j + 1 < kMmas ? w[j + 1] : after, 16);
+    for (int j = 0; j < kMmas; ++j) v[j] = q[j];
+    v[kMmas] = (shift & 2) ? q[kMmas] : 0u;
+#pragma unroll
+    for (int j = 0; j < kMmas; ++j) w[j] = __funnelshift_r(v[j], v[j + 1], 8 * (shift & 2));
   }
   if (n < kUnitScales) {
 #pragma unroll
@@ -251,16 +241,7 @@ __device__ __forceinline__ void few_store(const FewParams& p, int row, int col, 
     }
   };
   if (p.epi.z != nullptr) store(p.epi.z);
-  if (p.epi.act == kActRelu) {
-#pragma unroll
-    for (int j = 0; j < R; ++j) v[j] = act_value<kActRelu>(v[j]);
-  } else if (p.epi.act == kActGelu) {
-#pragma unroll
-    for (int j = 0; j < R; ++j) v[j] = act_value<kActGelu>(v[j]);
-  } else if (p.epi.act == kActSilu) {
-#pragma unroll
-    for (int j = 0; j < R; ++j) v[j] = act_value<kActSilu>(v[j]);
-  }
+  apply_act<R>(p.epi.act, v);
   if (p.epi.residual != nullptr) {
 #pragma unroll
     for (int j = 0; j < R; ++j)
@@ -439,16 +420,17 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       const int64_t row = (int64_t)(tile % p.m_tiles) * NT + lane;
       const uint8_t* w_row = scale_smem + slot * G::kScaleBytes + (32 * q + lane) * kPitch;
       const uint8_t* x_row = scale_smem + slot * G::kScaleBytes + (kLines + lane) * kPitch;
-      const bool w_odd = p.w_grain == 4 && ((line * p.k16) & 2);
-      const bool x_odd = p.x_grain == 4 && ((row * p.k16) & 2);
+      // a row's part starts where the row does, 16 bytes times a whole number further on
+      const int w_shift = p.w_grain == 2 ? (int)((line * p.k16) & 15) : 0;
       for (; kt < end; ++kt, ++it) {
         const int e = kt % kGroup;
         const int n = (int)min((int64_t)kUnitScales, p.k16 - (int64_t)kt * kUnitScales);
         uint32_t wa[kMmas], wb[kXGroups][kMmas];
-        read_scales(w_row, e, w_odd, n, wa);
+        read_scales(w_row, e, w_shift, n, wa);
 #pragma unroll
         for (int c = 0; c < kXGroups; ++c)
-          read_scales(x_row + (NT >= 32 ? 32 * c : 0) * kPitch, e, x_odd, n, wb[c]);
+          read_scales(x_row + (NT >= 32 ? 32 * c : 0) * kPitch, e,
+                      p.x_grain == 2 ? (int)(((row + 32 * c) * p.k16) & 15) : 0, n, wb[c]);
         const uint32_t st = it % S;
         if (ok && it >= (uint32_t)S) ok = mbar_wait_bounded(&empty[st], ((it / S) - 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
@@ -593,7 +575,7 @@ __global__ void k_clear_arrivals(uint32_t* p, int n) {
 
 int scale_grain(const uint8_t* p, int64_t k16) {
   const uintptr_t a = reinterpret_cast<uintptr_t>(p);
-  return (a | (uintptr_t)k16) % 16 == 0 ? 16 : (a % 4 == 0 ? 4 : 1);
+  return (a | (uintptr_t)k16) % 16 == 0 ? 16 : (a % 16 == 0 ? 2 : 1);
 }
 
 int rows_of_mma(int64_t m) { return m <= 16 ? 16 : (m <= 32 ? 32 : 64); }
