@@ -19,7 +19,8 @@ namespace {
 
 constexpr int kClipThreads = 512;
 constexpr int kPiece = kClipThreads * kChunk * 2;  // values of a piece: two chunks a thread
-constexpr int kListCapacity = 512;                 // tensors of one launch
+// Tensors of one launch: the arguments of a short list are copied faster.
+constexpr int kShortList = 64, kListCapacity = 512;
 constexpr int kClipMaxCtas = 1024;                 // partial sums per launch
 
 struct ListEntry {
@@ -28,16 +29,18 @@ struct ListEntry {
   int64_t n;
   int64_t first;  // the tensor's first piece
 };
+template <int CAP>
 struct ListArgs {
   int count;
   int64_t pieces;
-  uint32_t bf16[kListCapacity / 32];
-  ListEntry e[kListCapacity];
+  uint32_t bf16[CAP / 32];
+  ListEntry e[CAP];
 };
 
 // The entry that holds piece p: the last one whose first piece is at most p (empty
 // tensors have no piece and share their first with the next entry).
-__device__ __forceinline__ int find_entry(const ListArgs& a, int64_t p) {
+template <int CAP>
+__device__ __forceinline__ int find_entry(const ListArgs<CAP>& a, int64_t p) {
   int lo = 0, hi = a.count - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -46,7 +49,8 @@ __device__ __forceinline__ int find_entry(const ListArgs& a, int64_t p) {
   }
   return lo;
 }
-__device__ __forceinline__ bool entry_bf16(const ListArgs& a, int i) {
+template <int CAP>
+__device__ __forceinline__ bool entry_bf16(const ListArgs<CAP>& a, int i) {
   return (a.bf16[i >> 5] >> (i & 31)) & 1u;
 }
 __device__ __forceinline__ int pointer_grain(const void* p) {
@@ -103,8 +107,9 @@ __device__ __forceinline__ double block_sum(double v, double* s) {
   return v;
 }
 
+template <int CAP>
 __global__ void __launch_bounds__(kClipThreads)
-    k_square_sum(const __grid_constant__ ListArgs a, double* part) {
+    k_square_sum(const __grid_constant__ ListArgs<CAP> a, double* part) {
   __shared__ double s[kClipThreads / 32];
   double sum = 0.0;
   for (int64_t p = blockIdx.x; p < a.pieces; p += gridDim.x) {
@@ -113,6 +118,7 @@ __global__ void __launch_bounds__(kClipThreads)
     sum += (double)(entry_bf16(a, i) ? piece_squares<true>(a.e[i].data, at, a.e[i].n)
                                      : piece_squares<false>(a.e[i].data, at, a.e[i].n));
   }
+  pdl_launch_dependents();  // not before: waiting CTAs beside the streaming ones cost 5 %
   sum = block_sum(sum, s);
   if (threadIdx.x == 0) part[blockIdx.x] = sum;
 }
@@ -127,15 +133,18 @@ __device__ __forceinline__ float norm_of(const double* part, int parts, double* 
 __global__ void __launch_bounds__(kClipThreads)
     k_list_norm(const double* part, int parts, float* norm) {
   __shared__ double s[kClipThreads / 32];
+  pdl_wait();
   const float v = norm_of(part, parts, s);
   if (threadIdx.x == 0) *norm = v;
 }
 
+template <int CAP>
 __global__ void __launch_bounds__(kClipThreads)
-    k_clip(const __grid_constant__ ListArgs a, const double* part, int parts, float max_norm,
+    k_clip(const __grid_constant__ ListArgs<CAP> a, const double* part, int parts, float max_norm,
            float* norm) {
   __shared__ double s[kClipThreads / 32];
   __shared__ float s_coef;
+  pdl_wait();
   const float v = norm_of(part, parts, s);
   if (threadIdx.x == 0) {
     const float c = __fdiv_rn(max_norm, __fadd_rn(v, 1e-6f));
@@ -154,7 +163,8 @@ __global__ void __launch_bounds__(kClipThreads)
   }
 }
 
-int64_t fill_list(const TensorEntry* t, int count, ListArgs* a) {
+template <int CAP>
+int64_t fill_list(const TensorEntry* t, int count, ListArgs<CAP>* a) {
   a->count = count;
   int64_t first = 0;
   for (int i = 0; i < count; ++i) {
@@ -165,6 +175,37 @@ int64_t fill_list(const TensorEntry* t, int count, ListArgs* a) {
   return a->pieces = first;
 }
 
+template <int CAP>
+cudaError_t run_clip(const TensorEntry* t, int count, bool clip, float max_norm, float* norm,
+                     double* part, const DeviceInfo& dev, cudaStream_t stream) {
+  const int max_grid = std::min(kClipMaxCtas, 2 * dev.num_sms);
+  int parts = 0;
+  for (int i = 0; i < count; i += CAP) {
+    ListArgs<CAP> a{};
+    const int64_t pieces = fill_list(t + i, std::min(CAP, count - i), &a);
+    if (pieces == 0) continue;
+    const int grid = (int)std::min<int64_t>(pieces, max_grid);
+    k_square_sum<<<grid, kClipThreads, 0, stream>>>(a, part + parts);
+    parts += grid;
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+  }
+  bool written = false;
+  for (int i = (count - 1) / CAP * CAP; clip && i >= 0; i -= CAP) {
+    ListArgs<CAP> a{};
+    const int64_t pieces = fill_list(t + i, std::min(CAP, count - i), &a);
+    if (pieces == 0) continue;
+    const int grid = (int)std::min<int64_t>(pieces, max_grid);
+    const cudaError_t e =
+        launch_after(k_clip<CAP>, (unsigned)grid, kClipThreads, stream, a, (const double*)part,
+                     parts, max_norm, written ? (float*)nullptr : norm);
+    if (e != cudaSuccess) return e;
+    written = true;
+  }
+  if (written) return cudaSuccess;
+  return launch_after(k_list_norm, 1, kClipThreads, stream, (const double*)part, parts, norm);
+}
+
 }  // namespace
 
 int64_t clip_workspace() { return (int64_t)kClipMaxCtas * kClipMaxLaunches * sizeof(double); }
@@ -173,37 +214,9 @@ int64_t clip_capacity() { return (int64_t)kListCapacity * kClipMaxLaunches; }
 cudaError_t launch_clip(const TensorEntry* t, int count, bool clip, float max_norm, float* norm,
                         void* workspace, const DeviceInfo& dev, cudaStream_t stream) {
   double* part = static_cast<double*>(workspace);
-  const int max_grid = std::min(kClipMaxCtas, 2 * dev.num_sms);
-  int parts = 0;
-  for (int i = 0; i < count; i += kListCapacity) {
-    ListArgs a{};
-    const int64_t pieces = fill_list(t + i, std::min(kListCapacity, count - i), &a);
-    if (pieces == 0) continue;
-    const int grid = (int)std::min<int64_t>(pieces, max_grid);
-    k_square_sum<<<grid, kClipThreads, 0, stream>>>(a, part + parts);
-    parts += grid;
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess) return e;
-  }
-  bool written = false;
-  if (clip) {
-    for (int i = (count - 1) / kListCapacity * kListCapacity; i >= 0; i -= kListCapacity) {
-      ListArgs a{};
-      const int64_t pieces = fill_list(t + i, std::min(kListCapacity, count - i), &a);
-      if (pieces == 0) continue;
-      const int grid = (int)std::min<int64_t>(pieces, max_grid);
-      k_clip<<<grid, kClipThreads, 0, stream>>>(a, part, parts, max_norm,
-                                                written ? nullptr : norm);
-      written = true;
-      cudaError_t e = cudaGetLastError();
-      if (e != cudaSuccess) return e;
-    }
-  }
-  if (!written) {
-    k_list_norm<<<1, kClipThreads, 0, stream>>>(part, parts, norm);
-    return cudaGetLastError();
-  }
-  return cudaSuccess;
+  return count <= kShortList
+             ? run_clip<kShortList>(t, count, clip, max_norm, norm, part, dev, stream)
+             : run_clip<kListCapacity>(t, count, clip, max_norm, norm, part, dev, stream);
 }
 
 }  // namespace nvfp4

@@ -132,6 +132,7 @@ __global__ void __launch_bounds__(256) k_sf_layout(const uint8_t* __restrict__ s
   const int64_t kt = blockIdx.x % k_tiles, blk = blockIdx.x / k_tiles;
   const int64_t s0 = kt * kTileScales;
   const bool vec = k16 % kTileScales == 0 && (reinterpret_cast<uintptr_t>(sc) & 15) == 0;
+  const bool pairs = (k16 & 1) == 0 && (reinterpret_cast<uintptr_t>(sc) & 1) == 0;
   for (int i = threadIdx.x; i < L; i += blockDim.x) {
     const int64_t line = blk * L + i;
     uint32_t w[kKSteps];
@@ -142,6 +143,11 @@ __global__ void __launch_bounds__(256) k_sf_layout(const uint8_t* __restrict__ s
       if (vec) {
 #pragma unroll
         for (int j = 0; j < kKSteps; ++j) w[j] = __ldg(reinterpret_cast<const uint32_t*>(p) + j);
+      } else if (pairs) {
+#pragma unroll
+        for (int j = 0; j < kTileScales; j += 2)
+          if (s0 + j < k16)
+            w[j >> 2] |= (uint32_t)__ldg(reinterpret_cast<const uint16_t*>(p + j)) << (8 * (j & 3));
       } else {
         for (int j = 0; j < kTileScales && s0 + j < k16; ++j)
           w[j >> 2] |= (uint32_t)p[j] << (8 * (j & 3));
@@ -306,6 +312,17 @@ __device__ __forceinline__ void epilogue_block32(const GemmParams& p, const Epil
     const int64_t off = (int64_t)(b.row0 + lane) * p.N + b.col0;
     const bool live = lane < b.rows;
     if (e.z != nullptr && live) store_run32(e.z, p.d_bf16, off, v, v8);
+    if (e.residual != nullptr && p.d_bf16) {  // in flight during the activation
+      Chunk<true> r[2];
+#pragma unroll
+      for (int c = 0; c < 2; ++c)
+        r[c].load(e.residual, off + kChunk * c, live ? kChunk : 0, v8 ? 32 : 16);
+      apply_act<32>(e.act, v);
+#pragma unroll
+      for (int j = 0; j < 32; ++j) v[j] = __fadd_rn(v[j], r[j / kChunk].get(j % kChunk));
+      if (live) store_run32(p.d, true, off, v, v8);
+      return;
+    }
     apply_act<32>(e.act, v);
     if (e.residual != nullptr) {
 #pragma unroll

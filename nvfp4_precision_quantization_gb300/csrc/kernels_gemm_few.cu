@@ -479,6 +479,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         beta = __fmul_rn(__ldg(p.w_amax + (int64_t)col * p.w_amax_stride), p.w_finv);
         bias = p.epi.bias_at(col);
       }
+      // the residual is loaded 16 rows ahead of its use, the first before the sums are ready
+      // (not for a part: whoever joins the tile may be writing d, which may be the residual)
+      float r[16];
+      if (live && whole) few_residual<16>(p, row0, col, r);
       const bool ready = mbar_wait_bounded(&acc_full[b], (seg >> 1) & 1);
       if (!ready) *err = 1;
       if (barrier_or<1, 32 * kEpiWarps>(!ready || *(volatile int*)err)) break;
@@ -487,8 +491,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       float4* part = p.sums + ((int64_t)tile * p.parts + w.slice) * kSums + l;
 #pragma unroll 1
       for (int c = 0; c < rows; c += 16) {
-        float r[16];
-        if (whole && live) few_residual<16>(p, row0 + c, col, r);
+        float next[16];
+        if (whole && live && c + 16 < rows) few_residual<16>(p, row0 + c + 16, col, next);
         uint32_t v[16];
         tmem_ld16(tmem + lanes + b * NT + c, v);
         tmem_ld_wait();
@@ -503,6 +507,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                      make_float4(f[4 * g], f[4 * g + 1], f[4 * g + 2], f[4 * g + 3]));
         } else if (live) {
           few_store<16>(p, row0 + c, col, f, r, alpha + c, beta, bias);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) r[j] = next[j];
         }
       }
       tc_fence_before();
@@ -522,11 +528,12 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       barrier_or<1, 32 * kEpiWarps>(false);  // read before it is written again
       if (!last || !live) continue;
       const int groups = (rows + 3) / 4;
+      few_residual<16>(p, row0, col, r);
       const float4* from = p.sums + (int64_t)tile * p.parts * kSums + l;
 #pragma unroll 1
       for (int g0 = 0; g0 < groups; g0 += 4) {
-        float r[16], f[16];
-        few_residual<16>(p, row0 + 4 * g0, col, r);
+        float next[16], f[16];
+        if (g0 + 4 < groups) few_residual<16>(p, row0 + 4 * g0 + 16, col, next);
         auto load = [&](int part, float4 (&a)[4]) {
 #pragma unroll
           for (int g = 0; g < 4; ++g)
@@ -553,6 +560,8 @@ __global__ void __launch_bounds__(kFewThreads, 1)
               }
         }
         few_store<16>(p, row0 + 4 * g0, col, f, r, alpha + 4 * g0, beta, bias);
+#pragma unroll
+        for (int j = 0; j < 16; ++j) r[j] = next[j];
       }
     }
   }
