@@ -305,6 +305,7 @@ cudaError_t pick_norm(const NormKernelArgs& k, const DeviceInfo& dev, cudaStream
   if (c <= 1024 && !few) return run_norm<BF16, NV4, 32, 2>(k, dev, stream);
   if (c <= 2048) return run_norm<BF16, NV4, 128, 1>(k, dev, stream);
   if (c <= 4096) return run_norm<BF16, NV4, 256, 1>(k, dev, stream);
+  if (c <= 6144 && c > 4096) return run_norm<BF16, NV4, 384, 1>(k, dev, stream);
   if (c <= 8192 && !few) return run_norm<BF16, NV4, 256, 2>(k, dev, stream);
   if (c <= 8192) return run_norm<BF16, NV4, 512, 1>(k, dev, stream);
   if (c <= 16384 && !few) return run_norm<BF16, NV4, 512, 2>(k, dev, stream);

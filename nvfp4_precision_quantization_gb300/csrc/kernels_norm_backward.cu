@@ -274,8 +274,10 @@ cudaError_t pick_norm_backward(const NormBackwardKernelArgs& k, int max_parts,
                                const DeviceInfo& dev, cudaStream_t stream, int* parts) {
   const int c = k.cols;
   if (c <= 512) return run_norm_backward<BF16, 32, 1>(k, max_parts, dev, stream, parts);
+  if (c <= 1024) return run_norm_backward<BF16, 64, 1>(k, max_parts, dev, stream, parts);
   if (c <= 2048) return run_norm_backward<BF16, 128, 1>(k, max_parts, dev, stream, parts);
   if (c <= 4096) return run_norm_backward<BF16, 256, 1>(k, max_parts, dev, stream, parts);
+  if (c <= 6144) return run_norm_backward<BF16, 384, 1>(k, max_parts, dev, stream, parts);
   if (c <= 8192) return run_norm_backward<BF16, 512, 1>(k, max_parts, dev, stream, parts);
   if (c <= 16384) return run_norm_backward<BF16, 1024, 1>(k, max_parts, dev, stream, parts);
   return run_norm_backward<BF16, 1024, 2>(k, max_parts, dev, stream, parts);

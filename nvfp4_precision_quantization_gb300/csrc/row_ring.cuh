@@ -26,11 +26,13 @@ __device__ __forceinline__ float2 team_sum_max(float s, float m, float2* red) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (lane == 0) red[warp] = make_float2(s, m);
     __syncthreads();
-    const float2 v = red[warp - warp % kWarps + lane % kWarps];
+    constexpr int kTree = kWarps <= 2 ? 2 : kWarps <= 4 ? 4 : kWarps <= 8 ? 8 : kWarps <= 16 ? 16 : 32;
+    const int i = lane % kTree;
+    const float2 v = i < kWarps ? red[warp - warp % kWarps + i] : make_float2(0.0f, 0.0f);
     s = v.x;
     m = v.y;
 #pragma unroll
-    for (int d = kWarps / 2; d > 0; d >>= 1) {
+    for (int d = kTree / 2; d > 0; d >>= 1) {
       s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, d));
       m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
     }
