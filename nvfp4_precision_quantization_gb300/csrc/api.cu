@@ -721,6 +721,12 @@ nvfp4_status nvfp4_gemm_bias_act(const nvfp4_operand* a, const nvfp4_operand* b,
   if (epilogue->bias != nullptr && !valid_in_dtype(epilogue->bias_dtype))
     return fail(NVFP4_ERR_INVALID, "unknown bias_dtype");
   if (!valid_activation(epilogue->act)) return fail(NVFP4_ERR_INVALID, "unknown activation");
+  const uintptr_t esize = out_dtype == NVFP4_OUT_FP32 ? 4 : 2;
+  if ((reinterpret_cast<uintptr_t>(d) | reinterpret_cast<uintptr_t>(epilogue->residual) |
+       reinterpret_cast<uintptr_t>(epilogue->z)) % esize != 0 ||
+      reinterpret_cast<uintptr_t>(epilogue->bias) %
+              (epilogue->bias_dtype == NVFP4_IN_FP32 ? 4 : 2) != 0)
+    return fail(NVFP4_ERR_INVALID, "d, bias, residual or z is not aligned to its element size");
   if (m > 0 && n > 0 && (out_dtype == NVFP4_OUT_BF16 || out_dtype == NVFP4_OUT_FP32)) {
     const uint64_t bytes = (uint64_t)m * (uint64_t)n * (out_dtype == NVFP4_OUT_BF16 ? 2 : 4);
     if (epilogue->residual != d && bytes_overlap(epilogue->residual, bytes, d, bytes))

@@ -5,10 +5,14 @@
 // Bound by memory: the norm must be known before the first scaled value, so the list is
 // read twice and written once.  The list travels in the kernels' arguments (no device
 // table to keep or to copy) and is cut into pieces of kPiece values that a persistent
-// grid walks.  The second pass walks the pieces backwards, so it starts on what the
-// first pass read last, which the L2 still holds.  Each CTA of the first pass leaves one
+// grid walks, the second pass backwards, from what the first read last (worth 1 to 2 %:
+// holding the tail in L2 with evict-last loads, giving a piece to the same CTA in both
+// passes and streaming stores added nothing measurable).  Each CTA of the first pass leaves one
 // FP64 partial sum; each CTA of the second adds them all, in the same order, instead of
 // waiting for a kernel between the two.
+//
+// Measured: 973 M BF16 values into a second buffer 900 us: 280 us for the first pass (6.95
+// TB/s) and 597 us for the second (6.45 TB/s) when each is run cold.
 #include <algorithm>
 
 #include "internal.h"

