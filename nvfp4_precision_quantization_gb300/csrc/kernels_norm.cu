@@ -41,6 +41,7 @@ struct NormKernelArgs {
   bool w_bf16;
   int g_x, g_res, g_w, g_h, g_y, g_q8, g_codes;  // row grains (row_io.cuh)
   int g_min;  // the least of those of x, res, h, y (and of codes below 4)
+  bool bases_aligned;  // x and res start on 16 bytes
   int* status;
 };
 
@@ -67,8 +68,9 @@ __device__ __forceinline__ void norm_gather(const NormKernelArgs& a, int64_t bas
     if (a.h != nullptr) {
       Chunk<BF16> ch;
       ch.set(v[c]);
-      ch.store_warp<STAGED>(a.h, base + col, n, live ? warp_run(col - kChunk * lane, a.cols) : 0, a.g_h,
-                    stage, lane);
+      ch.store_warp<STAGED>(a.h, base + col, n,
+                            live ? warp_run(col - kChunk * lane, a.cols) : 0, a.g_h, stage,
+                            lane);
     }
     float w[kChunk];
     load_vector16(a.w, a.w_bf16, col, n, a.g_w, w);
@@ -106,7 +108,8 @@ __device__ __forceinline__ void norm_emit(const NormKernelArgs& a, int64_t row, 
       Chunk<BF16> cy;
       cy.set(v[c]);
       cy.store_warp<STAGED>(a.y, base + col, live ? chunk_len(col, a.cols) : 0,
-                    live ? warp_run(col - kChunk * lane, a.cols) : 0, a.g_y, stage, lane);
+                            live ? warp_run(col - kChunk * lane, a.cols) : 0, a.g_y, stage,
+                            lane);
     }
   }
   if constexpr (NV4) {
@@ -170,9 +173,8 @@ __device__ __forceinline__ void norm_emit(const NormKernelArgs& a, int64_t row, 
       if (!STAGED || a.g_q8 >= 4) {
         if (n > 0) store_bytes(a.q8 + base + col, cw, n);
       } else {
-        staged_store<4, kChunk>(reinterpret_cast<char*>(a.q8) + base + col - kChunk * lane,
-                                live ? (int)warp_run(col - kChunk * lane, a.cols) : 0, a.g_q8,
-                                stage, lane, cw);
+        shifted_store(reinterpret_cast<char*>(a.q8) + base + col - kChunk * lane,
+                      live ? (int)warp_run(col - kChunk * lane, a.cols) : 0, lane, cw);
       }
     }
   }
@@ -221,8 +223,18 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_add_rmsnorm(const Nor
   }
 }
 
-template <bool BF16, bool NV4, int TPR, int NCH>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
+// CTAs per SM that the registers of the kernel for unaligned rows have to allow: left to
+// itself the compiler takes up to 168 per thread, and the row's latencies lie open (4000 x 5001
+// BF16 76 us with 168, 58 with 80; FP32 86 and 71).
+constexpr int ring_any_ctas(bool bf16, int threads) {
+  const int n = (bf16 ? 1024 : 768) / threads;
+  return n > 0 ? n : 1;
+}
+
+// ANY: rows that are not 16-byte aligned (RowRing).
+template <bool BF16, bool NV4, int TPR, int NCH, bool ANY>
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR,
+                                  ANY ? ring_any_ctas(BF16, TPR < 256 ? 256 : TPR) : 1)
     k_add_rmsnorm_ring(const NormKernelArgs a, const RingArgs g) {
   constexpr int kThreads = TPR < 256 ? 256 : TPR;
   constexpr int kTeams = kThreads / TPR;
@@ -231,35 +243,48 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
   __shared__ float2 red[2][kThreads / 32];
   __shared__ __align__(8) uint64_t full[kRingStages];
   __shared__ int err;
-  const int t = threadIdx.x % TPR, team = threadIdx.x / TPR;
+  __shared__ __align__(16) uint8_t stages[ANY ? kThreads / 32 : 1][kStageBytes];
+  const int t = threadIdx.x % TPR, team = threadIdx.x / TPR, lane = threadIdx.x & 31;
+  uint8_t* out_stage = ANY ? stages[ANY ? threadIdx.x >> 5 : 0] : nullptr;
   const int64_t step = (int64_t)gridDim.x * kTeams;
-  const RowRing<2> ring{full, &err, ring_smem, {a.x, a.res}, a.rows, (int64_t)a.cols * kElem,
-                        kTeams, g};
+  const RowRing<2, ANY> ring{full, &err, ring_smem, {a.x, a.res}, a.rows,
+                             (int64_t)a.cols * kElem, kTeams, g};
   ring.start(step);
   int it = 0, s = 0;
   for (int64_t row0 = (int64_t)blockIdx.x * kTeams; row0 < a.rows; row0 += step, ++it) {
     const int64_t row = row0 + team;
     const bool live = row < a.rows;
     const int64_t base = row * a.cols;
-    const uint8_t* st = ring.stage(s) + team * a.cols * kElem;
+    const uint8_t* st = ring.stage(s) + ring.shift(row0) + team * a.cols * kElem;
     const bool ok = ring.wait(s, it);
+    ring.finish(s, row0);
     float v[NCH][kChunk], bmax[NCH], ss, mx;
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
       const int col = (c * TPR + t) * kChunk;
       const int n = live && ok ? chunk_len(col, a.cols) : 0;
       Chunk<BF16> cx;
-      cx.load_shared(st + col * kElem, n, threadIdx.x & 31);
+      if constexpr (ANY) {
+        cx.load_shared_any(st + min(col, a.cols) * kElem, lane);
+        cx.cut(n);
+      } else {
+        cx.load_shared(st + col * kElem, n, lane);
+      }
 #pragma unroll
       for (int i = 0; i < kChunk; ++i) v[c][i] = cx.get(i);
       if (a.res != nullptr) {
         Chunk<BF16> cr;
-        cr.load_shared(st + g.tensor_bytes + col * kElem, n, threadIdx.x & 31);
+        if constexpr (ANY) {
+          cr.load_shared_any(st + g.tensor_bytes + min(col, a.cols) * kElem, lane);
+          cr.cut(n);
+        } else {
+          cr.load_shared(st + g.tensor_bytes + col * kElem, n, lane);
+        }
 #pragma unroll
         for (int i = 0; i < kChunk; ++i) v[c][i] = __fadd_rn(v[c][i], cr.get(i));
       }
     }
-    norm_gather<BF16, TPR, NCH, false>(a, base, live && ok, t, nullptr, v, bmax, ss, mx);
+    norm_gather<BF16, TPR, NCH, ANY>(a, base, live && ok, t, out_stage, v, bmax, ss, mx);
     const float2 r = team_sum_max<TPR, true>(ss, mx, red[it & 1]);
     if (*(volatile int*)&err) {
       ring.give_up(it, row0, step, a.status);
@@ -267,9 +292,27 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
     }
     if (threadIdx.x == 0 && row0 + g.stages * step < a.rows)
       ring.fetch(s, row0 + g.stages * step);
-    norm_emit<BF16, NV4, TPR, NCH, false>(a, row, live, t, nullptr, v, bmax, r);
+    norm_emit<BF16, NV4, TPR, NCH, ANY>(a, row, live, t, out_stage, v, bmax, r);
     if (++s == g.stages) s = 0;
   }
+}
+
+// The ring kernel, where at least two stages fit and every CTA has several groups (done).
+template <bool BF16, bool NV4, int TPR, int NCH, bool ANY>
+cudaError_t run_norm_ring(const NormKernelArgs& k, int64_t groups, const DeviceInfo& dev,
+                          cudaStream_t stream, bool* done) {
+  constexpr int kThreads = TPR < 256 ? 256 : TPR;
+  auto ring = k_add_rmsnorm_ring<BF16, NV4, TPR, NCH, ANY>;
+  static const RingKernel limits = ring_kernel(ring, kThreads);
+  const RingPlan p = plan_ring(limits, k.res ? 2 : 1,
+                               (int64_t)(kThreads / TPR) * k.cols * (BF16 ? 2 : 4), ANY);
+  const int64_t fill = (int64_t)p.ctas * dev.num_sms;
+  if (p.ctas == 0 || groups <= 2 * fill) return cudaSuccess;
+  *done = true;
+  const cudaError_t e = allow_ring(ring, limits);
+  if (e != cudaSuccess) return e;
+  ring<<<(unsigned)fill, kThreads, p.g.stages * p.g.stage_bytes, stream>>>(k, p.g);
+  return cudaGetLastError();
 }
 
 template <bool BF16, bool NV4, int TPR, int NCH>
@@ -283,19 +326,19 @@ cudaError_t run_norm(const NormKernelArgs& k, const DeviceInfo& dev, cudaStream_
   const int resident = k.g_min >= 16 ? aligned : staged;
   const int64_t groups = (k.rows + kTeams - 1) / kTeams;
   const int64_t grid = std::min<int64_t>(groups, (int64_t)resident * dev.num_sms);
+  bool done = false;
+  cudaError_t e = cudaSuccess;
   if (k.g_min >= 16) {
-    auto ring = k_add_rmsnorm_ring<BF16, NV4, TPR, NCH>;
-    static const RingKernel limits = ring_kernel(ring, kThreads);
-    const RingPlan p = plan_ring(limits, k.res ? 2 : 1,
-                                 (int64_t)kTeams * k.cols * (BF16 ? 2 : 4));
-    const int64_t fill = (int64_t)p.ctas * dev.num_sms;
-    if (p.ctas > 0 && groups > 2 * fill) {
-      const cudaError_t e = allow_ring(ring, limits);
-      if (e != cudaSuccess) return e;
-      ring<<<(unsigned)fill, kThreads, p.g.stages * p.g.stage_bytes, stream>>>(k, p.g);
-      return cudaGetLastError();
-    }
+    e = run_norm_ring<BF16, NV4, TPR, NCH, false>(k, groups, dev, stream, &done);
+  } else if constexpr (NCH == 1 && (TPR > 32 || !BF16)) {
+    // Rows that are not aligned: one step per thread (two stages of longer rows seldom fit).
+    // Through the ring and loaded directly, BF16 with FP8 codes: 4000 x 5001 58 and 80 us,
+    // 16384 x 1001 41 and 88; FP32: 4000 x 5001 71 and 103, 16384 x 511 30 and 41.  BF16
+    // rows of one warp's team do not gain: 16384 x 500 25.4 and 22.6, 16384 x 511 26.7 and 25.8.
+    if (k.bases_aligned)
+      e = run_norm_ring<BF16, NV4, TPR, NCH, true>(k, groups, dev, stream, &done);
   }
+  if (done || e != cudaSuccess) return e;
   direct<<<(unsigned)grid, kThreads, 0, stream>>>(k);
   return cudaGetLastError();
 }
@@ -307,6 +350,9 @@ cudaError_t pick_norm(const NormKernelArgs& k, const DeviceInfo& dev, cudaStream
   const bool few = k.rows <= 2LL * dev.num_sms || k.g_min < 16;
   const int c = k.cols;
   if (c <= 512) return run_norm<BF16, NV4, 32, 1>(k, dev, stream);
+  // teams of two warps where those of four would be half idle (16384 x 1001 unaligned: 41 us,
+  // and 76 by four)
+  if (c <= 1024 && k.g_min < 16) return run_norm<BF16, NV4, 64, 1>(k, dev, stream);
   if (c <= 1024 && !few) return run_norm<BF16, NV4, 32, 2>(k, dev, stream);
   if (c <= 2048) return run_norm<BF16, NV4, 128, 1>(k, dev, stream);
   if (c <= 4096) return run_norm<BF16, NV4, 256, 1>(k, dev, stream);
@@ -360,6 +406,8 @@ cudaError_t launch_add_rmsnorm(const NormArgs& a, const DeviceInfo& dev, cudaStr
   // (codes are stored in words where they are so aligned)
   if (a.q8 && k.g_q8 < 4) k.g_min = std::min(k.g_min, k.g_q8);
   if (a.codes && k.g_codes < 4) k.g_min = std::min(k.g_min, k.g_codes);
+  k.bases_aligned =
+      (reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.residual)) % 16 == 0;
   k.status = dev.status;
   if (a.in == InType::BF16)
     return a.codes || a.amax ? pick_norm<true, true>(k, dev, stream)

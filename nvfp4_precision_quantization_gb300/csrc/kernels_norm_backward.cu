@@ -27,6 +27,7 @@ struct NormBackwardKernelArgs {
   bool w_bf16;
   int g_dy, g_h, g_dh, g_w, g_dx, g_part;
   int g_min;  // the least of those of dy, h, dh and dx
+  bool bases_aligned;  // dy, h and dh start on 16 bytes
   int* status;
 };
 
@@ -75,8 +76,8 @@ __device__ __forceinline__ void backward_emit(const NormBackwardKernelArgs& a, i
     }
     Chunk<BF16> co;
     co.set(dx);
-    co.store_warp<STAGED>(a.dx, base + col, n, live ? warp_run(col - kChunk * lane, a.cols) : 0, a.g_dx,
-                  stage, lane);
+    co.store_warp<STAGED>(a.dx, base + col, n,
+                          live ? warp_run(col - kChunk * lane, a.cols) : 0, a.g_dx, stage, lane);
   }
 }
 
@@ -167,7 +168,8 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
   backward_partials<TPR, NCH>(a, t, team, dw, s_dw);
 }
 
-template <bool BF16, int TPR, int NCH>
+// ANY: rows that are not 16-byte aligned (RowRing).
+template <bool BF16, int TPR, int NCH, bool ANY>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
     k_add_rmsnorm_backward_ring(const NormBackwardKernelArgs a, const RingArgs g) {
   pdl_launch_dependents();  // the columns' sum may be set up meanwhile
@@ -179,10 +181,12 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
   __shared__ float s_dw[kTeams > 1 ? TPR * NCH * kChunk : 1];
   __shared__ __align__(8) uint64_t full[kRingStages];
   __shared__ int err;
+  __shared__ __align__(16) uint8_t stages[ANY ? kThreads / 32 : 1][kStageBytes];
+  uint8_t* out_stage = ANY ? stages[ANY ? threadIdx.x >> 5 : 0] : nullptr;
   const int t = threadIdx.x % TPR, team = threadIdx.x / TPR, lane = threadIdx.x & 31;
   const int64_t step = (int64_t)gridDim.x * kTeams;
-  const RowRing<3> ring{full, &err, ring_smem, {a.dy, a.h, a.dh}, a.rows,
-                        (int64_t)a.cols * kElem, kTeams, g};
+  const RowRing<3, ANY> ring{full, &err, ring_smem, {a.dy, a.h, a.dh}, a.rows,
+                             (int64_t)a.cols * kElem, kTeams, g};
   ring.start(step);
   float dw[NCH][kChunk];
 #pragma unroll
@@ -194,16 +198,26 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
     const int64_t row = row0 + team;
     const bool live = row < a.rows;
     const float s = live ? a.rstd[row] : 0.0f;
-    const uint8_t* p = ring.stage(st) + team * a.cols * kElem;
+    const uint8_t* p = ring.stage(st) + ring.shift(row0) + team * a.cols * kElem;
     const bool ok = ring.wait(st, it);
+    ring.finish(st, row0);
     Chunk<BF16> cy[NCH], ch[NCH], cd[NCH];
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
       const int col = (c * TPR + t) * kChunk;
       const int n = live && ok ? chunk_len(col, a.cols) : 0;
-      cy[c].load_shared(p + col * kElem, n, lane);
-      ch[c].load_shared(p + g.tensor_bytes + col * kElem, n, lane);
-      if (a.dh != nullptr) cd[c].load_shared(p + 2 * g.tensor_bytes + col * kElem, n, lane);
+      if constexpr (ANY) {
+        const uint8_t* q = p + min(col, a.cols) * kElem;
+        cy[c].load_shared_any(q, lane);
+        ch[c].load_shared_any(q + g.tensor_bytes, lane);
+        if (a.dh != nullptr) cd[c].load_shared_any(q + 2 * g.tensor_bytes, lane);
+        cy[c].cut(n);
+        ch[c].cut(n);
+      } else {
+        cy[c].load_shared(p + col * kElem, n, lane);
+        ch[c].load_shared(p + g.tensor_bytes + col * kElem, n, lane);
+        if (a.dh != nullptr) cd[c].load_shared(p + 2 * g.tensor_bytes + col * kElem, n, lane);
+      }
     }
     const float dot = backward_gather<BF16, TPR, NCH>(a, t, s, cy, ch, dw);
     const float2 r = team_sum_max<TPR, true>(dot, 0.0f, red[it & 1]);
@@ -213,8 +227,8 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
     }
     if (threadIdx.x == 0 && row0 + g.stages * step < a.rows)
       ring.fetch(st, row0 + g.stages * step);
-    backward_emit<BF16, TPR, NCH, false>(a, row * a.cols, live, t, nullptr, s,
-                                  __fdiv_rn(r.x, (float)a.cols), cy, ch, cd);
+    backward_emit<BF16, TPR, NCH, ANY>(a, row * a.cols, live, t, out_stage, s,
+                                    __fdiv_rn(r.x, (float)a.cols), cy, ch, cd);
     if (++st == g.stages) st = 0;
   }
   backward_partials<TPR, NCH>(a, t, team, dw, s_dw);
@@ -241,6 +255,26 @@ __global__ void __launch_bounds__(256) k_column_sum(const float* part, int n, in
   }
 }
 
+// The ring kernel, where at least two stages fit and every CTA has several groups (done).
+template <bool BF16, int TPR, int NCH, bool ANY>
+cudaError_t run_backward_ring(const NormBackwardKernelArgs& k, int64_t groups, int max_parts,
+                              const DeviceInfo& dev, cudaStream_t stream, int* parts,
+                              bool* done) {
+  constexpr int kThreads = TPR < 256 ? 256 : TPR;
+  auto ring = k_add_rmsnorm_backward_ring<BF16, TPR, NCH, ANY>;
+  static const RingKernel limits = ring_kernel(ring, kThreads);
+  const RingPlan p = plan_ring(limits, k.dh ? 3 : 2,
+                               (int64_t)(kThreads / TPR) * k.cols * (BF16 ? 2 : 4), ANY);
+  const int64_t fill = std::min<int64_t>((int64_t)p.ctas * dev.num_sms, max_parts);
+  if (p.ctas == 0 || groups <= 2 * fill) return cudaSuccess;
+  *done = true;
+  const cudaError_t e = allow_ring(ring, limits);
+  if (e != cudaSuccess) return e;
+  *parts = (int)fill;
+  ring<<<(unsigned)fill, kThreads, p.g.stages * p.g.stage_bytes, stream>>>(k, p.g);
+  return cudaGetLastError();
+}
+
 template <bool BF16, int TPR, int NCH>
 cudaError_t run_norm_backward(const NormBackwardKernelArgs& k, int max_parts,
                               const DeviceInfo& dev, cudaStream_t stream, int* parts) {
@@ -254,20 +288,19 @@ cudaError_t run_norm_backward(const NormBackwardKernelArgs& k, int max_parts,
   const int64_t groups = (k.rows + kTeams - 1) / kTeams;
   const int grid = (int)std::min<int64_t>(
       std::min<int64_t>(groups, (int64_t)resident * dev.num_sms), max_parts);
-  if (k.g_min >= 16) {
-    auto ring = k_add_rmsnorm_backward_ring<BF16, TPR, NCH>;
-    static const RingKernel limits = ring_kernel(ring, kThreads);
-    const RingPlan p = plan_ring(limits, k.dh ? 3 : 2,
-                                 (int64_t)kTeams * k.cols * (BF16 ? 2 : 4));
-    const int64_t fill = std::min<int64_t>((int64_t)p.ctas * dev.num_sms, max_parts);
-    if (p.ctas > 0 && groups > 2 * fill) {
-      const cudaError_t e = allow_ring(ring, limits);
-      if (e != cudaSuccess) return e;
-      *parts = (int)fill;
-      ring<<<(unsigned)fill, kThreads, p.g.stages * p.g.stage_bytes, stream>>>(k, p.g);
-      return cudaGetLastError();
-    }
+  bool done = false;
+  cudaError_t e = cudaSuccess;
+  if constexpr (BF16 || NCH == 1) {  // two stages of longer FP32 rows do not fit
+    if (k.g_min >= 16)
+      e = run_backward_ring<BF16, TPR, NCH, false>(k, groups, max_parts, dev, stream, parts, &done);
   }
+  if constexpr (NCH == 1) {
+    // Rows that are not aligned.  BF16, through the ring and loaded directly: 4000 x 5001 62
+    // and 88 us, 16384 x 1001 46 and 76, 16384 x 25 30 and 35; FP32 4000 x 5001 74 and 123.
+    if (k.g_min < 16 && k.bases_aligned)
+      e = run_backward_ring<BF16, TPR, NCH, true>(k, groups, max_parts, dev, stream, parts, &done);
+  }
+  if (done || e != cudaSuccess) return e;
   *parts = grid;
   direct<<<grid, kThreads, 0, stream>>>(k);
   return cudaGetLastError();
@@ -319,6 +352,8 @@ cudaError_t launch_add_rmsnorm_backward(const NormBackwardArgs& a, const DeviceI
   k.g_part = row_grain(k.part, a.cols * 4);
   k.g_min = std::min(k.g_dy, std::min(k.g_h, k.g_dx));
   if (a.dh) k.g_min = std::min(k.g_min, k.g_dh);
+  k.bases_aligned = (reinterpret_cast<uintptr_t>(a.dy) | reinterpret_cast<uintptr_t>(a.h) |
+                     reinterpret_cast<uintptr_t>(a.dh)) % 16 == 0;
   k.status = dev.status;
   int parts = 0;
   const int max_parts = (int)std::min<int64_t>(a.rows, kNormBackwardParts);

@@ -181,6 +181,74 @@ __device__ __forceinline__ void staged_store(char* p, int bytes, int unit, uint8
   __syncwarp();
 }
 
+// Bytes [at, at + d) of a unit (at a multiple of d; d: 1, 2, 4 or 8) to q + at.
+__device__ __forceinline__ void store_piece(char* q, const uint32_t* x, int at, int d) {
+  if (d == 8) {
+    *reinterpret_cast<uint2*>(q + at) = at & 8 ? make_uint2(x[2], x[3]) : make_uint2(x[0], x[1]);
+    return;
+  }
+  const uint32_t hi = at & 4 ? x[3] : x[2], lo = at & 4 ? x[1] : x[0], w = at & 8 ? hi : lo;
+  if (d == 4) *reinterpret_cast<uint32_t*>(q + at) = w;
+  else if (d == 2) *reinterpret_cast<uint16_t*>(q + at) = (uint16_t)(w >> (8 * (at & 2)));
+  else *reinterpret_cast<uint8_t*>(q + at) = (uint8_t)(w >> (8 * (at & 3)));
+}
+
+// 16 one-byte codes of every lane, at most `bytes` bytes in all, to memory from any byte p on
+// as aligned 16-byte units: each lane takes the words of the lane before it and shifts its own
+// behind them, so that what it holds starts on a unit.  The units that the run begins and ends
+// in are stored as pieces of 1 to 8 bytes.  (The staging makes 16 one-byte stores of it: 4000
+// x 5001 norm 69 us that way, 58 this way.  For 2- and 4-byte elements, whose staging needs
+// half and a quarter of the stores, the shifts cost more than they save: 16384 x 1001 41 us
+// staged, 45 shifted.)
+__device__ __forceinline__ void shifted_store(char* p, int bytes, int lane, const uint32_t* w) {
+  constexpr int W = 4;
+  if (bytes <= 0) return;  // the same for the whole warp
+  const int b = (int)(reinterpret_cast<uintptr_t>(p) & 15);
+  uint32_t z[W + 8];
+#pragma unroll
+  for (int k = 0; k < 4; ++k) {
+    z[k] = __shfl_up_sync(0xffffffffu, w[W - 4 + k], 1);
+    z[W + 4 + k] = 0;
+  }
+#pragma unroll
+  for (int k = 0; k < W; ++k) z[4 + k] = w[k];
+#pragma unroll
+  for (int k = W + 7; k >= 2; --k) z[k] = (b & 8) ? z[k - 2] : z[k];
+#pragma unroll
+  for (int k = W + 7; k >= 1; --k) z[k] = (b & 4) ? z[k - 1] : z[k];
+  const int sh = 8 * (b & 3);
+  const int end = b + bytes;  // the run lies in [b, end) of the units from p - b on
+#pragma unroll
+  for (int u = 0; u <= W / 4; ++u) {
+    const int o = 4 * W * lane + 16 * u;
+    if (u == W / 4 && lane != 31) break;  // the next lane's first unit
+    uint32_t x[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      x[k] = __funnelshift_l(z[4 * u + k + 3], z[4 * u + k + 4], sh);
+    char* q = p - b + o;
+    if (o >= b && o + 16 <= end) {
+      *reinterpret_cast<uint4*>(q) = make_uint4(x[0], x[1], x[2], x[3]);
+    } else if (o < end) {
+      // [from, to) of the unit, in pieces that double up to 8 bytes and halve again
+      const int from = o < b ? b : 0, to = end - o < 16 ? end - o : 16;
+      int at = from;
+#pragma unroll
+      for (int d = 1; d <= 8; d *= 2)
+        if ((at & d) && at + d <= to) {
+          store_piece(q, x, at, d);
+          at += d;
+        }
+#pragma unroll
+      for (int d = 8; d >= 1; d /= 2)
+        if (at + d <= to) {
+          store_piece(q, x, at, d);
+          at += d;
+        }
+    }
+  }
+}
+
 __device__ __forceinline__ void ldg_v8(const void* p, uint32_t* w) {
   asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]),
@@ -277,6 +345,47 @@ struct Chunk {
       w[4 * k + 1] = u[k].y;
       w[4 * k + 2] = u[k].z;
       w[4 * k + 3] = u[k].w;
+    }
+  }
+  // The same for a chunk that starts at any element, by a whole warp whose lanes hold
+  // consecutive chunks: aligned words, a lane's in an order rotated so that the 32 lanes of an
+  // access hit all banks; the word that a chunk ends in is the next lane's first.  The words
+  // around the row lie inside the stage; elements from n on come out as anything.
+  __device__ __forceinline__ void load_shared_any(const uint8_t* p, int lane) {
+    const uint32_t a = smem_addr(p);
+    const uint32_t* q = reinterpret_cast<const uint32_t*>(p - (a & 3));
+    const int rot = BF16 ? lane >> 2 : lane >> 1;  // modulo kWords
+    uint32_t u[kWords];
+#pragma unroll
+    for (int k = 0; k < kWords; ++k) u[k] = q[(k + rot) & (kWords - 1)];
+#pragma unroll
+    for (int d = 1; d < kWords; d *= 2) {  // u[k] holds word k + rot: rotate back
+      uint32_t r[kWords];
+#pragma unroll
+      for (int k = 0; k < kWords; ++k) r[k] = (rot & d) ? u[(k - d) & (kWords - 1)] : u[k];
+#pragma unroll
+      for (int k = 0; k < kWords; ++k) u[k] = r[k];
+    }
+    if constexpr (BF16) {
+      uint32_t after = __shfl_down_sync(0xffffffffu, u[0], 1);
+      if (lane == 31) after = q[kWords];
+      const int sh = 8 * (int)(a & 2);
+#pragma unroll
+      for (int k = 0; k < kWords; ++k)
+        w[k] = __funnelshift_r(u[k], k + 1 < kWords ? u[k + 1] : after, sh);
+    } else {
+#pragma unroll
+      for (int k = 0; k < kWords; ++k) w[k] = u[k];
+    }
+  }
+  // Elements from n on become zero.
+  __device__ __forceinline__ void cut(int n) {
+    if (n >= kChunk) return;
+#pragma unroll
+    for (int i = 0; i < kChunk; ++i) {
+      if (i < n) continue;
+      if constexpr (BF16) w[i >> 1] &= (i & 1) ? 0x0000ffffu : 0xffff0000u;
+      else w[i] = 0;
     }
   }
   __device__ __forceinline__ float get(int i) const {

@@ -58,7 +58,12 @@ struct RingArgs {
   int stage_bytes;
 };
 
-template <int NT>
+// ANY: rows of any length and alignment within their tensors, whose bases are 16-byte aligned:
+// a stage receives the 16-byte units that cover the group, and the group starts `shift`
+// bytes into it.  The units never reach past the tensor: its last few bytes, if they fill
+// no unit, are copied by the threads (finish()).  They belong to the last group alone: a
+// group of several teams starts on a unit, or its rows are longer than one.
+template <int NT, bool ANY = false>
 struct RowRing {
   uint64_t* full;
   int* err;
@@ -72,7 +77,14 @@ struct RowRing {
   // thread 0: start the copies of the group of rows that begins at row0
   __device__ __forceinline__ void fetch(int s, int64_t row0) const {
     const int64_t left = rows - row0;
-    const uint32_t bytes = (uint32_t)((left < teams ? left : teams) * row_bytes);
+    int64_t from = row0 * row_bytes, to = from + (left < teams ? left : teams) * row_bytes;
+    if constexpr (ANY) {
+      from &= ~(int64_t)15;
+      const int64_t end = (rows * row_bytes) & ~(int64_t)15;
+      to = (to + 15) & ~(int64_t)15;
+      if (to > end) to = end > from ? end : from;
+    }
+    const uint32_t bytes = (uint32_t)(to - from);
     int n = 0;
 #pragma unroll
     for (int i = 0; i < NT; ++i) n += src[i] != nullptr;
@@ -80,8 +92,29 @@ struct RowRing {
 #pragma unroll
     for (int i = 0; i < NT; ++i)
       if (src[i] != nullptr)
-        bulk_copy_in(stage(s) + i * g.tensor_bytes,
-                     static_cast<const char*>(src[i]) + row0 * row_bytes, bytes, &full[s]);
+        if (!ANY || bytes > 0)
+          bulk_copy_in(stage(s) + i * g.tensor_bytes, static_cast<const char*>(src[i]) + from,
+                       bytes, &full[s]);
+  }
+  // ANY: where in its stage the group of rows at row0 starts.
+  __device__ __forceinline__ int shift(int64_t row0) const {
+    return ANY ? (int)((row0 * row_bytes) & 15) : 0;
+  }
+  // ANY, every thread, after wait(): the tensor's last bytes, which no unit holds, into the
+  // stage of the group that ends with them.
+  __device__ __forceinline__ void finish(int s, int64_t row0) const {
+    if constexpr (ANY) {
+      const int64_t total = rows * row_bytes, end = total & ~(int64_t)15;
+      if (row0 + teams < rows || end == total) return;  // the same for the whole CTA
+      const int64_t from = (row0 * row_bytes) & ~(int64_t)15;
+      const int n = (int)(total - end);
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+        if (src[i] != nullptr && (int)threadIdx.x < n)
+          stage(s)[i * g.tensor_bytes + (end - from) + threadIdx.x] =
+              static_cast<const uint8_t*>(src[i])[end + threadIdx.x];
+      __syncthreads();
+    }
   }
   __device__ __forceinline__ void start(int64_t step) const {
     if (threadIdx.x == 0) {
@@ -148,9 +181,10 @@ struct RingPlan {
   int ctas;
   RingArgs g;
 };
-RingPlan plan_ring(const RingKernel& k, int tensors, int64_t group_bytes) {
+RingPlan plan_ring(const RingKernel& k, int tensors, int64_t group_bytes, bool any = false) {
   RingPlan p{};
-  const int64_t tensor = (group_bytes + 127) / 128 * 128, stage = tensors * tensor;
+  // any: up to 30 bytes of the units around the rows, and a lane's reads past a row's end
+  const int64_t tensor = (group_bytes + (any ? 128 : 0) + 127) / 128 * 128, stage = tensors * tensor;
   for (int c = k.resident; c > 0; --c) {
     // an SM's 228 KB, of which every CTA takes 1 KB beside its own
     const int64_t room =

@@ -288,3 +288,34 @@ def test_other_stream():
     nv.nvfp4_add_rmsnorm(x, w, 1e-5, residual=r, y=y2, stream=s)
     s.synchronize()
     assert torch.equal(y, y2)
+
+
+# rows that start on any element, enough of them to run through shared memory in 16-byte
+# units at each team width, with a last few bytes that fill no unit
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,cols", [(50003, 25), (40009, 511), (20011, 513), (9001, 1001),
+                                       (9003, 2047), (5003, 2049), (5003, 4097), (4001, 5001),
+                                       (2003, 6145), (1501, 9001), (1301, 12002)])
+def test_many_unaligned_rows(rows, cols, dtype):
+    test_norm_and_sum(rows, cols, dtype)
+    test_backward(rows, cols, dtype)
+    if cols < 3000:
+        test_fp8_output(rows, cols, dtype, 128)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_many_unaligned_rows_in_place(dtype):
+    """h may be the residual, and dx may be dy: the units around a row's group hold its
+    neighbours' elements, which may have been replaced by then."""
+    x, r, w = _inputs(9001, 1001, dtype, 3)
+    h, y = torch.empty_like(x), torch.empty_like(x)
+    rstd = torch.empty(9001, device=DEV)
+    nv.nvfp4_add_rmsnorm(x, w, 1e-6, residual=r, h=h, y=y, rstd=rstd)
+    r2, y2 = r.clone(), torch.empty_like(x)
+    nv.nvfp4_add_rmsnorm(x, w, 1e-6, residual=r2, h=r2, y=y2, rstd=rstd)
+    assert torch.equal(r2, h) and torch.equal(y2, y)
+    dx, dw = torch.empty_like(x), torch.empty(1001, device=DEV)
+    nv.nvfp4_add_rmsnorm_backward(x, h, w, rstd, dx, dh=r, dweight=dw)
+    dy, dw2 = x.clone(), torch.empty(1001, device=DEV)
+    nv.nvfp4_add_rmsnorm_backward(dy, h, w, rstd, dy, dh=r, dweight=dw2)
+    assert torch.equal(dy, dx) and torch.equal(dw2, dw)
