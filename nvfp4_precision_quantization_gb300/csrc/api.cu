@@ -159,7 +159,8 @@ nvfp4_status quantize_impl(const void* x, int32_t in_dtype, int64_t rows, int64_
                            const nvfp4_config* cfg, const nvfp4_out* row, const nvfp4_out* col,
                            const float* noop, cudaStream_t stream,
                            const int64_t* group_ends = nullptr, int num_groups = 0,
-                           bool rht = false, uint32_t rht_mask = 0) {
+                           bool rht = false, uint32_t rht_mask = 0,
+                           bool follows_launch = false) {
   nvfp4_status st;
   if (!valid_in_dtype(in_dtype)) return fail(NVFP4_ERR_INVALID, "unknown in_dtype");
   if ((st = check_sizes(rows, cols)) != NVFP4_OK) return st;
@@ -252,6 +253,7 @@ nvfp4_status quantize_impl(const void* x, int32_t in_dtype, int64_t rows, int64_
   }
   cudaError_t e;
   prep.noop = noop;
+  q.follows_launch = follows_launch || nz + nc > 0;
   if (nz + nc > 0) {
     if (group_ends) {
       // grouped calls: the prep step must also refuse invalid group ends
@@ -560,6 +562,7 @@ nvfp4_status nvfp4_quantize_both_rht(const void* x, int32_t in_dtype, int64_t ro
   q.noop = noop;
   q.rht = true;
   q.rht_mask = sign_mask;
+  q.follows_launch = nz + nc > 0;
   q.row_codes = row->codes;
   q.row_scales = row->scales;
   q.row_amax = row->amax;
@@ -892,7 +895,7 @@ nvfp4_status nvfp4_grouped_quantize_rowwise(const void* x, int32_t in_dtype, int
   nvfp4_out r = *row;
   r.amax_in = row->amax;  // the expanded per-row amax is already in place
   return quantize_impl(x, in_dtype, rows, cols, &rcfg, &r, nullptr, noop, stream, group_ends,
-                       num_groups);
+                       num_groups, false, 0, true);
 }
 
 nvfp4_status nvfp4_grouped_quantize_rowwise_padded(
@@ -985,6 +988,7 @@ nvfp4_status nvfp4_grouped_quantize_rowwise_padded(
   q.pad_ends = padded_ends;
   q.rag_ends = ragged_ends;
   q.in_rows = tokens;
+  q.follows_launch = true;
   if ((e = launch_quantize(q, dev, stream)) != cudaSuccess) return cuda_fail(e, "quantize");
   return NVFP4_OK;
 }
@@ -1092,6 +1096,7 @@ nvfp4_status grouped_columnwise_impl(const void* x, int32_t in_dtype, int64_t ro
   q.col_grouped_per_tensor = !rs;
   q.rht = rht;
   q.rht_mask = sign_mask;
+  q.follows_launch = true;
   if ((e = launch_quantize(q, dev, stream)) != cudaSuccess) return cuda_fail(e, "quantize");
   return NVFP4_OK;
 }

@@ -140,6 +140,10 @@ struct QuantArgs {
   // walk each CTA's tiles the other way (a second pass over x then starts on the tiles
   // that the first one read last, still in L2)
   bool reverse_walk;
+  // a launch of the same call precedes this one.  Only then may the encode start while
+  // that launch still runs: it loads x before it waits, and whatever wrote x is complete
+  // by then, because the first launch of a call waits for the stream.
+  bool follows_launch;
 };
 cudaError_t launch_quantize(const QuantArgs& a, const DeviceInfo& dev, cudaStream_t stream);
 

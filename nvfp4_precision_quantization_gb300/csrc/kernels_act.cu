@@ -151,7 +151,10 @@ __global__ void __launch_bounds__(kActThreads, STAGED ? 2 : 3)
   constexpr int kCols = S::kCols, kStrip = 32 * kCols;
   __shared__ float s_sum[kStrip], s_max[kStrip];
   __shared__ __align__(16) uint8_t stages[STAGED ? kActWarps : 1][kStageBytes];
-  pdl_launch_dependents();  // the join may be set up meanwhile
+  // the join may be set up meanwhile; without one, the next launch in the stream is another
+  // call's, which may count on this one's dz
+  if (a.col_sum != nullptr || a.col_max != nullptr || a.row_max != nullptr)
+    pdl_launch_dependents();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int strip = blockIdx.x % a.strips, part = blockIdx.x / a.strips;
   const int sub = lane / a.lanes, step = 32 / a.lanes;  // rows side by side in the warp

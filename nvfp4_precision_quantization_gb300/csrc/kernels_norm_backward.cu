@@ -121,7 +121,9 @@ __device__ __forceinline__ void backward_partials(const NormBackwardKernelArgs& 
 template <bool BF16, int TPR, int NCH, bool STAGED>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
     k_add_rmsnorm_backward(const NormBackwardKernelArgs a) {
-  pdl_launch_dependents();  // the columns' sum may be set up meanwhile
+  // the columns' sum may be set up meanwhile; without one, the next launch in the stream is
+  // another call's, which may count on this one's dx
+  if (a.part != nullptr) pdl_launch_dependents();
   constexpr int kThreads = TPR < 256 ? 256 : TPR;
   constexpr int kTeams = kThreads / TPR;
   __shared__ float2 red[2][kThreads / 32];
@@ -172,7 +174,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
 template <bool BF16, int TPR, int NCH, bool ANY>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
     k_add_rmsnorm_backward_ring(const NormBackwardKernelArgs a, const RingArgs g) {
-  pdl_launch_dependents();  // the columns' sum may be set up meanwhile
+  if (a.part != nullptr) pdl_launch_dependents();  // as above
   constexpr int kThreads = TPR < 256 ? 256 : TPR;
   constexpr int kTeams = kThreads / TPR;
   constexpr int kElem = BF16 ? 2 : 4;

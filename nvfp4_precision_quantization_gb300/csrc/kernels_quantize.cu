@@ -1439,6 +1439,7 @@ cudaError_t launch_quantize(const QuantArgs& q, const DeviceInfo& dev, cudaStrea
     qc.row_codes = nullptr;
     qc.copy_dst = nullptr;
     qc.reverse_walk = !q.reverse_walk;
+    qc.follows_launch = true;
     const cudaError_t e = launch_quantize(qr, dev, stream);
     return e != cudaSuccess ? e : launch_quantize(qc, dev, stream);
   }
@@ -1565,7 +1566,7 @@ cudaError_t launch_quantize(const QuantArgs& q, const DeviceInfo& dev, cudaStrea
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = q.follows_launch ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, fn, map, map_rc, map_cc, a);
 }
 
