@@ -14,6 +14,7 @@ import ctypes as C
 import os
 import platform
 from array import array
+from contextlib import nullcontext
 from dataclasses import dataclass
 from itertools import chain
 from typing import Optional
@@ -200,6 +201,17 @@ def _stream(stream) -> Optional[int]:
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _workspace(workspace: Optional[torch.Tensor], need: int, device, stream):
+    """The workspace and its bytes; without one, `need` bytes that belong to the stream the
+    kernels run on, so that torch gives them to nobody else before those are done."""
+    if workspace is None:
+        if isinstance(stream, int):  # 1 is the legacy default stream, torch's 0
+            stream = torch.cuda.ExternalStream(stream if stream != 1 else 0)
+        with nullcontext() if stream is None else torch.cuda.stream(stream):
+            workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
+    return workspace, workspace.numel() * workspace.element_size()
 
 
 def _check(status: int):
@@ -436,11 +448,10 @@ def nvfp4_gemm(a: Operand, b: Operand, d: torch.Tensor, workspace: Optional[torc
     if a.codes.shape[0] != m or b.codes.shape[0] != n or b.codes.shape[1] * 2 != k:
         raise ValueError("operand shapes do not match d")
     need = nvfp4_gemm_workspace_size(m, n, k)
-    if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=d.device)
+    workspace, size = _workspace(workspace, need, d.device, stream)
     ca, cb = a._c(), b._c()
     _check(load_library().nvfp4_gemm(C.byref(ca), C.byref(cb), m, n, k, _ptr(d), od,
-                                      _ptr(workspace), workspace.numel(), _stream(stream)))
+                                      _ptr(workspace), size, _stream(stream)))
 
 
 def nvfp4_grouped_gemm_workspace_size(rows: int, n: int, k: int, num_groups: int) -> int:
@@ -467,12 +478,11 @@ def nvfp4_grouped_gemm(a: Operand, b: Operand, group_ends: torch.Tensor, d: torc
     if a.codes.shape[0] != rows or b.codes.shape[0] != groups * n or b.codes.shape[1] * 2 != k:
         raise ValueError("operand shapes do not match d and the group count")
     need = nvfp4_grouped_gemm_workspace_size(rows, n, k, groups)
-    if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=d.device)
+    workspace, size = _workspace(workspace, need, d.device, stream)
     ca, cb = a._c(), b._c()
     _check(load_library().nvfp4_grouped_gemm(C.byref(ca), C.byref(cb), _ptr(group_ends), groups,
                                               rows, n, k, _ptr(d), od, _ptr(workspace),
-                                              workspace.numel(), _stream(stream)))
+                                              size, _stream(stream)))
 
 
 def nvfp4_grouped_gemm_wgrad(a: Operand, b: Operand, group_ends: torch.Tensor, d: torch.Tensor,
@@ -493,12 +503,11 @@ def nvfp4_grouped_gemm_wgrad(a: Operand, b: Operand, group_ends: torch.Tensor, d
             or b.codes.shape[1] * 2 != tokens):
         raise ValueError("operand shapes do not match d and the group count")
     need = nvfp4_gemm_workspace_size(m, n, tokens)
-    if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=d.device)
+    workspace, size = _workspace(workspace, need, d.device, stream)
     ca, cb = a._c(), b._c()
     _check(load_library().nvfp4_grouped_gemm_wgrad(C.byref(ca), C.byref(cb), _ptr(group_ends),
                                                     groups, m, n, tokens, _ptr(d), od,
-                                                    _ptr(workspace), workspace.numel(),
+                                                    _ptr(workspace), size,
                                                     _stream(stream)))
 
 
@@ -574,12 +583,6 @@ def _vector(name: str, t: torch.Tensor, n: int) -> int:
     return _in_dtype(t)
 
 
-def _workspace(workspace: Optional[torch.Tensor], need: int, device):
-    if workspace is None:
-        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
-    return workspace, workspace.numel() * workspace.element_size()
-
-
 def nvfp4_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float,
                       residual: Optional[torch.Tensor] = None,
                       h: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
@@ -635,7 +638,7 @@ def nvfp4_add_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.
     if dweight is not None:
         need = 0 if workspace is not None else \
             nvfp4_add_rmsnorm_backward_workspace_size(rows, cols)
-        workspace, size = _workspace(workspace, need, h.device)
+        workspace, size = _workspace(workspace, need, h.device, stream)
     _check(load_library().nvfp4_add_rmsnorm_backward(
         _like("dy", dy, shape, dtype), h.data_ptr(), _like("dh", dh, shape, dtype), _in_dtype(h),
         weight.data_ptr(), _vector("weight", weight, cols), _floats("rstd", rstd, rows), rows,
@@ -666,7 +669,7 @@ def nvfp4_gemm_bias_act(a: Operand, b: Operand, d: torch.Tensor,
     shape, dtype = d.shape, d.dtype
     bd = _vector("bias", bias, n) if bias is not None else NVFP4_IN_FP32
     need = 0 if workspace is not None else nvfp4_gemm_bias_act_workspace_size(m, n, k)
-    workspace, size = _workspace(workspace, need, d.device)
+    workspace, size = _workspace(workspace, need, d.device, stream)
     ca, cb = a._c(), b._c()
     epi = _CEpilogue(_ptr(bias), bd, act, _like("residual", residual, shape, dtype),
                      _like("z", z, shape, dtype))
@@ -693,7 +696,7 @@ def nvfp4_bias_act_backward(dd: torch.Tensor, z: Optional[torch.Tensor], act: in
     size = 0
     if dbias is not None or row_amax is not None or col_amax is not None:
         need = 0 if workspace is not None else nvfp4_bias_act_backward_workspace_size(rows, cols)
-        workspace, size = _workspace(workspace, need, dd.device)
+        workspace, size = _workspace(workspace, need, dd.device, stream)
     _check(load_library().nvfp4_bias_act_backward(
         dd.data_ptr(), _like("z", z, shape, dtype), _in_dtype(dd), act, rows, cols,
         _like("dz", dz, shape, dtype), _floats("dbias", dbias, cols),
@@ -732,7 +735,7 @@ def nvfp4_grad_norm(tensors, norm: torch.Tensor, workspace: Optional[torch.Tenso
     """norm [1] (float32) = the 2-norm of all tensors (bfloat16 or float32) together."""
     _floats("norm", norm, 1)
     need = 0 if workspace is not None else nvfp4_clip_grad_norm_workspace_size()
-    workspace, size = _workspace(workspace, need, norm.device)
+    workspace, size = _workspace(workspace, need, norm.device, stream)
     items = _tensor_list(tensors, None)
     _check(load_library().nvfp4_grad_norm(items.buffer_info()[0], len(tensors), _ptr(norm),
                                           _ptr(workspace), size,
@@ -747,7 +750,7 @@ def nvfp4_clip_grad_norm(tensors, max_norm: float, norm: torch.Tensor, out=None,
     if out is not None and len(out) != len(tensors):
         raise ValueError("out must have one tensor for each tensor")
     need = 0 if workspace is not None else nvfp4_clip_grad_norm_workspace_size()
-    workspace, size = _workspace(workspace, need, norm.device)
+    workspace, size = _workspace(workspace, need, norm.device, stream)
     items = _tensor_list(tensors, out)
     _check(load_library().nvfp4_clip_grad_norm(items.buffer_info()[0], len(tensors), max_norm,
                                                _ptr(norm), _ptr(workspace), size,
