@@ -176,13 +176,15 @@ cudaError_t allow_ring(K kernel, const RingKernel& k) {  // on the current devic
 }
 
 // CTAs per SM and the ring of each: as many CTAs as the registers allow while each keeps
-// at least two stages.  ctas == 0: two stages do not fit.
+// at least two stages.  ctas == 0: two stages do not fit, or there is nothing to hold (rows
+// without columns).
 struct RingPlan {
   int ctas;
   RingArgs g;
 };
 RingPlan plan_ring(const RingKernel& k, int tensors, int64_t group_bytes, bool any = false) {
   RingPlan p{};
+  if (group_bytes <= 0) return p;
   // any: up to 30 bytes of the units around the rows, and a lane's reads past a row's end
   const int64_t tensor = (group_bytes + (any ? 128 : 0) + 127) / 128 * 128, stage = tensors * tensor;
   for (int c = k.resident; c > 0; --c) {

@@ -319,3 +319,32 @@ def test_many_unaligned_rows_in_place(dtype):
     dy, dw2 = x.clone(), torch.empty(1001, device=DEV)
     nv.nvfp4_add_rmsnorm_backward(dy, h, w, rstd, dy, dh=r, dweight=dw2)
     assert torch.equal(dy, dx) and torch.equal(dw2, dw)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows", [3, 40000])
+def test_rows_without_columns(rows, dtype):
+    """Nothing to sum: rstd is 1/sqrt(eps), scales are 1, the amax is 0."""
+    x, w = torch.empty(rows, 0, dtype=dtype, device=DEV), torch.empty(0, dtype=dtype, device=DEV)
+    r, h, y = torch.empty_like(x), torch.empty_like(x), torch.empty_like(x)
+    rstd, ok_r = guarded((rows,), torch.float32)
+    for block in (0, 128):
+        scale, ok = guarded((rows, 0 if block else 1), torch.float32)
+        codes = torch.empty(rows, 0, dtype=torch.uint8, device=DEV)
+        rstd.zero_()
+        nv.nvfp4_add_rmsnorm(x, w, 0.25, residual=r, h=h, y=y, rstd=rstd,
+                             fp8=nv.Fp8Out(codes, scale, block))
+        torch.cuda.synchronize()
+        assert bool((rstd == 2.0).all()) and bool((scale == 1.0).all())
+        ok()
+    amax, ok = guarded((rows,), torch.float32)
+    none = torch.empty(rows, 0, dtype=torch.uint8, device=DEV)
+    nv.nvfp4_add_rmsnorm(x, w, 0.25, row=nv.Out(none, none, amax),
+                         cfg=nv.Config(nv.NVFP4_ROW_SCALED, 448.0, 0, 0))
+    torch.cuda.synchronize()
+    assert bool((amax == 0.0).all())
+    ok()
+    ok_r()
+    # and back: no dx, no dweight
+    nv.nvfp4_add_rmsnorm_backward(y, h, w, rstd, x, dweight=torch.empty(0, device=DEV))
+    torch.cuda.synchronize()
