@@ -599,7 +599,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(acc_empty);  // TMEM may take the next tile's MMAs
-      if (!ready || *(volatile int*)err) break;
+      // the warp leaves together: what follows (shuffles, the next tile's TMEM loads) takes
+      // every lane, and each lane's wait gives up by its own clock
+      if (__any_sync(0xffffffffu, !ready || *(volatile int*)err)) break;
       if (job.kt1 == job.kt0) {  // an empty K range (an empty group): the sum is 0
 #pragma unroll
         for (int i = 0; i < kEpiCols; ++i) v[i] = 0u;
