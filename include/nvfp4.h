@@ -465,7 +465,7 @@ typedef struct {
  *   Outputs of y (at least one of y, fp8, row must be given unless x is empty):
  *   y    in in_dtype (it may be x or residual itself where h is not the same buffer);
  *   fp8  E4M3 with a scale per row or per 128 columns: scale = amax / 448 (at least
- *        2^-126; 1 where amax is 0), code = E4M3(y * (448 / amax));
+ *        2^-126; 1 where amax is 0), code = E4M3(y / scale);
  *   row  the rowwise NVFP4 output that nvfp4_quantize_rowwise defines, of the FP32 y,
  *        with cfg: 1x16 blocks, NVFP4_ROW_SCALED (each row's own amax, found in the same
  *        pass, or row->amax_in), or NVFP4_PER_TENSOR with row->amax_in (the amax of

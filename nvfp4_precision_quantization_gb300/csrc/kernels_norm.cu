@@ -47,10 +47,26 @@ struct NormKernelArgs {
 
 constexpr float kE4m3Max = 448.0f;
 
-// Encode scale of an E4M3 output whose largest magnitude is a.
-__device__ __forceinline__ float fp8_encode_scale(float a) { return global_scale(a, kE4m3Max); }
-__device__ __forceinline__ float fp8_decode_scale(float a) {
+// The scale of an E4M3 output whose largest magnitude is a.
+__device__ __forceinline__ float fp8_scale(float a) {
   return a == 0.0f ? 1.0f : fmaxf(__fdiv_rn(a, kE4m3Max), 0x1p-126f);
+}
+// Quotients by such a scale: the codes are those of y / scale, whatever the scale's rounding
+// and its lower bound make of it (codes of y * (448 / a) decoded to up to four times y for a
+// below 448 * 2^-126, and lay up to three roundings from the quotient otherwise).
+// q = y r with r = 1 / scale, and one Newton step on the residual y - q scale, which an FMA
+// gives exactly (Markstein, "Computation of elementary functions on the IBM RISC System/6000
+// processor", 1990): 16 divisions would cost five times the instructions.
+struct Fp8Divisor {
+  float r, scale;  // (an infinite scale: 0, so that the step adds nothing to 0)
+};
+__device__ __forceinline__ Fp8Divisor fp8_divisor(float scale) {
+  return {__frcp_rn(scale), isinf(scale) ? 0.0f : scale};
+}
+__device__ __forceinline__ Pair fp8_quotient(Pair y, const Fp8Divisor& d) {
+  const Pair q = pair_mul(y, {d.r, d.r});
+  const Pair rest = pair_fma({-q.x, -q.y}, {d.scale, d.scale}, y);
+  return pair_fma(rest, {d.r, d.r}, q);
 }
 
 // What a thread does with its part of a row once h is in v: h out, then h w with the sum
@@ -142,32 +158,31 @@ __device__ __forceinline__ void norm_emit(const NormKernelArgs& a, int64_t row, 
       if (n > 0) a.scales[row * spitch + col / 16] = (uint8_t)s8;
     }
   } else if (a.q8 != nullptr) {
-    if (live && t == 0 && !a.q8_blocks) a.q8_scale[row] = fp8_decode_scale(top);
-    const float S_row = fp8_encode_scale(top);
+    const float s_row = fp8_scale(top);
+    if (live && t == 0 && !a.q8_blocks) a.q8_scale[row] = s_row;
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
       const int col = (c * TPR + t) * kChunk;
       const int n = live ? chunk_len(col, a.cols) : 0;
-      float S = S_row;
+      float scale = s_row;
       if (a.q8_blocks) {  // 128 columns are eight neighbouring lanes
         float b = bmax[c];
 #pragma unroll
         for (int d = 4; d > 0; d >>= 1) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, d));
         b = __fmul_rn(b, s);
-        S = fp8_encode_scale(b);
+        scale = fp8_scale(b);
         if (n > 0 && (t & 7) == 0)
-          a.q8_scale[row * ((a.cols + 127) / 128) + col / 128] = fp8_decode_scale(b);
+          a.q8_scale[row * ((a.cols + 127) / 128) + col / 128] = scale;
       }
+      const Fp8Divisor d = fp8_divisor(scale);
       uint32_t cw[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
+        const Pair a01 = fp8_quotient({v[c][4 * i], v[c][4 * i + 1]}, d);
+        const Pair a23 = fp8_quotient({v[c][4 * i + 2], v[c][4 * i + 3]}, d);
         uint16_t lo, hi;
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
-            : "=h"(lo)
-            : "f"(__fmul_rn(v[c][4 * i + 1], S)), "f"(__fmul_rn(v[c][4 * i], S)));
-        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;"
-            : "=h"(hi)
-            : "f"(__fmul_rn(v[c][4 * i + 3], S)), "f"(__fmul_rn(v[c][4 * i + 2], S)));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(a01.y), "f"(a01.x));
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(a23.y), "f"(a23.x));
         cw[i] = (uint32_t)lo | ((uint32_t)hi << 16);
       }
       if (!STAGED || a.g_q8 >= 4) {

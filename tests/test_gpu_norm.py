@@ -348,3 +348,45 @@ def test_rows_without_columns(rows, dtype):
     # and back: no dx, no dweight
     nv.nvfp4_add_rmsnorm_backward(y, h, w, rstd, x, dweight=torch.empty(0, device=DEV))
     torch.cuda.synchronize()
+
+
+def _fp8(x, w, r, block):
+    """The FP32 y of a norm with its E4M3 codes and scale, from one call."""
+    rows, cols = x.shape
+    y = torch.empty_like(x)
+    codes = torch.empty(rows, cols, dtype=torch.uint8, device=DEV)
+    scale = torch.empty(rows, -(-cols // 128) if block else 1, device=DEV)
+    nv.nvfp4_add_rmsnorm(x, w, 1e-6, residual=r, y=y, fp8=nv.Fp8Out(codes, scale, block))
+    torch.cuda.synchronize()
+    each = scale.repeat_interleave(128 if block else cols, dim=1)[:, :cols]
+    return y, codes.view(torch.float8_e4m3fn), each
+
+
+@pytest.mark.parametrize("block", [0, 128])
+@pytest.mark.parametrize("rows,cols", [(3000, 4096), (2001, 4001), (4, 512)])
+def test_fp8_codes_are_those_of_the_quotient(rows, cols, block):
+    """code = E4M3(y / scale) with the stored scale: every code of the FP32 quotient."""
+    x, r, w = _inputs(rows, cols, torch.float32, 13)
+    y, codes, scale = _fp8(x, w, r, block)
+    want = (y / scale).clamp(-448.0, 448.0).to(torch.float8_e4m3fn)
+    assert torch.equal(codes.float(), want.float())
+
+
+@pytest.mark.parametrize("block", [0, 128])
+def test_fp8_of_tiny_values(block):
+    """A row whose maximum lies below 448 * 2^-126, and blocks of such values in ordinary
+    rows (weights of 1e-36): the scale stops at 2^-126, and code * scale is y within half a
+    step of E4M3 all the same."""
+    w = torch.ones(1024, device=DEV)
+    w[128:256] = 1e-36
+    w[512:640] = 3e-38
+    x, _, _ = _inputs(6, 1024, torch.float32, 4)
+    x[2] = x[2] / x[2].abs().max() * 1e-39  # y: about 1e-36
+    x[4] = x[4] / x[4].abs().max() * 5e-39
+    y, codes, scale = _fp8(x, w, None, block)
+    assert float(scale[2].min()) >= 2.0 ** -126
+    v, s, want = codes.double() * scale.double(), scale.double(), y.double()
+    assert bool(((v - want).abs() <= 2.0 ** -4 * want.abs() + 2.0 ** -10 * s).all())
+    # the largest is not lost: its code times the scale is within half a step of it
+    top = want[2].abs().max()
+    assert top > 0 and abs(v[2].abs().max() - top) <= 2.0 ** -4 * top
