@@ -47,6 +47,12 @@ struct NormKernelArgs {
 
 constexpr float kE4m3Max = 448.0f;
 
+// The maximum of |h w| s over values of |h w| up to m, NaN skipped: 0 where the product is one
+// (m infinite and s = 0, a row whose only value other than 0 is NaN; m = 0 and s infinite).
+__device__ __forceinline__ float amax_times(float m, float s) {
+  return fmaxf(__fmul_rn(m, s), 0.0f);
+}
+
 // The scale of an E4M3 output whose largest magnitude is a.
 __device__ __forceinline__ float fp8_scale(float a) {
   return a == 0.0f ? 1.0f : fmaxf(__fdiv_rn(a, kE4m3Max), 0x1p-126f);
@@ -111,7 +117,7 @@ __device__ __forceinline__ void norm_emit(const NormKernelArgs& a, int64_t row, 
   const int64_t base = row * a.cols;
   const float mean = a.cols > 0 ? __fdiv_rn(r.x, (float)a.cols) : 0.0f;
   const float s = __frsqrt_rn(__fadd_rn(mean, a.eps));
-  const float top = __fmul_rn(r.y, s);  // amax of the row's y
+  const float top = amax_times(r.y, s);  // amax of the row's y
   if (live && t == 0 && a.rstd != nullptr) a.rstd[row] = s;
 #pragma unroll
   for (int c = 0; c < NCH; ++c)
@@ -139,7 +145,7 @@ __device__ __forceinline__ void norm_emit(const NormKernelArgs& a, int64_t row, 
     for (int c = 0; c < NCH; ++c) {
       const int col = (c * TPR + t) * kChunk;
       const int n = live ? chunk_len(col, a.cols) : 0;
-      const float b = __fmul_rn(bmax[c], s);
+      const float b = amax_times(bmax[c], s);
       uint32_t cw[2] = {0, 0};
       uint32_t s8 = 0;
       if (n == 0) {  // nothing of the row
@@ -169,7 +175,7 @@ __device__ __forceinline__ void norm_emit(const NormKernelArgs& a, int64_t row, 
         float b = bmax[c];
 #pragma unroll
         for (int d = 4; d > 0; d >>= 1) b = fmaxf(b, __shfl_xor_sync(0xffffffffu, b, d));
-        b = __fmul_rn(b, s);
+        b = amax_times(b, s);
         scale = fp8_scale(b);
         if (n > 0 && (t & 7) == 0)
           a.q8_scale[row * ((a.cols + 127) / 128) + col / 128] = scale;

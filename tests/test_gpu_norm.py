@@ -390,3 +390,29 @@ def test_fp8_of_tiny_values(block):
     # the largest is not lost: its code times the scale is within half a step of it
     top = want[2].abs().max()
     assert top > 0 and abs(v[2].abs().max() - top) <= 2.0 ** -4 * top
+
+
+def test_maxima_skip_nan():
+    """A row with an infinity has rstd 0, so its other values are 0 and that one is NaN; rows of
+    zeros with eps = 0 have an infinite rstd and are NaN throughout.  The maxima skip NaN:
+    they are 0 and the scales 1, and the rows between are as they were."""
+    x = torch.ones(4, 256, device=DEV)
+    x[0, 200], x[2] = float("inf"), 0.0
+    w = torch.full((256,), 2.0, device=DEV)
+    for block in (0, 128):
+        codes = torch.empty(4, 256, dtype=torch.uint8, device=DEV)
+        scale = torch.empty(4, 2 if block else 1, device=DEV)
+        y = torch.empty_like(x)
+        nv.nvfp4_add_rmsnorm(x, w, 0.0, y=y, fp8=nv.Fp8Out(codes, scale, block))
+        torch.cuda.synchronize()
+        assert bool(y[0, 200].isnan()) and bool(y[2].isnan().all())
+        assert float(y[0, :200].abs().max()) == 0.0
+        assert bool((scale[0] == 1.0).all()) and bool((scale[2] == 1.0).all())
+        for i in (1, 3):
+            v = codes[i].view(torch.float8_e4m3fn).float() * scale[i].repeat_interleave(
+                256 // scale.shape[1])
+            assert bool(((v - y[i]).abs() <= 2.0 ** -4 * y[i].abs()).all())
+    o = nv.alloc_out(4, 256, 4)
+    nv.nvfp4_add_rmsnorm(x, w, 0.0, row=o, cfg=nv.Config(nv.NVFP4_ROW_SCALED, 448.0, 0, 0))
+    torch.cuda.synchronize()
+    assert float(o.amax[0]) == 0.0 and float(o.amax[2]) == 0.0 and float(o.amax[1]) > 0.0
