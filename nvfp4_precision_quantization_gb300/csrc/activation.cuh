@@ -15,22 +15,6 @@ enum : int { kActNone = 0, kActRelu = 1, kActGelu = 2, kActSilu = 3 };
 constexpr float kGelu2C = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kGeluA = 0.044715f;
 
-__device__ __forceinline__ float sigmoid_fast(float x) {
-  return __fdividef(1.0f, __fadd_rn(1.0f, __expf(-x)));
-}
-
-template <int ACT>
-__device__ __forceinline__ float act_value(float z) {
-  if constexpr (ACT == kActRelu) return z < 0.0f ? 0.0f : z;  // NaN stays
-  if constexpr (ACT == kActGelu) {
-    const float z2 = __fmul_rn(z, z);
-    const float u2 = __fmul_rn(z, __fmaf_rn(kGelu2C * kGeluA, z2, kGelu2C));
-    return __fmul_rn(z, sigmoid_fast(u2));
-  }
-  if constexpr (ACT == kActSilu) return __fmul_rn(z, sigmoid_fast(z));
-  return z;
-}
-
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -95,8 +79,10 @@ __device__ __forceinline__ Pair act_value(Pair z) {
     }
     const Pair t = pair_add({ex2_approx(-w.x), ex2_approx(-w.y)}, {1.0f, 1.0f});
     return pair_mul(z, {rcp_approx(t.x), rcp_approx(t.y)});
+  } else if constexpr (ACT == kActRelu) {
+    return {z.x < 0.0f ? 0.0f : z.x, z.y < 0.0f ? 0.0f : z.y};  // NaN stays
   } else {
-    return {act_value<ACT>(z.x), act_value<ACT>(z.y)};
+    return z;
   }
 }
 

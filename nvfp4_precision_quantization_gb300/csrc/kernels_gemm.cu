@@ -712,25 +712,31 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// d = act(bias) + residual: the epilogue of an empty sum (k == 0).
+// d = act(bias) + residual: the epilogue of an empty sum (k == 0), two elements at a time
+// because the activations' one form is of pairs.
 __global__ void __launch_bounds__(256) k_epilogue_only(const Epilogue e, void* d, bool bf16,
                                                        int64_t m, int n) {
-  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < m * n;
-       i += (int64_t)gridDim.x * 256) {
-    float v = e.bias_at((int)(i % n));
-    if (e.z != nullptr) {
-      if (bf16) static_cast<__nv_bfloat16*>(e.z)[i] = __float2bfloat16_rn(v);
-      else static_cast<float*>(e.z)[i] = v;
+  const int64_t total = m * n;
+  auto put = [&](void* base, int64_t i, float v) {
+    if (bf16) static_cast<__nv_bfloat16*>(base)[i] = __float2bfloat16_rn(v);
+    else static_cast<float*>(base)[i] = v;
+  };
+  for (int64_t i = 2 * ((int64_t)blockIdx.x * 256 + threadIdx.x); i < total;
+       i += 2 * (int64_t)gridDim.x * 256) {
+    const int count = i + 1 < total ? 2 : 1;
+    float v[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j) v[j] = j < count ? e.bias_at((int)((i + j) % n)) : 0.0f;
+    if (e.z != nullptr)
+      for (int j = 0; j < count; ++j) put(e.z, i + j, v[j]);
+    apply_act<2>(e.act, v);
+    for (int j = 0; j < count; ++j) {
+      float r = 0.0f;
+      if (e.residual != nullptr)
+        r = bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(e.residual)[i + j])
+                 : static_cast<const float*>(e.residual)[i + j];
+      put(d, i + j, e.residual != nullptr ? __fadd_rn(v[j], r) : v[j]);
     }
-    v = e.act == kActRelu   ? act_value<kActRelu>(v)
-        : e.act == kActGelu ? act_value<kActGelu>(v)
-        : e.act == kActSilu ? act_value<kActSilu>(v)
-                            : v;
-    if (e.residual != nullptr)
-      v = __fadd_rn(v, bf16 ? __bfloat162float(static_cast<const __nv_bfloat16*>(e.residual)[i])
-                            : static_cast<const float*>(e.residual)[i]);
-    if (bf16) static_cast<__nv_bfloat16*>(d)[i] = __float2bfloat16_rn(v);
-    else static_cast<float*>(d)[i] = v;
   }
 }
 
@@ -738,7 +744,7 @@ __global__ void __launch_bounds__(256) k_epilogue_only(const Epilogue e, void* d
 
 cudaError_t launch_epilogue_only(const Epilogue& e, void* d, bool bf16, int64_t m, int64_t n,
                                  const DeviceInfo& dev, cudaStream_t stream) {
-  const int64_t grid = std::min<int64_t>((m * n + 255) / 256, 8LL * dev.num_sms);
+  const int64_t grid = std::min<int64_t>((m * n + 511) / 512, 8LL * dev.num_sms);
   k_epilogue_only<<<(unsigned)grid, 256, 0, stream>>>(e, d, bf16, m, (int)n);
   return cudaGetLastError();
 }

@@ -265,3 +265,35 @@ def test_backward_in_place_unaligned_and_partial():
         zo2, do2 = at_offset(z, offset), at_offset(dd, offset)
         nv.nvfp4_bias_act_backward(do2, zo2, nv.NVFP4_ACT_SILU, zo2)
         assert torch.equal(zo2, dz)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("name", list(ACTS))
+@pytest.mark.parametrize("m,n", [(3, 41), (1, 1), (700, 513)])
+def test_empty_sum_of_every_activation(m, n, name, dtype):
+    """k == 0 against the definition, with the same evaluation as every other k: the values
+    of a product with all-zero codes, byte for byte."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(m + n)
+    bias = 6 * torch.randn(n, generator=g, device=DEV)
+    res = torch.randn(m, n, generator=g, device=DEV).to(dtype)
+
+    def zeros(lines, k):
+        return nv.Operand(torch.zeros(lines, k // 2, dtype=torch.uint8, device=DEV),
+                          torch.zeros(lines, k // 16, dtype=torch.uint8, device=DEV),
+                          torch.ones(lines, device=DEV), RS, 448.0)
+    out = []
+    for k in (0, 64):
+        d, ok_d = guarded((m, n), dtype)
+        z, ok_z = guarded((m, n), dtype)
+        nv.nvfp4_gemm_bias_act(zeros(m, k), zeros(n, k), d, bias=bias, act=ACTS[name],
+                               residual=res, z=z)
+        torch.cuda.synchronize()
+        ok_d()
+        ok_z()
+        out.append((d, z))
+    assert torch.equal(out[0][0], out[1][0]) and torch.equal(out[0][1], out[1][1])
+    zz = bias.double().expand(m, n)
+    want = act(zz, name) + res.double()
+    tol = 2.0 ** -20 * (1 + zz.abs()) + (2.0 ** -23 + half_ulp(dtype)) * 1.01 * want.abs()
+    assert bool(((out[0][0].double() - want).abs() <= tol).all())
