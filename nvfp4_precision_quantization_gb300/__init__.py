@@ -16,7 +16,6 @@ import platform
 from array import array
 from contextlib import nullcontext
 from dataclasses import dataclass
-from itertools import chain
 from typing import Optional
 
 import torch
@@ -577,6 +576,25 @@ def _floats(name: str, t: Optional[torch.Tensor], n: int) -> Optional[int]:
     return t.data_ptr()
 
 
+def _on_gpu(*tensors) -> None:
+    """Refuse a host tensor: the kernels would take its address for device memory."""
+    for t in tensors:
+        if t is not None and t.get_device() < 0:
+            raise ValueError(f"every tensor must be on the GPU, got one on {t.device}")
+
+
+def _operand_sizes(name: str, o: Operand, lines: int, k: int) -> None:
+    """The kernels read codes [lines][k/2], scales [lines][k/16] and one or `lines` amax."""
+    c, s, a = o.codes, o.scales, o.amax
+    if not c.is_contiguous() or s.numel() != lines * (k // 16) or not s.is_contiguous() or \
+            c.element_size() != 1 or s.element_size() != 1:
+        raise ValueError(f"{name}: codes [lines][k/2] and scales [lines][k/16] must be contiguous "
+                         "bytes")
+    if a.dtype is not torch.float32 or not a.is_contiguous() or \
+            a.numel() < (lines if o.mode == NVFP4_ROW_SCALED else 1):
+        raise ValueError(f"{name}.amax must be contiguous float32, one per line or one")
+
+
 def _vector(name: str, t: torch.Tensor, n: int) -> int:
     if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous with {n} elements")
@@ -595,12 +613,14 @@ def nvfp4_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float,
     rows, cols = _matrix(x)
     shape, dtype = x.shape, x.dtype
     cfp8 = crow = None
+    quantized = ()
     if fp8 is not None:
         if fp8.codes.shape != shape or not fp8.codes.is_contiguous() or \
                 fp8.codes.element_size() != 1:
             raise ValueError("fp8.codes must be a contiguous one-byte tensor of x's shape")
         scale = _floats("fp8.scale", fp8.scale, rows * (-(-cols // 128) if fp8.block else 1))
         cfp8 = C.byref(_CFp8Out(fp8.codes.data_ptr(), scale, fp8.block))
+        quantized = (fp8.codes, fp8.scale)
     if row is not None:
         if cfg is None:
             raise ValueError("a row output needs cfg")
@@ -612,11 +632,13 @@ def nvfp4_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float,
         _floats("row.amax", row.amax, lines)
         _floats("row.amax_in", row.amax_in, lines)
         crow = C.byref(row._c())
-    _check(load_library().nvfp4_add_rmsnorm(
-        x.data_ptr(), _like("residual", residual, shape, dtype), _in_dtype(x),
-        weight.data_ptr(), _vector("weight", weight, cols), rows, cols, eps,
-        _like("h", h, shape, dtype), _like("y", y, shape, dtype), _floats("rstd", rstd, rows),
-        cfp8, C.byref(cfg) if cfg is not None else None, crow, _stream(stream)))
+        quantized += (row.codes, row.scales, row.amax, row.amax_in)
+    args = (x.data_ptr(), _like("residual", residual, shape, dtype), _in_dtype(x),
+            weight.data_ptr(), _vector("weight", weight, cols), rows, cols, eps,
+            _like("h", h, shape, dtype), _like("y", y, shape, dtype), _floats("rstd", rstd, rows),
+            cfp8, C.byref(cfg) if cfg is not None else None, crow)
+    _on_gpu(x, weight, residual, h, y, rstd, *quantized)
+    _check(load_library().nvfp4_add_rmsnorm(*args, _stream(stream)))
 
 
 def nvfp4_add_rmsnorm_backward_workspace_size(rows: int, cols: int) -> int:
@@ -634,16 +656,18 @@ def nvfp4_add_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.
     beside the norm's, is added) and dweight [cols] float32."""
     rows, cols = _matrix(h)
     shape, dtype = h.shape, h.dtype
+    args = (_like("dy", dy, shape, dtype), h.data_ptr(), _like("dh", dh, shape, dtype),
+            _in_dtype(h), weight.data_ptr(), _vector("weight", weight, cols),
+            _floats("rstd", rstd, rows), rows, cols, _like("dx", dx, shape, dtype),
+            _floats("dweight", dweight, cols))
+    _on_gpu(dy, h, weight, rstd, dx, dweight, dh, workspace)
     size = 0
     if dweight is not None:
         need = 0 if workspace is not None else \
             nvfp4_add_rmsnorm_backward_workspace_size(rows, cols)
         workspace, size = _workspace(workspace, need, h.device, stream)
-    _check(load_library().nvfp4_add_rmsnorm_backward(
-        _like("dy", dy, shape, dtype), h.data_ptr(), _like("dh", dh, shape, dtype), _in_dtype(h),
-        weight.data_ptr(), _vector("weight", weight, cols), _floats("rstd", rstd, rows), rows,
-        cols, _like("dx", dx, shape, dtype), _floats("dweight", dweight, cols), _ptr(workspace),
-        size, _stream(stream)))
+    _check(load_library().nvfp4_add_rmsnorm_backward(*args, _ptr(workspace), size,
+                                                     _stream(stream)))
 
 
 def nvfp4_gemm_bias_act_workspace_size(m: int, n: int, k: int) -> int:
@@ -667,12 +691,15 @@ def nvfp4_gemm_bias_act(a: Operand, b: Operand, d: torch.Tensor,
     if a.codes.shape[0] != m or b.codes.shape[0] != n or b.codes.shape[1] * 2 != k:
         raise ValueError("operand shapes do not match d")
     shape, dtype = d.shape, d.dtype
+    _operand_sizes("a", a, m, k)
+    _operand_sizes("b", b, n, k)
     bd = _vector("bias", bias, n) if bias is not None else NVFP4_IN_FP32
+    epi = _CEpilogue(_ptr(bias), bd, act, _like("residual", residual, shape, dtype),
+                     _like("z", z, shape, dtype))
+    _on_gpu(a.codes, a.scales, a.amax, b.codes, b.scales, b.amax, d, bias, residual, z, workspace)
     need = 0 if workspace is not None else nvfp4_gemm_bias_act_workspace_size(m, n, k)
     workspace, size = _workspace(workspace, need, d.device, stream)
     ca, cb = a._c(), b._c()
-    epi = _CEpilogue(_ptr(bias), bd, act, _like("residual", residual, shape, dtype),
-                     _like("z", z, shape, dtype))
     _check(load_library().nvfp4_gemm_bias_act(C.byref(ca), C.byref(cb), m, n, k, C.byref(epi),
                                               _ptr(d), od, _ptr(workspace), size,
                                               _stream(stream)))
@@ -693,15 +720,15 @@ def nvfp4_bias_act_backward(dd: torch.Tensor, z: Optional[torch.Tensor], act: in
     the maxima of |dz|, ready to be the amax_in of the quantization of dz."""
     rows, cols = _matrix(dd)
     shape, dtype = dd.shape, dd.dtype
+    args = (dd.data_ptr(), _like("z", z, shape, dtype), _in_dtype(dd), act, rows, cols,
+            _like("dz", dz, shape, dtype), _floats("dbias", dbias, cols),
+            _floats("row_amax", row_amax, rows), _floats("col_amax", col_amax, cols))
+    _on_gpu(dd, z, dz, dbias, row_amax, col_amax, workspace)
     size = 0
     if dbias is not None or row_amax is not None or col_amax is not None:
         need = 0 if workspace is not None else nvfp4_bias_act_backward_workspace_size(rows, cols)
         workspace, size = _workspace(workspace, need, dd.device, stream)
-    _check(load_library().nvfp4_bias_act_backward(
-        dd.data_ptr(), _like("z", z, shape, dtype), _in_dtype(dd), act, rows, cols,
-        _like("dz", dz, shape, dtype), _floats("dbias", dbias, cols),
-        _floats("row_amax", row_amax, rows), _floats("col_amax", col_amax, cols),
-        _ptr(workspace), size, _stream(stream)))
+    _check(load_library().nvfp4_bias_act_backward(*args, _ptr(workspace), size, _stream(stream)))
 
 
 def nvfp4_clip_grad_norm_workspace_size() -> int:
@@ -727,16 +754,21 @@ def _tensor_list(tensors, out):
                 not all(map(T.is_contiguous, out)):
             raise ValueError("out must be contiguous tensors of the tensors' types and sizes")
         to = list(map(T.data_ptr, out))
-    return array("q", chain.from_iterable(zip(data, to, sizes, codes)))
+    if -1 in map(T.get_device, tensors) or out is not None and -1 in map(T.get_device, out):
+        _on_gpu(*tensors, *(out or ()))
+    words = [0] * (4 * len(data))
+    words[0::4], words[1::4], words[2::4], words[3::4] = data, to, sizes, codes
+    return array("q", words)
 
 
 def nvfp4_grad_norm(tensors, norm: torch.Tensor, workspace: Optional[torch.Tensor] = None,
                     stream=None) -> None:
     """norm [1] (float32) = the 2-norm of all tensors (bfloat16 or float32) together."""
     _floats("norm", norm, 1)
+    items = _tensor_list(tensors, None)
+    _on_gpu(norm, workspace)
     need = 0 if workspace is not None else nvfp4_clip_grad_norm_workspace_size()
     workspace, size = _workspace(workspace, need, norm.device, stream)
-    items = _tensor_list(tensors, None)
     _check(load_library().nvfp4_grad_norm(items.buffer_info()[0], len(tensors), _ptr(norm),
                                           _ptr(workspace), size,
                                           _stream(stream)))
@@ -749,9 +781,10 @@ def nvfp4_clip_grad_norm(tensors, max_norm: float, norm: torch.Tensor, out=None,
     _floats("norm", norm, 1)
     if out is not None and len(out) != len(tensors):
         raise ValueError("out must have one tensor for each tensor")
+    items = _tensor_list(tensors, out)
+    _on_gpu(norm, workspace)
     need = 0 if workspace is not None else nvfp4_clip_grad_norm_workspace_size()
     workspace, size = _workspace(workspace, need, norm.device, stream)
-    items = _tensor_list(tensors, out)
     _check(load_library().nvfp4_clip_grad_norm(items.buffer_info()[0], len(tensors), max_norm,
                                                _ptr(norm), _ptr(workspace), size,
                                                _stream(stream)))

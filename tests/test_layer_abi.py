@@ -170,3 +170,51 @@ def test_binding_refusals(lib):
         nv.nvfp4_gemm_bias_act(op, op, torch.zeros(4, 5))
     with pytest.raises(ValueError, match="bias"):
         nv.nvfp4_gemm_bias_act(op, op, torch.zeros(4, 4), bias=torch.zeros(5))
+
+
+def _on_host():
+    """Each layer operator with arguments that are right but for where they lie."""
+    x, w, f = torch.zeros(4, 64), torch.ones(64), torch.zeros(4)
+    op = nv.Operand(torch.zeros(4, 32, dtype=torch.uint8), torch.zeros(4, 4, dtype=torch.uint8),
+                    f, nv.NVFP4_ROW_SCALED, 448.0)
+    ws = torch.zeros(1 << 20, dtype=torch.uint8)
+    return {
+        "norm": lambda: nv.nvfp4_add_rmsnorm(x, w, 1e-5, y=x),
+        "norm codes": lambda: nv.nvfp4_add_rmsnorm(
+            x, w, 1e-5, fp8=nv.Fp8Out(torch.zeros(4, 64, dtype=torch.uint8), f)),
+        "norm rows": lambda: nv.nvfp4_add_rmsnorm(
+            x, w, 1e-5, row=nv.Out(op.codes, op.scales, f),
+            cfg=nv.Config(nv.NVFP4_ROW_SCALED, 448.0, 0, 0)),
+        "norm backward": lambda: nv.nvfp4_add_rmsnorm_backward(x, x, w, f, x, dweight=w),
+        "product": lambda: nv.nvfp4_gemm_bias_act(op, op, torch.zeros(4, 4), workspace=ws),
+        "activation backward": lambda: nv.nvfp4_bias_act_backward(x, x, 1, x, dbias=w),
+        "gradient norm": lambda: nv.nvfp4_grad_norm([w], torch.zeros(1), workspace=ws),
+        "clipping": lambda: nv.nvfp4_clip_grad_norm([w], 1.0, torch.zeros(1), out=[w.clone()],
+                                                    workspace=ws),
+    }
+
+
+@pytest.mark.parametrize("name", ["norm", "norm codes", "norm rows", "norm backward", "product",
+                                  "activation backward", "gradient norm", "clipping"])
+def test_host_tensors_are_refused(lib, name):
+    """Their addresses would reach the kernels as device memory."""
+    with pytest.raises(ValueError, match="on the GPU"):
+        _on_host()[name]()
+
+
+def test_operand_sizes_are_checked(lib):
+    """The kernels read codes [lines][k/2], scales [lines][k/16] and an amax per line."""
+    def op(codes=(8, 32), scales=(8, 4), amax=(8,), mode=nv.NVFP4_ROW_SCALED, dtype=torch.float32):
+        return nv.Operand(torch.zeros(codes, dtype=torch.uint8),
+                          torch.zeros(scales, dtype=torch.uint8), torch.zeros(amax, dtype=dtype),
+                          mode, 448.0)
+    good, d = op(), torch.zeros(8, 8)
+    wide = op(codes=(8, 64))
+    wide.codes = wide.codes[:, :32]  # rows further apart than the kernel steps
+    for bad in (op(scales=(8, 3)), op(scales=(4, 4)), op(amax=(7,)), op(dtype=torch.float64),
+                op(amax=(0,), mode=nv.NVFP4_PER_TENSOR), wide):
+        for pair, name in (((bad, good), "a"), ((good, bad), "b")):
+            with pytest.raises(ValueError, match=name):
+                nv.nvfp4_gemm_bias_act(*pair, d)
+    with pytest.raises(ValueError, match="on the GPU"):
+        nv.nvfp4_gemm_bias_act(good, op(amax=(1,), mode=nv.NVFP4_PER_TENSOR), d)

@@ -87,6 +87,7 @@ def test_allocated_on_the_given_stream(name, given, monkeypatch):
         allocated.append(current[-1])
         return empty(*args, **kw)
     monkeypatch.setattr(nv, "_lib", _Library())
+    monkeypatch.setattr(nv, "_on_gpu", lambda *tensors: None)
     monkeypatch.setattr(torch.cuda, "stream", selected)
     monkeypatch.setattr(torch.cuda, "ExternalStream", External)
     monkeypatch.setattr(torch, "empty", recorded)
