@@ -157,7 +157,7 @@ __device__ __forceinline__ void norm_emit(const NormKernelArgs& a, int64_t row, 
       if (!STAGED || a.g_codes >= 4) {
         if (n > 0) store_bytes(codes, cw, (n + 1) / 2);
       } else {
-        staged_store<2, 8>(reinterpret_cast<char*>(codes) - 8 * lane,
+        staged_store<2, 8, 1, 2>(reinterpret_cast<char*>(codes) - 8 * lane,
                            live ? ((int)warp_run(col - kChunk * lane, a.cols) + 1) / 2 : 0,
                            a.g_codes, stage, lane, cw);
       }
@@ -202,7 +202,8 @@ __device__ __forceinline__ void norm_emit(const NormKernelArgs& a, int64_t row, 
 }
 
 // Rows straight from memory into registers: few rows (each CTA has one or two, so there
-// is nothing to run ahead of), and (STAGED) rows that are not 16-byte aligned.
+// is nothing to run ahead of), and (STAGED) unaligned ones that the ring does not take: rows of
+// more than 16384 columns, BF16 rows of one warp's team, tensors that do not start on 16 bytes.
 template <bool BF16, bool NV4, int TPR, int NCH, bool STAGED>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_add_rmsnorm(const NormKernelArgs a) {
   constexpr int kThreads = TPR < 256 ? 256 : TPR;
@@ -318,6 +319,18 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR,
   }
 }
 
+// The direct kernel.
+template <bool BF16, bool NV4, int TPR, int NCH, bool STAGED>
+cudaError_t run_norm_direct(const NormKernelArgs& k, int64_t groups, const DeviceInfo& dev,
+                            cudaStream_t stream) {
+  constexpr int kThreads = TPR < 256 ? 256 : TPR;
+  const auto kernel = k_add_rmsnorm<BF16, NV4, TPR, NCH, STAGED>;
+  static const int resident = resident_ctas(kernel, kThreads);
+  const int64_t grid = std::min<int64_t>(groups, (int64_t)resident * dev.num_sms);
+  kernel<<<(unsigned)grid, kThreads, 0, stream>>>(k);
+  return cudaGetLastError();
+}
+
 // The ring kernel, where at least two stages fit and every CTA has several groups (done).
 template <bool BF16, bool NV4, int TPR, int NCH, bool ANY>
 cudaError_t run_norm_ring(const NormKernelArgs& k, int64_t groups, const DeviceInfo& dev,
@@ -336,32 +349,39 @@ cudaError_t run_norm_ring(const NormKernelArgs& k, int64_t groups, const DeviceI
   return cudaGetLastError();
 }
 
-template <bool BF16, bool NV4, int TPR, int NCH>
+// ROWS: which rows pick_norm sends here (the kernels of the others are not made): aligned ones,
+// few or many, or many alone, or those that are not aligned.
+enum NormRows { kAnyRows, kFewAlignedOrUnaligned, kManyAligned, kUnaligned };
+
+template <bool BF16, bool NV4, int TPR, int NCH, NormRows ROWS>
 cudaError_t run_norm(const NormKernelArgs& k, const DeviceInfo& dev, cudaStream_t stream) {
   constexpr int kThreads = TPR < 256 ? 256 : TPR;
   constexpr int kTeams = kThreads / TPR;
-  const auto direct = k.g_min >= 16 ? k_add_rmsnorm<BF16, NV4, TPR, NCH, false>
-                                    : k_add_rmsnorm<BF16, NV4, TPR, NCH, true>;
-  static const int aligned = resident_ctas(k_add_rmsnorm<BF16, NV4, TPR, NCH, false>, kThreads);
-  static const int staged = resident_ctas(k_add_rmsnorm<BF16, NV4, TPR, NCH, true>, kThreads);
-  const int resident = k.g_min >= 16 ? aligned : staged;
   const int64_t groups = (k.rows + kTeams - 1) / kTeams;
-  const int64_t grid = std::min<int64_t>(groups, (int64_t)resident * dev.num_sms);
   bool done = false;
   cudaError_t e = cudaSuccess;
-  if (k.g_min >= 16) {
-    e = run_norm_ring<BF16, NV4, TPR, NCH, false>(k, groups, dev, stream, &done);
-  } else if constexpr (NCH == 1 && (TPR > 32 || !BF16)) {
+  if constexpr (ROWS != kUnaligned) {
+    if (k.g_min >= 16) {
+      // few rows: one or two for each CTA, so never through the ring
+      if constexpr (ROWS != kFewAlignedOrUnaligned)
+        e = run_norm_ring<BF16, NV4, TPR, NCH, false>(k, groups, dev, stream, &done);
+      if (done || e != cudaSuccess) return e;
+      return run_norm_direct<BF16, NV4, TPR, NCH, false>(k, groups, dev, stream);
+    }
+  }
+  if constexpr (ROWS != kManyAligned) {
     // Rows that are not aligned: one step per thread (two stages of longer rows seldom fit).
     // Through the ring and loaded directly, BF16 with FP8 codes: 4000 x 5001 58 and 80 us,
     // 16384 x 1001 41 and 88; FP32: 4000 x 5001 71 and 103, 16384 x 511 30 and 41.  BF16
     // rows of one warp's team do not gain: 16384 x 500 25.4 and 22.6, 16384 x 511 26.7 and 25.8.
-    if (k.bases_aligned)
-      e = run_norm_ring<BF16, NV4, TPR, NCH, true>(k, groups, dev, stream, &done);
+    if constexpr (NCH == 1 && (TPR > 32 || !BF16)) {
+      if (k.bases_aligned)
+        e = run_norm_ring<BF16, NV4, TPR, NCH, true>(k, groups, dev, stream, &done);
+      if (done || e != cudaSuccess) return e;
+    }
+    return run_norm_direct<BF16, NV4, TPR, NCH, true>(k, groups, dev, stream);
   }
-  if (done || e != cudaSuccess) return e;
-  direct<<<(unsigned)grid, kThreads, 0, stream>>>(k);
-  return cudaGetLastError();
+  return cudaErrorInvalidValue;  // not reached: pick_norm sends no other rows here
 }
 
 template <bool BF16, bool NV4>
@@ -370,19 +390,19 @@ cudaError_t pick_norm(const NormKernelArgs& k, const DeviceInfo& dev, cudaStream
   // for staged rows, whose loads in flight take twice the registers
   const bool few = k.rows <= 2LL * dev.num_sms || k.g_min < 16;
   const int c = k.cols;
-  if (c <= 512) return run_norm<BF16, NV4, 32, 1>(k, dev, stream);
+  if (c <= 512) return run_norm<BF16, NV4, 32, 1, kAnyRows>(k, dev, stream);
   // teams of two warps where those of four would be half idle (16384 x 1001 unaligned: 41 us,
   // and 76 by four)
-  if (c <= 1024 && k.g_min < 16) return run_norm<BF16, NV4, 64, 1>(k, dev, stream);
-  if (c <= 1024 && !few) return run_norm<BF16, NV4, 32, 2>(k, dev, stream);
-  if (c <= 2048) return run_norm<BF16, NV4, 128, 1>(k, dev, stream);
-  if (c <= 4096) return run_norm<BF16, NV4, 256, 1>(k, dev, stream);
-  if (c <= 6144 && c > 4096) return run_norm<BF16, NV4, 384, 1>(k, dev, stream);
-  if (c <= 8192 && !few) return run_norm<BF16, NV4, 256, 2>(k, dev, stream);
-  if (c <= 8192) return run_norm<BF16, NV4, 512, 1>(k, dev, stream);
-  if (c <= 16384 && !few) return run_norm<BF16, NV4, 512, 2>(k, dev, stream);
-  if (c <= 16384) return run_norm<BF16, NV4, 1024, 1>(k, dev, stream);
-  return run_norm<BF16, NV4, 1024, 2>(k, dev, stream);
+  if (c <= 1024 && k.g_min < 16) return run_norm<BF16, NV4, 64, 1, kUnaligned>(k, dev, stream);
+  if (c <= 1024 && !few) return run_norm<BF16, NV4, 32, 2, kManyAligned>(k, dev, stream);
+  if (c <= 2048) return run_norm<BF16, NV4, 128, 1, kAnyRows>(k, dev, stream);
+  if (c <= 4096) return run_norm<BF16, NV4, 256, 1, kAnyRows>(k, dev, stream);
+  if (c <= 6144) return run_norm<BF16, NV4, 384, 1, kAnyRows>(k, dev, stream);
+  if (c <= 8192 && !few) return run_norm<BF16, NV4, 256, 2, kManyAligned>(k, dev, stream);
+  if (c <= 8192) return run_norm<BF16, NV4, 512, 1, kFewAlignedOrUnaligned>(k, dev, stream);
+  if (c <= 16384 && !few) return run_norm<BF16, NV4, 512, 2, kManyAligned>(k, dev, stream);
+  if (c <= 16384) return run_norm<BF16, NV4, 1024, 1, kFewAlignedOrUnaligned>(k, dev, stream);
+  return run_norm<BF16, NV4, 1024, 2, kAnyRows>(k, dev, stream);
 }
 
 }  // namespace

@@ -83,8 +83,9 @@ struct UnitType<1> {
 };
 
 // A staged load in two steps, so that several can be in flight: the warp's units into
-// registers, then through shared memory into each lane's W words.
-template <int W, int PITCH>
+// registers, then through shared memory into each lane's W words.  ELEM: bytes of an element,
+// the least unit that there can be.
+template <int W, int PITCH, int ELEM>
 struct StagedLoad {
   uint32_t v[2 * W];  // units of 2 bytes take a register each, wider ones W words in all
 
@@ -122,13 +123,13 @@ struct StagedLoad {
   }
   __device__ __forceinline__ void issue(const char* p, int bytes, int unit, int lane) {
     if (unit == 8) issue_units<8>(p, bytes, lane);
-    else if (unit == 4) issue_units<4>(p, bytes, lane);
-    else issue_units<2>(p, bytes, lane);
+    else if (ELEM == 4 || unit == 4) issue_units<4>(p, bytes, lane);
+    else if constexpr (ELEM == 2) issue_units<2>(p, bytes, lane);
   }
   __device__ __forceinline__ void settle(int unit, uint8_t* smem, int lane, uint32_t* w) const {
     if (unit == 8) settle_units<8>(smem, lane);
-    else if (unit == 4) settle_units<4>(smem, lane);
-    else settle_units<2>(smem, lane);
+    else if (ELEM == 4 || unit == 4) settle_units<4>(smem, lane);
+    else if constexpr (ELEM == 2) settle_units<2>(smem, lane);
     __syncwarp();
 #pragma unroll
     for (int k = 0; k < W; k += 4) {
@@ -159,8 +160,20 @@ __device__ __forceinline__ void staged_store_units(char* p, int bytes, const uin
   else
     staged_store_units<W, PITCH, UNIT, false>(p, bytes, smem, lane);
 }
-// Words of every lane to memory through shared memory (see StagedUnits).
-template <int W, int PITCH>
+template <int W, int PITCH, int LEAST, int MOST>
+__device__ __forceinline__ void staged_store_least(char* p, int bytes, int unit,
+                                                   const uint8_t* smem, int lane) {
+  if constexpr (MOST > LEAST) {
+    if (unit < MOST) {
+      staged_store_least<W, PITCH, LEAST, MOST / 2>(p, bytes, unit, smem, lane);
+      return;
+    }
+  }
+  staged_store_units<W, PITCH, MOST>(p, bytes, smem, lane);
+}
+// Words of every lane to memory through shared memory (see StagedUnits), in units of LEAST to
+// MOST bytes.
+template <int W, int PITCH, int LEAST, int MOST>
 __device__ __forceinline__ void staged_store(char* p, int bytes, int unit, uint8_t* smem,
                                              int lane, const uint32_t* w) {
   if constexpr (W % 4 == 0) {
@@ -174,10 +187,7 @@ __device__ __forceinline__ void staged_store(char* p, int bytes, int unit, uint8
       *reinterpret_cast<uint32_t*>(smem + 4 * W * lane + 4 * k) = w[k];
   }
   __syncwarp();
-  if (unit == 8) staged_store_units<W, PITCH, 8>(p, bytes, smem, lane);
-  else if (unit == 4) staged_store_units<W, PITCH, 4>(p, bytes, smem, lane);
-  else if (unit == 2) staged_store_units<W, PITCH, 2>(p, bytes, smem, lane);
-  else staged_store_units<W, PITCH, 1>(p, bytes, smem, lane);
+  staged_store_least<W, PITCH, LEAST, MOST>(p, bytes, unit, smem, lane);
   __syncwarp();
 }
 
@@ -310,7 +320,8 @@ struct Chunk {
     char* p = static_cast<char*>(base) + (off - (int64_t)kChunk * lane) * kElem;
 #pragma unroll
     for (int h = 0; h < kWords; h += 8)
-      staged_store<8, 4 * kWords>(p + 4 * h, (int)run * kElem - 4 * h, grain, smem, lane, w + h);
+      staged_store<8, 4 * kWords, kElem, 8>(p + 4 * h, (int)run * kElem - 4 * h, grain, smem,
+                                            lane, w + h);
   }
   // From a row held in shared memory, 16-byte aligned (so n is a whole number of 16-byte
   // units).  Lanes are 32 or 64 bytes apart; rotating the order of a lane's units spreads
@@ -431,7 +442,7 @@ struct Chunk {
 template <bool BF16, bool STAGED>
 struct ChunkLoad {
   Chunk<BF16> c;
-  StagedLoad<8, 4 * Chunk<BF16>::kWords> raw[STAGED ? Chunk<BF16>::kWords / 8 : 1];
+  StagedLoad<8, 4 * Chunk<BF16>::kWords, BF16 ? 2 : 4> raw[STAGED ? Chunk<BF16>::kWords / 8 : 1];
 
   __device__ __forceinline__ void issue(const void* base, int64_t off, int n, int64_t run,
                                         int grain, int lane) {
