@@ -64,14 +64,14 @@ __device__ __forceinline__ float fp8_scale(float a) {
 // gives exactly (Markstein, "Computation of elementary functions on the IBM RISC System/6000
 // processor", 1990): 16 divisions would cost five times the instructions.
 struct Fp8Divisor {
-  float r, scale;  // (an infinite scale: 0, so that the step adds nothing to 0)
+  float r, minus;  // 1 / scale, and -scale (0 for an infinite one: the step adds nothing to 0)
 };
 __device__ __forceinline__ Fp8Divisor fp8_divisor(float scale) {
-  return {__frcp_rn(scale), isinf(scale) ? 0.0f : scale};
+  return {__frcp_rn(scale), isinf(scale) ? 0.0f : -scale};
 }
 __device__ __forceinline__ Pair fp8_quotient(Pair y, const Fp8Divisor& d) {
   const Pair q = pair_mul(y, {d.r, d.r});
-  const Pair rest = pair_fma({-q.x, -q.y}, {d.scale, d.scale}, y);
+  const Pair rest = pair_fma(q, {d.minus, d.minus}, y);
   return pair_fma(rest, {d.r, d.r}, q);
 }
 
