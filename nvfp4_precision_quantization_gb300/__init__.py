@@ -193,10 +193,19 @@ def _ptr(t) -> Optional[int]:
     return t.data_ptr()
 
 
+def _current_raw_stream(device: int) -> int:
+    return torch.cuda.current_stream(device).cuda_stream
+
+
+# The handle alone where this torch has a call for it (a Stream object costs as much as the
+# launch of a small kernel); it is not part of torch's interface, so a torch without it is served
+# by the one above.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", _current_raw_stream)
+
+
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        # the handle alone: a Stream object costs as much as the launch of a small kernel
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+        return _raw_stream(torch.cuda.current_device())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

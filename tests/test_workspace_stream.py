@@ -125,3 +125,27 @@ def test_other_stream_without_a_workspace(name):
         torch.cuda.synchronize()
         assert all(bool((f == 0xA5).all()) for f in filled)
         assert all(torch.equal(o, w) for o, w in zip(outs, want))
+
+
+def test_current_stream_without_torchs_inner_call(monkeypatch):
+    """A torch that lacks the inner call for the handle is served through its interface."""
+    import importlib.util
+    monkeypatch.delattr(torch._C, "_cuda_getCurrentRawStream", raising=False)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 3)
+    monkeypatch.setattr(torch.cuda, "current_stream",
+                        lambda device=None: type("S", (), {"cuda_stream": 0x4560 + device}))
+    spec = importlib.util.spec_from_file_location("nv_again", nv.__file__)
+    again = importlib.util.module_from_spec(spec)
+    monkeypatch.setitem(__import__("sys").modules, "nv_again", again)
+    spec.loader.exec_module(again)
+    assert again._stream(None) == 0x4563
+    assert again._stream(0x1230) == 0x1230 and again._stream(_Stream()) == 0x1230
+
+
+@pytest.mark.gpu
+def test_current_stream_is_the_same_by_both_ways():
+    s = torch.cuda.Stream()
+    for stream in (torch.cuda.current_stream(), s):
+        with torch.cuda.stream(stream):
+            assert nv._stream(None) == nv._current_raw_stream(torch.cuda.current_device()) == \
+                stream.cuda_stream
