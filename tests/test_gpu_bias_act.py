@@ -297,3 +297,28 @@ def test_empty_sum_of_every_activation(m, n, name, dtype):
     want = act(zz, name) + res.double()
     tol = 2.0 ** -20 * (1 + zz.abs()) + (2.0 ** -23 + half_ulp(dtype)) * 1.01 * want.abs()
     assert bool(((out[0][0].double() - want).abs() <= tol).all())
+
+
+def _moved(o, codes, scales, amax):
+    """The operand with its tensors starting off their allocations' alignment."""
+    return nv.Operand(at_offset(o.codes, codes), at_offset(o.scales, scales),
+                      at_offset(o.amax, amax), o.mode, o.bound)
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 300, 544), (5, 129, 2080), (40, 1000, 96), (64, 256, 8224),
+                                   (300, 500, 320), (129, 10100, 1056), (450, 5000, 96)])
+@pytest.mark.parametrize("start", [1, 2, 8])
+def test_scales_that_start_anywhere(m, n, k, start):
+    """Scale tensors that start off 16 bytes are copied byte by byte, and change nothing: every
+    scale reaches the place that it has otherwise."""
+    (a, b), _, _ = _operands(m, n, k, m + n + k)
+    bias = torch.randn(n, device=DEV)
+    want = torch.empty(m, n, device=DEV)
+    nv.nvfp4_gemm_bias_act(a, b, want, bias=bias, act=nv.NVFP4_ACT_GELU)
+    for x, w in ((start, 0), (0, start), (start, start)):
+        d, ok = guarded((m, n), torch.float32)
+        nv.nvfp4_gemm_bias_act(_moved(a, 16, x, 1), _moved(b, 32, w, 3), d, bias=bias,
+                               act=nv.NVFP4_ACT_GELU)
+        torch.cuda.synchronize()
+        assert torch.equal(d, want)
+        ok()
