@@ -544,7 +544,7 @@ __global__ void __launch_bounds__(kPipeThreads, 2)
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&col_bar[b]);
-    if (!mbar_wait_bounded(&col_bar[b], parity)) return false;
+    if (!__all_sync(0xffffffffu, mbar_wait_bounded(&col_bar[b], parity))) return false;
     float* const cbase = a.col_amax + (a.col_grouped ? (int64_t)cur_g * a.K : 0);
     const int64_t span0 = (int64_t)ss * kSpan;
     for (int i = tid; i < kSpan; i += kConsumerWarps * 32) {
@@ -625,12 +625,13 @@ __global__ void __launch_bounds__(kPipeThreads, 2)
         cur_g = g_now;
       }
     }
-    if (!mbar_wait_bounded(&full[s], (uint32_t)((k / kStages) & 1))) {
+    const bool ok = mbar_wait_bounded(&full[s], (uint32_t)((k / kStages) & 1));
+    if (!ok) {
       abort_flag = 1;
-      if (lane == 0) raise_status(a.status, kStatusTimeout);
-      break;
+      raise_status(a.status, kStatusTimeout);
     }
-    if (abort_flag) break;
+    // each lane's wait gives up by its own clock: a warp, whose shuffles follow, leaves together
+    if (__any_sync(0xffffffffu, !ok || abort_flag)) break;
     const uint8_t* stage = smem + s * kTileBytes + (rg * 32 + ro) * 128;
     Acc rp[8], ct[4] = {0, 0, 0, 0};
 #pragma unroll
@@ -691,11 +692,11 @@ __global__ void __launch_bounds__(kPipeThreads, 2)
       }
     }
   }
-  if (COL && cur_ss >= 0 && !abort_flag && !flush_cols(cur_ss)) {
+  if (COL && cur_ss >= 0 && !__any_sync(0xffffffffu, abort_flag) && !flush_cols(cur_ss)) {
     abort_flag = 1;
     if (lane == 0) raise_status(a.status, kStatusTimeout);
   }
-  if (ROW && cur_tm >= 0 && !abort_flag) flush_rows(cur_tm);
+  if (ROW && cur_tm >= 0 && !__any_sync(0xffffffffu, abort_flag)) flush_rows(cur_tm);
   if (TEN) {
     float m;
     if constexpr (BF16) m = bf16x2_hmax_f32(tmx);

@@ -957,13 +957,11 @@ __global__ void __launch_bounds__(kPipeThreads, 2)
       const int s = k % NS;
       if (k >= NS) {
         const bool ok = mbar_wait_bounded(&empty[s], (uint32_t)(((k / NS) - 1) & 1));
-        if (!ok || abort_flag) {
-          if (lane == 0 && !ok) {
-            abort_flag = 1;
-            raise_status(a.status, kStatusTimeout);
-          }
-          break;
+        if (!ok) {
+          abort_flag = 1;
+          raise_status(a.status, kStatusTimeout);
         }
+        if (__any_sync(0xffffffffu, !ok || abort_flag)) break;
         issue(k);
         issued = k + 1;
       }
@@ -1077,10 +1075,12 @@ __global__ void __launch_bounds__(kPipeThreads, 2)
     const bool ok = mbar_wait_bounded(&full[s], (uint32_t)((k / NS) & 1));
     if (!ok) {
       abort_flag = 1;
-      if (lane == 0) raise_status(a.status, kStatusTimeout);
+      raise_status(a.status, kStatusTimeout);
     }
-    if constexpr (B2D) consumer_sync();  // every consumer sees the same abort decision
-    if (abort_flag) break;
+    // each lane's wait gives up by its own clock, and the producer may abort at any time: those
+    // that meet again (a warp in its shuffles, with 16x16 blocks every consumer at the next
+    // barrier) leave together
+    if (B2D ? consumer_any(!ok || abort_flag) : __any_sync(0xffffffffu, !ok || abort_flag)) break;
     const uint8_t* stage = smem + s * kTileBytes;
     auto& m = meta[s];
     const bool interior = tm < a.full_m && tn < a.full_n;

@@ -99,6 +99,19 @@ struct TileCursor {
 __device__ __forceinline__ void consumer_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(kConsumerWarps * 32) : "memory");
 }
+// The same, and whether any consumer's flag was set: one answer for all of them.
+__device__ __forceinline__ bool consumer_any(bool flag) {
+  uint32_t any;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %1, 0;\n\t"
+      "barrier.cta.red.or.pred q, 1, %2, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(any)
+      : "r"((uint32_t)flag), "n"(kConsumerWarps * 32)
+      : "memory");
+  return any != 0;
+}
 
 // Issue the two TMA boxes of tile (tm, tn) into `dst`, completing on `bar`; the
 // tile's rows start at x row src_row0 (tm * kTileRows unless x is ragged).

@@ -39,3 +39,21 @@ def test_few_rows_epilogue_leaves_by_a_vote():
     exits = _exits(code)
     assert len(exits) == code.count("break;") == 1
     assert exits[0].startswith("barrier_or<")
+
+
+def test_amax_and_encode_warps_leave_by_a_vote():
+    # consumers of the amax pass, up to the first shuffle or __syncwarp
+    code = _after("kernels_amax.cu", "mbar_wait_bounded(&full[s], (uint32_t)((k / kStages) & 1))",
+                  "const uint8_t* stage = smem")
+    assert _exits(code) == ["__any_sync(0xffffffffu, !ok || abort_flag)"]
+    assert code.count("break;") == 1
+    s = open(os.path.join(CSRC, "kernels_amax.cu")).read()
+    assert "if (!__all_sync(0xffffffffu, mbar_wait_bounded(&col_bar[b], parity))) return false;" in s
+    # the encode's producer warp and its consumers; with 16x16 blocks all consumers decide
+    code = _after("kernels_quantize.cu", "mbar_wait_bounded(&empty[s],", "issue(k);")
+    assert _exits(code) == ["__any_sync(0xffffffffu, !ok || abort_flag)"]
+    code = _after("kernels_quantize.cu", "mbar_wait_bounded(&full[s], (uint32_t)((k / NS) & 1))",
+                  "const uint8_t* stage = smem")
+    assert _exits(code) == ["B2D ? consumer_any(!ok || abort_flag) : "
+                            "__any_sync(0xffffffffu, !ok || abort_flag)"]
+    assert code.count("break;") == 1 and "consumer_sync" not in code
