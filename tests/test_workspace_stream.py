@@ -149,3 +149,19 @@ def test_current_stream_is_the_same_by_both_ways():
         with torch.cuda.stream(stream):
             assert nv._stream(None) == nv._current_raw_stream(torch.cuda.current_device()) == \
                 stream.cuda_stream
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("handle", [0, 1, 2])  # the default stream, legacy and per thread
+@pytest.mark.parametrize("name", ["gemm_bias_act", "bias_act_backward", "clip_grad_norm"])
+def test_default_stream_handles(name, handle):
+    outs, call = _calls("cuda")[name]
+    call(None)
+    torch.cuda.synchronize()
+    want = [o.clone() for o in outs]
+    for o in outs:
+        o.zero_()
+    torch.cuda.synchronize()
+    call(handle)
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, w) for o, w in zip(outs, want))
