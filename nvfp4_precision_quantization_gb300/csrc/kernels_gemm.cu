@@ -33,9 +33,10 @@
 //             sectors.
 // With an epilogue (EPI: bias, activation, residual, the pre-activation kept) the same
 // warps finish the tile in blocks of 32 x 32 (epilogue_block32), the residual's lines asked
-// for while the MMAs run.  Measured (bias, GELU, z kept): 16384 x 28672 x 8192 1.95 ms, 3.94
-// PFLOP/s, against 1.87 ms for the product alone; 8192 x 8192 x 2048 130 us, 146 with a
-// residual, 103 for the product alone: with few K tiles the epilogue's stores show.
+// for while the MMAs run.  Measured (bias, GELU): 16384 x 28672 x 8192 1.89 ms, 1.97 with z
+// kept, 3.9 PFLOP/s, 2.03 with a residual, against 1.87 ms for the product alone; 8192 x 8192
+// x 2048 134 us, 149 with z, 145 with a residual, 171 with both, 96 for the product alone: with
+// few K tiles the epilogue's loads and stores show.
 // Scales reach the kernel in the layout their TMEM copies want (see SfLayout): a
 // pre-pass (k_sf_layout) rewrites the compact [lines][k/16] scales of both operands
 // into the caller's workspace.

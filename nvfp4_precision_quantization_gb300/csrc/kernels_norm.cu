@@ -9,10 +9,10 @@
 // with the positive s is monotonic; the scale of the whole row is therefore known one
 // barrier after its last load.
 //
-// Measured (E4M3 output, residual): 16384 x 8192 BF16 155 us, 6.05 TB/s, 0.91 of a copy (182
-// us without the ring); 4000 x 5000 FP32 in 128-column blocks 49 us, 5.3 TB/s (barriers and
-// shared-memory rotations are in sight there: issue slots are 54 % used); one row of 8192
-// 4.1 us, which is a launch and one pass of latencies.
+// Measured (E4M3 output, residual): 16384 x 8192 BF16 147 us, 6.4 TB/s, 0.96 of a copy (182
+// us without the ring), NVFP4 rows 153 us; 4000 x 5000 FP32 in 128-column blocks 49 us, 5.3
+// TB/s (barriers and shared-memory rotations are in sight there: issue slots are 54 % used);
+// one row of 8192 3.0 us, which is a launch and one pass of latencies.
 #include "row_ring.cuh"
 
 namespace nvfp4 {
@@ -371,8 +371,8 @@ cudaError_t run_norm(const NormKernelArgs& k, const DeviceInfo& dev, cudaStream_
   }
   if constexpr (ROWS != kManyAligned) {
     // Rows that are not aligned: one step per thread (two stages of longer rows seldom fit).
-    // Through the ring and loaded directly, BF16 with FP8 codes: 4000 x 5001 58 and 80 us,
-    // 16384 x 1001 41 and 88; FP32: 4000 x 5001 71 and 103, 16384 x 511 30 and 41.  BF16
+    // Through the ring and loaded directly, BF16 with FP8 codes: 4000 x 5001 59 and 80 us,
+    // 16384 x 1001 42 and 88; FP32: 4000 x 5001 69 and 103, 16384 x 511 30 and 41.  BF16
     // rows of one warp's team do not gain: 16384 x 500 25.4 and 22.6, 16384 x 511 26.7 and 25.8.
     if constexpr (NCH == 1 && (TPR > 32 || !BF16)) {
       if (k.bases_aligned)

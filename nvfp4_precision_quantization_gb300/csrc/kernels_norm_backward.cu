@@ -6,8 +6,8 @@
 // h and dh in registers across the one reduction that the row needs, and each thread the
 // weight's gradient of its columns across all rows of its CTA.
 //
-// Measured: 16384 x 8192 BF16 with dh 174 us, 6.15 TB/s, 0.92 of a copy (266 us without the
-// ring); 4000 x 5000 FP32 52 us, 4.6 TB/s (313 of a team's 384 threads have columns, and the
+// Measured: 16384 x 8192 BF16 with dh 176 us, 6.1 TB/s, 0.91 of a copy (266 us without the
+// ring); 4000 x 5000 FP32 51 us, 4.7 TB/s (313 of a team's 384 threads have columns, and the
 // dw sums are joined by a second launch of 3 us).
 #include "row_ring.cuh"
 
@@ -297,7 +297,7 @@ cudaError_t run_norm_backward(const NormBackwardKernelArgs& k, int max_parts,
       e = run_backward_ring<BF16, TPR, NCH, false>(k, groups, max_parts, dev, stream, parts, &done);
   }
   if constexpr (NCH == 1) {
-    // Rows that are not aligned.  BF16, through the ring and loaded directly: 4000 x 5001 62
+    // Rows that are not aligned.  BF16, through the ring and loaded directly: 4000 x 5001 59
     // and 88 us, 16384 x 1001 46 and 76, 16384 x 25 30 and 35; FP32 4000 x 5001 74 and 123.
     if (k.g_min < 16 && k.bases_aligned)
       e = run_backward_ring<BF16, TPR, NCH, true>(k, groups, max_parts, dev, stream, parts, &done);
