@@ -506,6 +506,80 @@ NVFP4_API nvfp4_status nvfp4_add_rmsnorm_backward(const void *dy, const void *h,
                                                   nvfp4_stream_t stream);
 
 /*
+ * A dropout mask that is never stored: an element's bit is a function of seed, offset and its
+ * index i (row-major, from 0), so the backward pass gives the same seed and offset.
+ *   Element i is dropped where its 16 random bits are below t = round(p * 2^16); what is kept
+ *   is multiplied by 2^16 / (2^16 - t) (p == 1 drops everything; t == 0 drops nothing).  A
+ *   dropped NaN or infinity is 0.
+ *   The bits: half i % 2 (low half first) of word (i % 8) / 2 of the Philox4x32-10 block
+ *   [Salmon et al. 2011] with the counter words (i / 8 low, i / 8 high, offset low, offset
+ *   high) and the key (seed low, seed high).
+ *   p: in [0, 1].  offset: another one for each layer and step.
+ *   offset_add: optional, one device value (8-byte aligned) added to offset when the call's
+ *   kernels run, so that a captured call gets a new mask with each replay.
+ */
+typedef struct {
+    float p;
+    uint64_t seed;
+    uint64_t offset;
+    const uint64_t *offset_add;
+} nvfp4_mask;
+
+/*
+ * nvfp4_dropout -- y = residual + drop(x) (drop(x) where residual is NULL), the sum in FP32.
+ *   x, residual, y: n elements of dtype; y may be x or residual itself.  n < 2^48.
+ *   Its gradients: the residual's is dy, x's is nvfp4_dropout(dy) with the same mask.
+ */
+NVFP4_API nvfp4_status nvfp4_dropout(const void *x, const void *residual, int32_t dtype, int64_t n,
+                                     const nvfp4_mask *mask, void *y, nvfp4_stream_t stream);
+
+/*
+ * nvfp4_add_layernorm -- dropout, residual addition and layer norm of each row:
+ *   h = residual + drop(x) (x where mask is NULL; residual may be NULL)
+ *   mean = mean_c(h), rstd = 1 / sqrt(mean_c((h - mean)^2) + eps)
+ *   y = (h - mean) * rstd * weight + bias
+ * computed in FP32 from the unrounded h, in one read of x and residual.
+ *   bias: optional, [cols] of weight_dtype.
+ *   h (optional, with a residual or a mask), mean, rstd (optional, [rows] FP32): what
+ *   nvfp4_add_layernorm_backward takes.
+ *   The mask's element r * cols + c is that of row r, column c (as nvfp4_dropout's of the
+ *   whole matrix).
+ *   Everything else, y, fp8 and row with cfg among it, as for nvfp4_add_rmsnorm.
+ *   cols <= NVFP4_RMSNORM_MAX_COLS.  cols == 0: mean is 0, rstd is 1/sqrt(eps).
+ */
+NVFP4_API nvfp4_status nvfp4_add_layernorm(const void *x, const void *residual, int32_t in_dtype,
+                                           const nvfp4_mask *mask, const void *weight,
+                                           const void *bias, int32_t weight_dtype, int64_t rows,
+                                           int64_t cols, float eps, void *h, void *y, float *mean,
+                                           float *rstd, const nvfp4_fp8_out *fp8,
+                                           const nvfp4_config *cfg, const nvfp4_out *row,
+                                           nvfp4_stream_t stream);
+
+/*
+ * nvfp4_add_layernorm_backward -- gradients of nvfp4_add_layernorm (a quantized output passes
+ * its gradient straight through).  With n = (h - mean) * rstd and g = dy * weight:
+ *   dresidual = rstd * (g - mean_c(g) - n * mean_c(g * n)) + dh
+ *   dx = dresidual, through the forward's mask where there is one
+ *   dweight = sum_rows dy * n,  dbias = sum_rows dy
+ *   dy, h, dh, dx, dresidual: [rows][cols] of in_dtype; dh (optional) is the gradient that
+ *   reaches h beside the norm's; dx and dresidual may each be dy, h or dh itself, but not one
+ *   another.  dresidual is optional with a mask and NULL without one (dx is both then).
+ *   h, mean, rstd: as the forward wrote them (h is x where it had neither residual nor mask).
+ *   dweight, dbias (optional): [cols] FP32, overwritten; their sums run in a fixed order.
+ *   workspace: device, 16-byte aligned, at least
+ *   nvfp4_add_layernorm_backward_workspace_size(rows, cols) bytes (unused without dweight and
+ *   dbias); two calls in flight at once need two workspaces.
+ *   cols <= NVFP4_RMSNORM_MAX_COLS.
+ */
+NVFP4_API nvfp4_status nvfp4_add_layernorm_backward_workspace_size(int64_t rows, int64_t cols,
+                                                                   uint64_t *bytes);
+NVFP4_API nvfp4_status nvfp4_add_layernorm_backward(
+    const void *dy, const void *h, const void *dh, int32_t in_dtype, const nvfp4_mask *mask,
+    const void *weight, int32_t weight_dtype, const float *mean, const float *rstd, int64_t rows,
+    int64_t cols, void *dx, void *dresidual, float *dweight, float *dbias, void *workspace,
+    uint64_t workspace_bytes, nvfp4_stream_t stream);
+
+/*
  * nvfp4_gemm_bias_act -- nvfp4_gemm with bias, activation and residual in its epilogue:
  *   z = dequant(a) x dequant(b)^T + bias,   d = act(z) + residual
  * in FP32 from the tensor cores' accumulator, without the product going to memory.
@@ -533,6 +607,61 @@ NVFP4_API nvfp4_status nvfp4_gemm_bias_act(const nvfp4_operand *a, const nvfp4_o
                                            const nvfp4_epilogue *epilogue, void *d,
                                            int32_t out_dtype, void *workspace,
                                            uint64_t workspace_bytes, nvfp4_stream_t stream);
+
+/*
+ * nvfp4_gemm_gated -- the gated feed-forward block's two projections, activation and product:
+ *   g = dequant(a) x dequant(b_g)^T + bias_g,   u = dequant(a) x dequant(b_u)^T + bias_u
+ *   d = act(g) * u
+ * in FP32 from the tensor cores' accumulators, without g and u going to memory (unless kept).
+ *   a: m lines; b: 2n lines, b_g's n and then b_u's, one operand (so that the backward
+ *   products with it, and with the gradient of gu, are one nvfp4_gemm each).
+ *   d [m][n] of out_dtype; k, workspace as for nvfp4_gemm, workspace_bytes at least
+ *   nvfp4_gemm_gated_workspace_size(m, n, k).  n < 2^30.
+ *   epilogue->bias      optional, [2n] of bias_dtype (NVFP4_IN_BF16 or NVFP4_IN_FP32)
+ *   epilogue->act       nvfp4_activation (NVFP4_ACT_NONE: d = g * u)
+ *   epilogue->gu        optional, [m][2n] of out_dtype: receives g and u side by side, for
+ *                       nvfp4_gated_backward
+ *   epilogue->row_amax  optional, [m] FP32; epilogue->col_amax optional, [n] FP32: the exact
+ *                       maxima of |d| as it is stored (NaN skipped), which the quantization
+ *                       of d takes as amax_in
+ *   Few rows (decoding) run on a kernel of their own that streams b once.
+ *   k == 0: g and u are the biases.
+ */
+typedef struct {
+    const void *bias;
+    int32_t bias_dtype;
+    int32_t act;
+    void *gu;
+    float *row_amax;
+    float *col_amax;
+} nvfp4_gated_epilogue;
+NVFP4_API nvfp4_status nvfp4_gemm_gated_workspace_size(int64_t m, int64_t n, int64_t k,
+                                                       uint64_t *bytes);
+NVFP4_API nvfp4_status nvfp4_gemm_gated(const nvfp4_operand *a, const nvfp4_operand *b, int64_t m,
+                                        int64_t n, int64_t k,
+                                        const nvfp4_gated_epilogue *epilogue, void *d,
+                                        int32_t out_dtype, void *workspace,
+                                        uint64_t workspace_bytes, nvfp4_stream_t stream);
+
+/*
+ * nvfp4_gated_backward -- gradients of d = act(g) * u, from gu as nvfp4_gemm_gated kept it:
+ *   dgu = [dd * u * act'(g) | dd * act(g)]   (relu'(0) = 0)
+ *   dbias = sum_rows dgu (of the unrounded values, in a fixed order)
+ * and the exact row and column maxima of |dgu| as it is stored, which the quantization of dgu
+ * takes as amax_in, so that it needs no amax pass.
+ *   dd [rows][cols], gu and dgu [rows][2 cols] of dtype; dgu may be gu itself.
+ *   dbias [2 cols], row_amax [rows] (over both halves), col_amax [2 cols]: optional, FP32.
+ *   workspace: device, 16-byte aligned, at least
+ *   nvfp4_gated_backward_workspace_size(rows, cols) bytes (unused when dbias, row_amax and
+ *   col_amax are all NULL); two calls in flight at once need two workspaces.  cols < 2^30.
+ */
+NVFP4_API nvfp4_status nvfp4_gated_backward_workspace_size(int64_t rows, int64_t cols,
+                                                           uint64_t *bytes);
+NVFP4_API nvfp4_status nvfp4_gated_backward(const void *dd, const void *gu, int32_t dtype,
+                                            int32_t act, int64_t rows, int64_t cols, void *dgu,
+                                            float *dbias, float *row_amax, float *col_amax,
+                                            void *workspace, uint64_t workspace_bytes,
+                                            nvfp4_stream_t stream);
 
 /*
  * nvfp4_bias_act_backward -- gradients of d = act(z), z = product + bias:

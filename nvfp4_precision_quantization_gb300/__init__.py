@@ -39,7 +39,11 @@ __all__ = [
     "nvfp4_add_rmsnorm_backward_workspace_size", "nvfp4_gemm_bias_act",
     "nvfp4_gemm_bias_act_workspace_size", "nvfp4_bias_act_backward",
     "nvfp4_bias_act_backward_workspace_size", "nvfp4_grad_norm", "nvfp4_clip_grad_norm",
-    "nvfp4_clip_grad_norm_workspace_size",
+    "nvfp4_clip_grad_norm_workspace_size", "Mask",
+    "nvfp4_add_layernorm", "nvfp4_add_layernorm_backward",
+    "nvfp4_add_layernorm_backward_workspace_size", "nvfp4_dropout", "nvfp4_gemm_gated",
+    "nvfp4_gemm_gated_workspace_size", "nvfp4_gated_backward",
+    "nvfp4_gated_backward_workspace_size",
 ]
 
 NVFP4_OK = 0
@@ -77,6 +81,10 @@ EXPORTED_SYMBOLS = (
     "nvfp4_gemm_bias_act_workspace_size", "nvfp4_bias_act_backward",
     "nvfp4_bias_act_backward_workspace_size", "nvfp4_grad_norm", "nvfp4_clip_grad_norm",
     "nvfp4_clip_grad_norm_workspace_size",
+    "nvfp4_add_layernorm", "nvfp4_add_layernorm_backward",
+    "nvfp4_add_layernorm_backward_workspace_size", "nvfp4_dropout", "nvfp4_gemm_gated",
+    "nvfp4_gemm_gated_workspace_size", "nvfp4_gated_backward",
+    "nvfp4_gated_backward_workspace_size",
 )
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -174,6 +182,16 @@ def load_library():
         "nvfp4_clip_grad_norm_workspace_size": [C.POINTER(C.c_uint64)],
         "nvfp4_grad_norm": [vp, i32, vp, vp, C.c_uint64, vp],
         "nvfp4_clip_grad_norm": [vp, i32, f32, vp, vp, C.c_uint64, vp],
+        "nvfp4_dropout": [vp, vp, i32, i64, vp, vp, vp],
+        "nvfp4_add_layernorm": [vp, vp, i32, vp, vp, vp, i32, i64, i64, f32, vp, vp, vp, vp, vp,
+                                vp, vp, vp],
+        "nvfp4_add_layernorm_backward_workspace_size": [i64, i64, C.POINTER(C.c_uint64)],
+        "nvfp4_add_layernorm_backward": [vp, vp, vp, i32, vp, vp, i32, vp, vp, i64, i64, vp, vp,
+                                         vp, vp, vp, C.c_uint64, vp],
+        "nvfp4_gemm_gated_workspace_size": [i64, i64, i64, C.POINTER(C.c_uint64)],
+        "nvfp4_gemm_gated": [vp, vp, i64, i64, i64, vp, vp, i32, vp, C.c_uint64, vp],
+        "nvfp4_gated_backward_workspace_size": [i64, i64, C.POINTER(C.c_uint64)],
+        "nvfp4_gated_backward": [vp, vp, i32, i32, i64, i64, vp, vp, vp, vp, vp, C.c_uint64, vp],
     }
     for name, args in sig.items():
         fn = getattr(L, name)
@@ -610,17 +628,9 @@ def _vector(name: str, t: torch.Tensor, n: int) -> int:
     return _in_dtype(t)
 
 
-def nvfp4_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float,
-                      residual: Optional[torch.Tensor] = None,
-                      h: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
-                      rstd: Optional[torch.Tensor] = None, fp8: Optional[Fp8Out] = None,
-                      row: Optional[Out] = None, cfg: Optional[Config] = None,
-                      stream=None) -> None:
-    """h = x + residual, y = h * weight / sqrt(mean(h^2) + eps) of each row of x [rows][cols]
-    (bfloat16 or float32).  Outputs: h, y (x's type), rstd [rows], and one quantized form of
-    the FP32 y: fp8 (Fp8Out) or row with cfg (rowwise NVFP4, as nvfp4_quantize_rowwise)."""
-    rows, cols = _matrix(x)
-    shape, dtype = x.shape, x.dtype
+def _norm_outputs(rows: int, cols: int, shape, fp8: Optional[Fp8Out], row: Optional[Out],
+                  cfg: Optional[Config]):
+    """The quantized outputs of a norm as C arguments (fp8, row), and their tensors."""
     cfp8 = crow = None
     quantized = ()
     if fp8 is not None:
@@ -642,6 +652,21 @@ def nvfp4_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float,
         _floats("row.amax_in", row.amax_in, lines)
         crow = C.byref(row._c())
         quantized += (row.codes, row.scales, row.amax, row.amax_in)
+    return cfp8, crow, quantized
+
+
+def nvfp4_add_rmsnorm(x: torch.Tensor, weight: torch.Tensor, eps: float,
+                      residual: Optional[torch.Tensor] = None,
+                      h: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                      rstd: Optional[torch.Tensor] = None, fp8: Optional[Fp8Out] = None,
+                      row: Optional[Out] = None, cfg: Optional[Config] = None,
+                      stream=None) -> None:
+    """h = x + residual, y = h * weight / sqrt(mean(h^2) + eps) of each row of x [rows][cols]
+    (bfloat16 or float32).  Outputs: h, y (x's type), rstd [rows], and one quantized form of
+    the FP32 y: fp8 (Fp8Out) or row with cfg (rowwise NVFP4, as nvfp4_quantize_rowwise)."""
+    rows, cols = _matrix(x)
+    shape, dtype = x.shape, x.dtype
+    cfp8, crow, quantized = _norm_outputs(rows, cols, shape, fp8, row, cfg)
     args = (x.data_ptr(), _like("residual", residual, shape, dtype), _in_dtype(x),
             weight.data_ptr(), _vector("weight", weight, cols), rows, cols, eps,
             _like("h", h, shape, dtype), _like("y", y, shape, dtype), _floats("rstd", rstd, rows),
@@ -677,6 +702,111 @@ def nvfp4_add_rmsnorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.
         workspace, size = _workspace(workspace, need, h.device, stream)
     _check(load_library().nvfp4_add_rmsnorm_backward(*args, _ptr(workspace), size,
                                                      _stream(stream)))
+
+
+class _CMask(C.Structure):
+    _fields_ = [("p", C.c_float), ("seed", C.c_uint64), ("offset", C.c_uint64),
+                ("offset_add", C.c_void_p)]
+
+
+@dataclass
+class Mask:
+    """A dropout mask that is never stored (nvfp4_mask): drop probability p, the generator's
+    seed and the call's number offset (another one for each layer and step; the backward pass
+    gives the same).  offset_add: optional int64 tensor of one element on the GPU, added to
+    offset when the kernels run (for captured calls)."""
+    p: float
+    seed: int
+    offset: int
+    offset_add: Optional[torch.Tensor] = None
+
+    def _c(self):
+        add = self.offset_add
+        if add is not None and (add.dtype is not torch.int64 or add.numel() != 1):
+            raise ValueError("offset_add must be one int64")
+        low = (1 << 64) - 1
+        return C.byref(_CMask(self.p, self.seed & low, self.offset & low, _ptr(add)))
+
+
+def _mask(mask: Optional[Mask]):
+    """A mask as a C argument, and its device tensor."""
+    return (None, None) if mask is None else (mask._c(), mask.offset_add)
+
+
+def nvfp4_dropout(x: torch.Tensor, mask: Mask, y: torch.Tensor,
+                  residual: Optional[torch.Tensor] = None, stream=None) -> None:
+    """y = residual + drop(x) (bfloat16 or float32, any contiguous shape); y may be x or
+    residual.  The gradient of x is nvfp4_dropout(dy, mask, dx)."""
+    if not x.is_contiguous():
+        raise ValueError("x must be contiguous")
+    shape, dtype = x.shape, x.dtype
+    cmask, add = _mask(mask)
+    args = (x.data_ptr(), _like("residual", residual, shape, dtype), _in_dtype(x), x.numel(),
+            cmask, _like("y", y, shape, dtype))
+    _on_gpu(x, residual, y, add)
+    _check(load_library().nvfp4_dropout(*args, _stream(stream)))
+
+
+def nvfp4_add_layernorm(x: torch.Tensor, weight: torch.Tensor, eps: float,
+                        bias: Optional[torch.Tensor] = None,
+                        residual: Optional[torch.Tensor] = None, mask: Optional[Mask] = None,
+                        h: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                        mean: Optional[torch.Tensor] = None,
+                        rstd: Optional[torch.Tensor] = None, fp8: Optional[Fp8Out] = None,
+                        row: Optional[Out] = None, cfg: Optional[Config] = None,
+                        stream=None) -> None:
+    """h = residual + drop(x), y = (h - mean(h)) * rstd * weight + bias of each row of x
+    [rows][cols] (bfloat16 or float32), rstd = 1 / sqrt(var(h) + eps).  Outputs: h, y (x's type),
+    mean and rstd [rows], and one quantized form of the FP32 y: fp8 (Fp8Out) or row with cfg
+    (rowwise NVFP4, as nvfp4_quantize_rowwise).  bias has weight's type."""
+    rows, cols = _matrix(x)
+    shape, dtype = x.shape, x.dtype
+    cfp8, crow, quantized = _norm_outputs(rows, cols, shape, fp8, row, cfg)
+    cmask, add = _mask(mask)
+    wd = _vector("weight", weight, cols)
+    if bias is not None and _vector("bias", bias, cols) != wd:
+        raise ValueError("bias must have weight's type")
+    args = (x.data_ptr(), _like("residual", residual, shape, dtype), _in_dtype(x), cmask,
+            weight.data_ptr(), _ptr(bias), wd, rows, cols, eps, _like("h", h, shape, dtype),
+            _like("y", y, shape, dtype), _floats("mean", mean, rows), _floats("rstd", rstd, rows),
+            cfp8, C.byref(cfg) if cfg is not None else None, crow)
+    _on_gpu(x, weight, bias, residual, add, h, y, mean, rstd, *quantized)
+    _check(load_library().nvfp4_add_layernorm(*args, _stream(stream)))
+
+
+def nvfp4_add_layernorm_backward_workspace_size(rows: int, cols: int) -> int:
+    v = C.c_uint64(0)
+    _check(load_library().nvfp4_add_layernorm_backward_workspace_size(rows, cols, C.byref(v)))
+    return v.value
+
+
+def nvfp4_add_layernorm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor,
+                                 mean: torch.Tensor, rstd: torch.Tensor, dx: torch.Tensor,
+                                 dweight: Optional[torch.Tensor] = None,
+                                 dbias: Optional[torch.Tensor] = None,
+                                 dh: Optional[torch.Tensor] = None,
+                                 mask: Optional[Mask] = None,
+                                 dresidual: Optional[torch.Tensor] = None,
+                                 workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Gradients of nvfp4_add_layernorm: dx (through the forward's mask), dresidual (with a mask;
+    without one dx is both), dweight and dbias [cols] float32; dh, the gradient reaching h
+    beside the norm's, is added."""
+    rows, cols = _matrix(h)
+    shape, dtype = h.shape, h.dtype
+    cmask, add = _mask(mask)
+    args = (_like("dy", dy, shape, dtype), h.data_ptr(), _like("dh", dh, shape, dtype),
+            _in_dtype(h), cmask, weight.data_ptr(), _vector("weight", weight, cols),
+            _floats("mean", mean, rows), _floats("rstd", rstd, rows), rows, cols,
+            _like("dx", dx, shape, dtype), _like("dresidual", dresidual, shape, dtype),
+            _floats("dweight", dweight, cols), _floats("dbias", dbias, cols))
+    _on_gpu(dy, h, weight, mean, rstd, dx, dweight, dbias, dh, add, dresidual, workspace)
+    size = 0
+    if dweight is not None or dbias is not None:
+        need = 0 if workspace is not None else \
+            nvfp4_add_layernorm_backward_workspace_size(rows, cols)
+        workspace, size = _workspace(workspace, need, h.device, stream)
+    _check(load_library().nvfp4_add_layernorm_backward(*args, _ptr(workspace), size,
+                                                       _stream(stream)))
 
 
 def nvfp4_gemm_bias_act_workspace_size(m: int, n: int, k: int) -> int:
@@ -738,6 +868,74 @@ def nvfp4_bias_act_backward(dd: torch.Tensor, z: Optional[torch.Tensor], act: in
         need = 0 if workspace is not None else nvfp4_bias_act_backward_workspace_size(rows, cols)
         workspace, size = _workspace(workspace, need, dd.device, stream)
     _check(load_library().nvfp4_bias_act_backward(*args, _ptr(workspace), size, _stream(stream)))
+
+
+class _CGatedEpilogue(C.Structure):
+    _fields_ = [("bias", C.c_void_p), ("bias_dtype", C.c_int32), ("act", C.c_int32),
+                ("gu", C.c_void_p), ("row_amax", C.c_void_p), ("col_amax", C.c_void_p)]
+
+
+def nvfp4_gemm_gated_workspace_size(m: int, n: int, k: int) -> int:
+    v = C.c_uint64(0)
+    _check(load_library().nvfp4_gemm_gated_workspace_size(m, n, k, C.byref(v)))
+    return v.value
+
+
+def nvfp4_gemm_gated(a: Operand, b: Operand, d: torch.Tensor,
+                     bias: Optional[torch.Tensor] = None, act: int = NVFP4_ACT_SILU,
+                     gu: Optional[torch.Tensor] = None,
+                     row_amax: Optional[torch.Tensor] = None,
+                     col_amax: Optional[torch.Tensor] = None,
+                     workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """d [m][n] (bfloat16 or float32) = act(g) * u, [g | u] = dequant(a) x dequant(b)^T + bias: b
+    has 2n lines, the gate's and then the up projection's.  bias [2n] bfloat16 or float32; gu
+    [m][2n] of d's type receives g and u; row_amax [m], col_amax [n] the maxima of |d|, ready to
+    be the amax_in of its quantization."""
+    m, n = _matrix(d)
+    od = NVFP4_OUT_FP32 if d.dtype == torch.float32 else NVFP4_OUT_BF16
+    _in_dtype(d)
+    k = a.codes.shape[1] * 2
+    if a.codes.shape[0] != m or b.codes.shape[0] != 2 * n or b.codes.shape[1] * 2 != k:
+        raise ValueError("operand shapes do not match d (b has twice d's columns)")
+    _operand_sizes("a", a, m, k)
+    _operand_sizes("b", b, 2 * n, k)
+    bd = _vector("bias", bias, 2 * n) if bias is not None else NVFP4_IN_FP32
+    epi = _CGatedEpilogue(_ptr(bias), bd, act, _like("gu", gu, (m, 2 * n), d.dtype),
+                          _floats("row_amax", row_amax, m), _floats("col_amax", col_amax, n))
+    _on_gpu(a.codes, a.scales, a.amax, b.codes, b.scales, b.amax, d, bias, gu, row_amax, col_amax,
+            workspace)
+    need = 0 if workspace is not None else nvfp4_gemm_gated_workspace_size(m, n, k)
+    workspace, size = _workspace(workspace, need, d.device, stream)
+    ca, cb = a._c(), b._c()
+    _check(load_library().nvfp4_gemm_gated(C.byref(ca), C.byref(cb), m, n, k, C.byref(epi),
+                                           _ptr(d), od, _ptr(workspace), size, _stream(stream)))
+
+
+def nvfp4_gated_backward_workspace_size(rows: int, cols: int) -> int:
+    v = C.c_uint64(0)
+    _check(load_library().nvfp4_gated_backward_workspace_size(rows, cols, C.byref(v)))
+    return v.value
+
+
+def nvfp4_gated_backward(dd: torch.Tensor, gu: torch.Tensor, act: int, dgu: torch.Tensor,
+                         dbias: Optional[torch.Tensor] = None,
+                         row_amax: Optional[torch.Tensor] = None,
+                         col_amax: Optional[torch.Tensor] = None,
+                         workspace: Optional[torch.Tensor] = None, stream=None) -> None:
+    """dgu [rows][2 cols] = [dd * u * act'(g) | dd * act(g)] for dd [rows][cols] and gu = [g | u],
+    dbias [2 cols] = its column sums, row_amax [rows] / col_amax [2 cols] = the maxima of |dgu|,
+    ready to be the amax_in of the quantization of dgu.  dgu may be gu."""
+    rows, cols = _matrix(dd)
+    both, dtype = (rows, 2 * cols), dd.dtype
+    args = (dd.data_ptr(), _like("gu", gu, both, dtype), _in_dtype(dd), act, rows, cols,
+            _like("dgu", dgu, both, dtype), _floats("dbias", dbias, 2 * cols),
+            _floats("row_amax", row_amax, rows), _floats("col_amax", col_amax, 2 * cols))
+    _on_gpu(dd, gu, dgu, dbias, row_amax, col_amax, workspace)
+    size = 0
+    if dbias is not None or row_amax is not None or col_amax is not None:
+        need = 0 if workspace is not None else nvfp4_gated_backward_workspace_size(rows, cols)
+        workspace, size = _workspace(workspace, need, dd.device, stream)
+    _check(load_library().nvfp4_gated_backward(*args, _ptr(workspace), size, _stream(stream)))
 
 
 def nvfp4_clip_grad_norm_workspace_size() -> int:

@@ -30,16 +30,22 @@ __device__ __forceinline__ float with_sign(float m, float z) {
   return __uint_as_float(__float_as_uint(m) | (__float_as_uint(z) & 0x80000000u));
 }
 
-// act'(z) of a pair.  GELU and SILU are z p(u), p = 1 / (1 + exp(-u)), u odd in z, so with
-// a = |z|, t = exp(-u(a)) <= 1 and r = 1 / (1 + t) = p(u(a)):
-//   act' = 1/2 + sgn(z) (r - 1/2 + a t r^2 u'(a)),
+// act'(z) of a pair, and its value.  GELU and SILU are z p(u), p = 1 / (1 + exp(-u)), u odd in z,
+// so with a = |z|, t = exp(-u(a)) <= 1 and r = 1 / (1 + t) = p(u(a)):
+//   act' = 1/2 + sgn(z) (r - 1/2 + a t r^2 u'(a)),   act = z r (z >= 0) or z t r,
 // where p (1 - p) = t r^2 is never the difference of 1 and a rounded p (it is multiplied by
 // a u' of up to 100 before it vanishes).  a is cut at 64, where t is 0 or below 2^-92, so that
-// 0 never meets an infinite u'; a NaN stays one.
+// 0 never meets an infinite u' (and the value of a z below -64 is 0); a NaN stays one.
 template <int ACT>
-__device__ __forceinline__ Pair act_slope(Pair z) {
-  if constexpr (ACT == kActRelu) return {z.x > 0.0f ? 1.0f : 0.0f, z.y > 0.0f ? 1.0f : 0.0f};
-  if constexpr (ACT != kActGelu && ACT != kActSilu) return {1.0f, 1.0f};
+__device__ __forceinline__ Pair act_slope(Pair z, Pair& value) {
+  if constexpr (ACT == kActRelu) {
+    value = {z.x < 0.0f ? 0.0f : z.x, z.y < 0.0f ? 0.0f : z.y};  // NaN stays
+    return {z.x > 0.0f ? 1.0f : 0.0f, z.y > 0.0f ? 1.0f : 0.0f};
+  }
+  if constexpr (ACT != kActGelu && ACT != kActSilu) {
+    value = z;
+    return {1.0f, 1.0f};
+  }
   constexpr float kLog2e = 1.4426950408889634f;
   Pair a;
   asm("min.NaN.f32 %0, %1, 0f42800000;" : "=f"(a.x) : "f"(fabsf(z.x)));
@@ -58,11 +64,19 @@ __device__ __forceinline__ Pair act_slope(Pair z) {
   const Pair t = {ex2_approx(-w.x), ex2_approx(-w.y)};
   const Pair one_t = pair_add(t, {1.0f, 1.0f});
   const Pair r = {rcp_approx(one_t.x), rcp_approx(one_t.y)};
-  const Pair q = pair_mul(pair_mul(t, r), r);
+  const Pair tr = pair_mul(t, r);
+  value = pair_mul(z, {z.x < 0.0f ? (z.x < -64.0f ? 0.0f : tr.x) : r.x,
+                       z.y < 0.0f ? (z.y < -64.0f ? 0.0f : tr.y) : r.y});
+  const Pair q = pair_mul(tr, r);
   Pair aq = pair_mul(a, q);
   if constexpr (ACT == kActGelu) aq = pair_mul(aq, du);
   const Pair m = pair_add(pair_add(r, {-0.5f, -0.5f}), aq);
   return pair_add({with_sign(m.x, z.x), with_sign(m.y, z.y)}, {0.5f, 0.5f});
+}
+template <int ACT>
+__device__ __forceinline__ Pair act_slope(Pair z) {
+  Pair value;
+  return act_slope<ACT>(z, value);
 }
 
 // act(z) of a pair: z p with p = 1 / (1 + 2^-w), w = u log2(e).

@@ -618,7 +618,7 @@ nvfp4_status gemm_impl(const nvfp4_operand* a, const nvfp4_operand* b, const int
                        int32_t num_groups, int64_t m, int64_t n, int64_t k, void* d,
                        int32_t out_dtype, void* workspace, uint64_t workspace_bytes,
                        nvfp4_stream_t stream, bool static_ws, bool k_grouped = false,
-                       const Epilogue* epilogue = nullptr) {
+                       const Epilogue* epilogue = nullptr, const GatedOut* gated = nullptr) {
   nvfp4_status st;
   if ((st = check_sizes(m, n)) != NVFP4_OK) return st;
   if ((st = check_sizes(k, 0)) != NVFP4_OK) return st;
@@ -631,14 +631,21 @@ nvfp4_status gemm_impl(const nvfp4_operand* a, const nvfp4_operand* b, const int
     if (!(o->bound == 448.0f || o->bound == 256.0f))
       return fail(NVFP4_ERR_INVALID, "operand bound must be 448 or 256");
   }
-  if (m == 0 || n == 0) return NVFP4_OK;
+  if (m == 0 || n == 0) {  // the maxima of nothing
+    cudaError_t e = cudaSuccess;
+    if (gated && gated->row_amax && m > 0) e = cudaMemsetAsync(gated->row_amax, 0, 4 * m, stream);
+    if (e == cudaSuccess && gated && gated->col_amax && n > 0)
+      e = cudaMemsetAsync(gated->col_amax, 0, 4 * n, stream);
+    return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "cudaMemsetAsync");
+  }
   if (d == nullptr) return fail(NVFP4_ERR_INVALID, "d is NULL");
   const size_t esize = out_dtype == NVFP4_OUT_BF16 ? 2 : 4;
   if (k == 0 && epilogue != nullptr) {  // the empty sum's epilogue
     DeviceInfo dev;
     if ((st = current_device(&dev)) != NVFP4_OK) return st;
-    cudaError_t e = launch_epilogue_only(*epilogue, d, out_dtype == NVFP4_OUT_BF16, m, n, dev,
-                                         stream);
+    const bool bf16 = out_dtype == NVFP4_OUT_BF16;
+    cudaError_t e = gated ? launch_gated_epilogue_only(*epilogue, *gated, d, bf16, m, n, dev, stream)
+                          : launch_epilogue_only(*epilogue, d, bf16, m, n, dev, stream);
     return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "epilogue launch");
   }
   if (k == 0) {  // the empty sum
@@ -658,8 +665,8 @@ nvfp4_status gemm_impl(const nvfp4_operand* a, const nvfp4_operand* b, const int
   if (k_grouped && k % 256 != 0)
     return fail(NVFP4_ERR_UNSUPPORTED, "grouped wgrad GEMM: tokens must be a multiple of 256");
   GemmLayout L = gemm_layout(m, n, k, group_ends && !k_grouped ? (int64_t)num_groups * n : n);
-  const bool few = epilogue != nullptr && gemm_few(m, n);
-  if (few) L.workspace_bytes = gemm_few_workspace(m, n);
+  const bool few = epilogue != nullptr && (gated != nullptr || gemm_few(m, n));
+  if (few) L.workspace_bytes = gemm_few_workspace(m, n, gated != nullptr);
   if (L.tiles_m * L.tiles_n >= (1LL << 31)) return fail(NVFP4_ERR_UNSUPPORTED, "too many tiles");
   if (static_ws) {
     if ((uint64_t)L.workspace_bytes > (uint64_t)NVFP4_GEMM_STATIC_WS_BYTES)
@@ -695,6 +702,7 @@ nvfp4_status gemm_impl(const nvfp4_operand* a, const nvfp4_operand* b, const int
   g.num_groups = num_groups;
   g.k_grouped = k_grouped;
   g.epilogue = epilogue;
+  g.gated = gated;
   cudaError_t e = few ? launch_gemm_few(g, dev, stream) : launch_gemm(g, dev, stream);
   if (e != cudaSuccess) return cuda_fail(e, "gemm launch");
   return NVFP4_OK;
@@ -712,7 +720,7 @@ nvfp4_status nvfp4_gemm_bias_act_workspace_size(int64_t m, int64_t n, int64_t k,
                                                 uint64_t* bytes) {
   const nvfp4_status st = nvfp4_gemm_workspace_size(m, n, k, bytes);
   if (st == NVFP4_OK && *bytes > 0 && gemm_few(m, n))
-    *bytes = (uint64_t)gemm_few_workspace(m, n);
+    *bytes = (uint64_t)gemm_few_workspace(m, n, false);
   return st;
 }
 
@@ -742,6 +750,42 @@ nvfp4_status nvfp4_gemm_bias_act(const nvfp4_operand* a, const nvfp4_operand* b,
                    epilogue->residual, epilogue->z};
   return gemm_impl(a, b, nullptr, 0, m, n, k, d, out_dtype, workspace, workspace_bytes, stream,
                    false, false, &e);
+}
+
+nvfp4_status nvfp4_gemm_gated_workspace_size(int64_t m, int64_t n, int64_t k, uint64_t* bytes) {
+  if (bytes == nullptr) return fail(NVFP4_ERR_INVALID, "bytes is NULL");
+  nvfp4_status st;
+  if ((st = check_gated_sizes(m, n)) != NVFP4_OK) return st;
+  if ((st = check_sizes(k, 0)) != NVFP4_OK) return st;
+  *bytes = (m == 0 || n == 0 || k == 0) ? 0 : (uint64_t)gemm_few_workspace(m, n, true);
+  return NVFP4_OK;
+}
+
+nvfp4_status nvfp4_gemm_gated(const nvfp4_operand* a, const nvfp4_operand* b, int64_t m, int64_t n,
+                              int64_t k, const nvfp4_gated_epilogue* epilogue, void* d,
+                              int32_t out_dtype, void* workspace, uint64_t workspace_bytes,
+                              nvfp4_stream_t stream) {
+  nvfp4_status st;
+  if (epilogue == nullptr) return fail(NVFP4_ERR_INVALID, "epilogue is NULL");
+  if (epilogue->bias != nullptr && !valid_in_dtype(epilogue->bias_dtype))
+    return fail(NVFP4_ERR_INVALID, "unknown bias_dtype");
+  if (!valid_activation(epilogue->act)) return fail(NVFP4_ERR_INVALID, "unknown activation");
+  if ((st = check_gated_sizes(m, n)) != NVFP4_OK) return st;
+  const int32_t dtype = out_dtype == NVFP4_OUT_FP32 ? NVFP4_IN_FP32 : NVFP4_IN_BF16;
+  if ((st = check_elems({d, epilogue->gu}, dtype)) != NVFP4_OK) return st;
+  if (epilogue->bias != nullptr &&
+      (st = check_elems({epilogue->bias}, epilogue->bias_dtype)) != NVFP4_OK)
+    return st;
+  if ((st = check_elems({epilogue->row_amax, epilogue->col_amax}, NVFP4_IN_FP32)) != NVFP4_OK)
+    return st;
+  const uint64_t bytes = (uint64_t)m * (uint64_t)n * (uint64_t)elem_bytes(dtype);
+  if (bytes_overlap(epilogue->gu, 2 * bytes, d, bytes))
+    return fail(NVFP4_ERR_INVALID, "gu overlaps d");
+  const Epilogue e{epilogue->bias, epilogue->bias_dtype == NVFP4_IN_BF16, epilogue->act, nullptr,
+                   nullptr};
+  const GatedOut g{epilogue->gu, epilogue->row_amax, epilogue->col_amax};
+  return gemm_impl(a, b, nullptr, 0, m, n, k, d, out_dtype, workspace, workspace_bytes, stream,
+                   false, false, &e, &g);
 }
 
 nvfp4_status nvfp4_grouped_gemm_workspace_size(int64_t rows, int64_t n, int64_t k,

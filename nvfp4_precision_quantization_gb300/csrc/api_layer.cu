@@ -1,5 +1,5 @@
-// api_layer.cu -- the C ABI of the layer operators (norm, bias and activation, gradient
-// clipping): argument checks and launches, by the conventions of api.cu.
+// api_layer.cu -- the C ABI of the layer operators (norms, dropout, bias and activation, the
+// gated activation, gradient clipping): argument checks and launches, by the conventions of api.cu.
 #include <memory>
 
 #include "api_common.h"
@@ -7,18 +7,6 @@
 using namespace nvfp4;
 
 namespace {
-
-bool aligned(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
-
-int64_t elem_bytes(int32_t dtype) { return dtype == NVFP4_IN_BF16 ? 2 : 4; }
-
-// Every pointer that is given must be aligned to its element.
-nvfp4_status check_elems(std::initializer_list<const void*> ptrs, int32_t dtype) {
-  for (const void* p : ptrs)
-    if (!aligned(p, elem_bytes(dtype)))
-      return fail(NVFP4_ERR_INVALID, "a tensor is not aligned to its element size");
-  return NVFP4_OK;
-}
 
 nvfp4_status check_norm(int32_t in_dtype, int32_t weight_dtype, const void* weight, int64_t rows,
                         int64_t cols) {
@@ -32,39 +20,38 @@ nvfp4_status check_norm(int32_t in_dtype, int32_t weight_dtype, const void* weig
   return check_elems({weight}, weight_dtype);
 }
 
-nvfp4_status check_workspace(const void* workspace, uint64_t have, uint64_t need) {
-  if (need == 0) return NVFP4_OK;
-  if (workspace == nullptr || !aligned(workspace, 16))
-    return fail(NVFP4_ERR_INVALID, "workspace must be non-NULL and 16-byte aligned");
-  if (have < need)
-    return fail(NVFP4_ERR_INVALID,
-                "workspace of " + std::to_string(have) + " bytes, " + std::to_string(need) +
-                    " needed");
+// A mask as the kernels take it (nothing is dropped without one).
+nvfp4_status make_mask(const nvfp4_mask* m, DropMask* out) {
+  *out = DropMask{};
+  if (m == nullptr) return NVFP4_OK;
+  if (!(m->p >= 0.0f && m->p <= 1.0f)) return fail(NVFP4_ERR_INVALID, "mask->p must be in [0, 1]");
+  if (!aligned(m->offset_add, 8))
+    return fail(NVFP4_ERR_INVALID, "mask->offset_add is not 8-byte aligned");
+  out->key0 = (uint32_t)m->seed;
+  out->key1 = (uint32_t)(m->seed >> 32);
+  out->threshold = (uint32_t)((double)m->p * 65536.0 + 0.5);
+  // (everything dropped: the scale is never used)
+  out->scale = out->threshold < 65536 ? (float)(65536.0 / (65536 - out->threshold)) : 0.0f;
+  out->offset = m->offset;
+  out->offset_add = reinterpret_cast<const unsigned long long*>(m->offset_add);
   return NVFP4_OK;
 }
 
-// Whether out shares bytes with in without starting where it starts (an element written
-// before another thread reads it).
-bool shifted(const void* out, const void* in, uint64_t bytes) {
-  return out != in && bytes_overlap(out, bytes, in, bytes);
-}
-
-}  // namespace
-
-extern "C" {
-
-nvfp4_status nvfp4_add_rmsnorm(const void* x, const void* residual, int32_t in_dtype,
-                               const void* weight, int32_t weight_dtype, int64_t rows,
-                               int64_t cols, float eps, void* h, void* y, float* rstd,
-                               const nvfp4_fp8_out* fp8, const nvfp4_config* cfg,
-                               const nvfp4_out* row, nvfp4_stream_t stream) {
+// The checks that both norms share, and the call's arguments.  What only the layer norm has
+// (bias, mask, mean) is in n already.
+nvfp4_status norm_impl(const void* x, const void* residual, int32_t in_dtype, const void* weight,
+                       int32_t weight_dtype, int64_t rows, int64_t cols, float eps, void* h,
+                       void* y, float* rstd, const nvfp4_fp8_out* fp8, const nvfp4_config* cfg,
+                       const nvfp4_out* row, NormArgs& n, bool sum_is_x,
+                       cudaError_t (*launch)(const NormArgs&, const DeviceInfo&, cudaStream_t),
+                       nvfp4_stream_t stream) {
   nvfp4_status st;
   if ((st = check_norm(in_dtype, weight_dtype, weight, rows, cols)) != NVFP4_OK) return st;
   if ((st = check_elems({x, residual, h, y}, in_dtype)) != NVFP4_OK) return st;
   if ((st = check_elems({rstd}, NVFP4_IN_FP32)) != NVFP4_OK) return st;
   if (!(eps >= 0.0f)) return fail(NVFP4_ERR_INVALID, "eps must be >= 0");
   if (x == nullptr && rows * cols > 0) return fail(NVFP4_ERR_INVALID, "x is NULL");
-  if (h != nullptr && residual == nullptr)
+  if (h != nullptr && sum_is_x)
     return fail(NVFP4_ERR_INVALID, "h is the sum with a residual: residual is NULL");
   if (rows * cols > 0 && y == nullptr && fp8 == nullptr && row == nullptr)
     return fail(NVFP4_ERR_INVALID, "no output: y, fp8 and row are NULL");
@@ -75,7 +62,6 @@ nvfp4_status nvfp4_add_rmsnorm(const void* x, const void* residual, int32_t in_d
   for (const void* in : {x, residual})
     if (shifted(h, in, bytes) || shifted(y, in, bytes))
       return fail(NVFP4_ERR_INVALID, "h or y overlaps x or residual without being it");
-  NormArgs n{};
   if (fp8 != nullptr) {
     if (fp8->block != 0 && fp8->block != 128)
       return fail(NVFP4_ERR_INVALID, "fp8->block must be 0 or 128");
@@ -123,8 +109,123 @@ nvfp4_status nvfp4_add_rmsnorm(const void* x, const void* residual, int32_t in_d
   n.h = h;
   n.y = y;
   n.rstd = rstd;
-  cudaError_t e = launch_add_rmsnorm(n, dev, stream);
+  cudaError_t e = launch(n, dev, stream);
   return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "norm launch");
+}
+
+}  // namespace
+
+extern "C" {
+
+nvfp4_status nvfp4_add_rmsnorm(const void* x, const void* residual, int32_t in_dtype,
+                               const void* weight, int32_t weight_dtype, int64_t rows,
+                               int64_t cols, float eps, void* h, void* y, float* rstd,
+                               const nvfp4_fp8_out* fp8, const nvfp4_config* cfg,
+                               const nvfp4_out* row, nvfp4_stream_t stream) {
+  NormArgs n{};
+  return norm_impl(x, residual, in_dtype, weight, weight_dtype, rows, cols, eps, h, y, rstd, fp8,
+                   cfg, row, n, residual == nullptr, launch_add_rmsnorm, stream);
+}
+
+nvfp4_status nvfp4_add_layernorm(const void* x, const void* residual, int32_t in_dtype,
+                                 const nvfp4_mask* mask, const void* weight, const void* bias,
+                                 int32_t weight_dtype, int64_t rows, int64_t cols, float eps,
+                                 void* h, void* y, float* mean, float* rstd,
+                                 const nvfp4_fp8_out* fp8, const nvfp4_config* cfg,
+                                 const nvfp4_out* row, nvfp4_stream_t stream) {
+  nvfp4_status st;
+  NormArgs n{};
+  if ((st = make_mask(mask, &n.mask)) != NVFP4_OK) return st;
+  if (!valid_in_dtype(weight_dtype)) return fail(NVFP4_ERR_INVALID, "unknown weight_dtype");
+  if ((st = check_elems({bias}, weight_dtype)) != NVFP4_OK) return st;
+  if ((st = check_elems({mean}, NVFP4_IN_FP32)) != NVFP4_OK) return st;
+  n.bias = bias;
+  n.mean = mean;
+  return norm_impl(x, residual, in_dtype, weight, weight_dtype, rows, cols, eps, h, y, rstd, fp8,
+                   cfg, row, n, residual == nullptr && mask == nullptr, launch_add_layernorm,
+                   stream);
+}
+
+nvfp4_status nvfp4_dropout(const void* x, const void* residual, int32_t dtype, int64_t n,
+                           const nvfp4_mask* mask, void* y, nvfp4_stream_t stream) {
+  nvfp4_status st;
+  if (!valid_in_dtype(dtype)) return fail(NVFP4_ERR_INVALID, "unknown dtype");
+  if (n < 0 || n >= (1LL << 48)) return fail(NVFP4_ERR_INVALID, "n must be in [0, 2^48)");
+  if (mask == nullptr) return fail(NVFP4_ERR_INVALID, "mask is NULL");
+  DropoutArgs a{};
+  if ((st = make_mask(mask, &a.mask)) != NVFP4_OK) return st;
+  if ((st = check_elems({x, residual, y}, dtype)) != NVFP4_OK) return st;
+  if (n > 0 && (x == nullptr || y == nullptr))
+    return fail(NVFP4_ERR_INVALID, "x and y must be non-NULL");
+  const uint64_t bytes = (uint64_t)(n * elem_bytes(dtype));
+  if (shifted(y, x, bytes) || shifted(y, residual, bytes))
+    return fail(NVFP4_ERR_INVALID, "y overlaps an input without being it");
+  DeviceInfo dev;
+  if ((st = current_device(&dev)) != NVFP4_OK) return st;
+  a.x = x;
+  a.residual = residual;
+  a.in = dtype == NVFP4_IN_BF16 ? InType::BF16 : InType::FP32;
+  a.n = n;
+  a.y = y;
+  cudaError_t e = launch_dropout(a, dev, stream);
+  return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "dropout launch");
+}
+
+nvfp4_status nvfp4_add_layernorm_backward_workspace_size(int64_t rows, int64_t cols,
+                                                         uint64_t* bytes) {
+  if (bytes == nullptr) return fail(NVFP4_ERR_INVALID, "bytes is NULL");
+  nvfp4_status st = check_sizes(rows, cols);
+  if (st != NVFP4_OK) return st;
+  *bytes = (uint64_t)add_layernorm_backward_workspace(rows, cols);
+  return NVFP4_OK;
+}
+
+nvfp4_status nvfp4_add_layernorm_backward(
+    const void* dy, const void* h, const void* dh, int32_t in_dtype, const nvfp4_mask* mask,
+    const void* weight, int32_t weight_dtype, const float* mean, const float* rstd, int64_t rows,
+    int64_t cols, void* dx, void* dresidual, float* dweight, float* dbias, void* workspace,
+    uint64_t workspace_bytes, nvfp4_stream_t stream) {
+  nvfp4_status st;
+  NormBackwardArgs n{};
+  if ((st = make_mask(mask, &n.mask)) != NVFP4_OK) return st;
+  if ((st = check_norm(in_dtype, weight_dtype, weight, rows, cols)) != NVFP4_OK) return st;
+  if ((st = check_elems({dy, h, dh, dx, dresidual}, in_dtype)) != NVFP4_OK) return st;
+  if ((st = check_elems({mean, rstd, dweight, dbias}, NVFP4_IN_FP32)) != NVFP4_OK) return st;
+  if (rows * cols > 0 && (dy == nullptr || h == nullptr || mean == nullptr || rstd == nullptr ||
+                          dx == nullptr))
+    return fail(NVFP4_ERR_INVALID, "dy, h, mean, rstd and dx must be non-NULL");
+  if (dresidual != nullptr && mask == nullptr)
+    return fail(NVFP4_ERR_INVALID, "without a mask dx is the residual's gradient too: dresidual "
+                                   "must be NULL");
+  const uint64_t bytes = (uint64_t)(rows * cols * elem_bytes(in_dtype));
+  for (const void* in : {dy, h, dh})
+    if (shifted(dx, in, bytes) || shifted(dresidual, in, bytes))
+      return fail(NVFP4_ERR_INVALID, "dx or dresidual overlaps an input without being it");
+  if (bytes_overlap(dx, bytes, dresidual, bytes))
+    return fail(NVFP4_ERR_INVALID, "dx overlaps dresidual");
+  if ((dweight != nullptr || dbias != nullptr) &&
+      (st = check_workspace(workspace, workspace_bytes,
+                            (uint64_t)add_layernorm_backward_workspace(rows, cols))) != NVFP4_OK)
+    return st;
+  DeviceInfo dev;
+  if ((st = current_device(&dev)) != NVFP4_OK) return st;
+  n.dy = dy;
+  n.h = h;
+  n.dh = dh;
+  n.in = in_dtype == NVFP4_IN_BF16 ? InType::BF16 : InType::FP32;
+  n.weight = weight;
+  n.weight_bf16 = weight_dtype == NVFP4_IN_BF16;
+  n.mean = mean;
+  n.rstd = rstd;
+  n.rows = rows;
+  n.cols = cols;
+  n.dx = dx;
+  n.dresidual = dresidual;
+  n.dweight = dweight;
+  n.dbias = dbias;
+  n.workspace = workspace;
+  cudaError_t e = launch_add_layernorm_backward(n, dev, stream);
+  return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "layer norm backward launch");
 }
 
 nvfp4_status nvfp4_add_rmsnorm_backward_workspace_size(int64_t rows, int64_t cols,
@@ -222,6 +323,52 @@ nvfp4_status nvfp4_bias_act_backward(const void* dd, const void* z, int32_t dtyp
   a.workspace = workspace;
   cudaError_t e = launch_bias_act_backward(a, dev, stream);
   return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "activation backward launch");
+}
+
+nvfp4_status nvfp4_gated_backward_workspace_size(int64_t rows, int64_t cols, uint64_t* bytes) {
+  if (bytes == nullptr) return fail(NVFP4_ERR_INVALID, "bytes is NULL");
+  nvfp4_status st = check_gated_sizes(rows, cols);
+  if (st != NVFP4_OK) return st;
+  *bytes = rows * cols > 0 ? (uint64_t)gated_backward_workspace(rows, cols) : 0;
+  return NVFP4_OK;
+}
+
+nvfp4_status nvfp4_gated_backward(const void* dd, const void* gu, int32_t dtype, int32_t act,
+                                  int64_t rows, int64_t cols, void* dgu, float* dbias,
+                                  float* row_amax, float* col_amax, void* workspace,
+                                  uint64_t workspace_bytes, nvfp4_stream_t stream) {
+  nvfp4_status st;
+  if (!valid_in_dtype(dtype)) return fail(NVFP4_ERR_INVALID, "unknown dtype");
+  if (!valid_activation(act)) return fail(NVFP4_ERR_INVALID, "unknown activation");
+  if ((st = check_gated_sizes(rows, cols)) != NVFP4_OK) return st;
+  if ((st = check_elems({dd, gu, dgu}, dtype)) != NVFP4_OK) return st;
+  if ((st = check_elems({dbias, row_amax, col_amax}, NVFP4_IN_FP32)) != NVFP4_OK) return st;
+  if (rows * cols > 0 && (dd == nullptr || gu == nullptr || dgu == nullptr))
+    return fail(NVFP4_ERR_INVALID, "dd, gu and dgu must be non-NULL");
+  const uint64_t bytes = (uint64_t)(rows * cols * elem_bytes(dtype));
+  if (bytes_overlap(dgu, 2 * bytes, dd, bytes)) return fail(NVFP4_ERR_INVALID, "dgu overlaps dd");
+  if (shifted(dgu, gu, 2 * bytes))
+    return fail(NVFP4_ERR_INVALID, "dgu overlaps gu without being it");
+  if (rows * cols > 0 && (dbias || row_amax || col_amax) &&
+      (st = check_workspace(workspace, workspace_bytes,
+                            (uint64_t)gated_backward_workspace(rows, cols))) != NVFP4_OK)
+    return st;
+  DeviceInfo dev;
+  if ((st = current_device(&dev)) != NVFP4_OK) return st;
+  GatedBackwardArgs a{};
+  a.dd = dd;
+  a.gu = gu;
+  a.in = dtype == NVFP4_IN_BF16 ? InType::BF16 : InType::FP32;
+  a.act = act;
+  a.rows = rows;
+  a.cols = cols;
+  a.dgu = dgu;
+  a.dbias = dbias;
+  a.row_amax = row_amax;
+  a.col_amax = col_amax;
+  a.workspace = workspace;
+  cudaError_t e = launch_gated_backward(a, dev, stream);
+  return e == cudaSuccess ? NVFP4_OK : cuda_fail(e, "gated backward launch");
 }
 
 nvfp4_status nvfp4_clip_grad_norm_workspace_size(uint64_t* bytes) {

@@ -218,8 +218,17 @@ struct Epilogue {
   }
 #endif
 };
+// Beside an Epilogue (bias [2N], act): what the gated product d = act(g) u keeps.
+struct GatedOut {
+  void* gu;         // [M][2N] of D's type, g's columns first, or NULL
+  float* row_amax;  // [M] or NULL: max |d| as stored
+  float* col_amax;  // [N] or NULL
+};
 cudaError_t launch_epilogue_only(const Epilogue& e, void* d, bool bf16, int64_t m, int64_t n,
                                  const DeviceInfo& dev, cudaStream_t stream);
+cudaError_t launch_gated_epilogue_only(const Epilogue& e, const GatedOut& g, void* d, bool bf16,
+                                       int64_t m, int64_t n, const DeviceInfo& dev,
+                                       cudaStream_t stream);
 
 struct GemmArgs {
   const uint8_t* a_codes;
@@ -246,10 +255,11 @@ struct GemmArgs {
   // a_amax [num_groups*M] or [num_groups], b_amax [num_groups*N] or [num_groups]
   bool k_grouped;
   const Epilogue* epilogue;  // optional, not with groups
+  const GatedOut* gated;     // the gated product (with an epilogue): B has 2N lines
 };
 // Few rows of A, or few tiles (kernels_gemm_few.cu), with an epilogue.
 bool gemm_few(int64_t m, int64_t n);
-int64_t gemm_few_workspace(int64_t m, int64_t n);  // bytes
+int64_t gemm_few_workspace(int64_t m, int64_t n, bool gated);  // bytes
 cudaError_t launch_gemm_few(const GemmArgs& a, const DeviceInfo& dev, cudaStream_t stream);
 struct GemmLayout {
   int64_t k_tiles, tiles_m, tiles_n;
@@ -259,17 +269,41 @@ struct GemmLayout {
 GemmLayout gemm_layout(int64_t M, int64_t N, int64_t K, int64_t b_lines);
 cudaError_t launch_gemm(const GemmArgs& a, const DeviceInfo& dev, cudaStream_t stream);
 
-// Residual addition and RMS norm of each row (kernels_norm.cu).
+// A dropout mask (dropout.cuh): an element is dropped where its 16 bits are below threshold.
+struct DropMask {
+  uint32_t key0, key1;   // of the seed
+  uint32_t threshold;    // 0 (nothing is dropped) .. 65536 (everything is)
+  float scale;           // of what is kept
+  uint64_t offset;
+  const unsigned long long* offset_add;  // device, or NULL
+};
+
+// y = residual + drop(x) of n elements (kernels_dropout.cu).
+struct DropoutArgs {
+  const void* x;
+  const void* residual;  // or NULL
+  InType in;
+  int64_t n;
+  DropMask mask;
+  void* y;
+};
+cudaError_t launch_dropout(const DropoutArgs& a, const DeviceInfo& dev, cudaStream_t stream);
+
+// Residual addition and norm of each row: RMS (kernels_norm.cu) or layer norm
+// (kernels_layernorm.cu; x through the mask, bias and mean are its own).
 struct NormArgs {
   const void* x;
   const void* residual;  // or NULL
   InType in;
+  DropMask mask;
   const void* weight;
+  const void* bias;  // of the weight's type, or NULL
   bool weight_bf16;
   int64_t rows, cols;
   float eps;
   void* h;      // or NULL
   void* y;      // or NULL
+  float* mean;  // or NULL
   float* rstd;  // or NULL
   // E4M3 output (q8 == NULL: none): a scale per row or per q8_block (128) columns
   uint8_t* q8;
@@ -285,6 +319,7 @@ struct NormArgs {
   float bound;
 };
 cudaError_t launch_add_rmsnorm(const NormArgs& a, const DeviceInfo& dev, cudaStream_t stream);
+cudaError_t launch_add_layernorm(const NormArgs& a, const DeviceInfo& dev, cudaStream_t stream);
 
 struct NormBackwardArgs {
   const void* dy;
@@ -297,12 +332,20 @@ struct NormBackwardArgs {
   int64_t rows, cols;
   void* dx;
   float* dweight;   // or NULL
-  void* workspace;  // >= add_rmsnorm_backward_workspace(rows, cols) bytes with dweight
+  void* workspace;  // >= add_{rms,layer}norm_backward_workspace(rows, cols) bytes with dweight
+  // layer norm alone
+  DropMask mask;
+  const float* mean;
+  void* dresidual;  // or NULL
+  float* dbias;     // or NULL
 };
 constexpr int64_t kNormBackwardParts = 608;  // at most this many CTAs, one partial dw each
 int64_t add_rmsnorm_backward_workspace(int64_t rows, int64_t cols);
 cudaError_t launch_add_rmsnorm_backward(const NormBackwardArgs& a, const DeviceInfo& dev,
                                         cudaStream_t stream);
+int64_t add_layernorm_backward_workspace(int64_t rows, int64_t cols);
+cudaError_t launch_add_layernorm_backward(const NormBackwardArgs& a, const DeviceInfo& dev,
+                                          cudaStream_t stream);
 
 // Gradients of bias and activation (kernels_act.cu).
 struct ActBackwardArgs {
@@ -320,6 +363,24 @@ struct ActBackwardArgs {
 int64_t bias_act_backward_workspace(int64_t rows, int64_t cols);
 cudaError_t launch_bias_act_backward(const ActBackwardArgs& a, const DeviceInfo& dev,
                                      cudaStream_t stream);
+
+// Gradients of d = act(g) u (kernels_gated_act.cu): gu and dgu are [rows][2 cols], g's columns
+// first.
+struct GatedBackwardArgs {
+  const void* dd;
+  const void* gu;
+  InType in;
+  int act;
+  int64_t rows, cols;
+  void* dgu;
+  float* dbias;     // [2 cols] or NULL
+  float* row_amax;  // [rows] or NULL
+  float* col_amax;  // [2 cols] or NULL
+  void* workspace;  // >= gated_backward_workspace(rows, cols) bytes unless all three are NULL
+};
+int64_t gated_backward_workspace(int64_t rows, int64_t cols);
+cudaError_t launch_gated_backward(const GatedBackwardArgs& a, const DeviceInfo& dev,
+                                  cudaStream_t stream);
 
 // Global norm of a list of tensors, and clipping by it (kernels_clip.cu).
 struct TensorEntry {

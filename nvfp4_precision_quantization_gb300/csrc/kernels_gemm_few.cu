@@ -13,6 +13,9 @@
 //     of a line at a time (16 bytes of a line alone would fetch a 64-byte burst for each
 //     unit): asynchronous copies to shared memory a group ahead, from there to registers
 //     and into tensor memory.
+// GATED (the gated product, D = act(A Bg^T + bg) (A Bu^T + bu), B's lines the gate's and then
+// the up projection's): a tile is 128 lines of each, in two accumulators, so that a lane of the
+// epilogue holds both factors of its column; a unit is 256 values of the 256 lines.
 // Warps: 0 loads codes (TMA, a ring of S stages), 1 issues the MMAs, 2-5 copy scales and
 // write them to TMEM (one per lane quarter), 6-9 are the epilogue (two accumulators, so the
 // next tile's MMAs run meanwhile).  Lane l of the accumulator is line l of B, so a warp
@@ -36,13 +39,20 @@ namespace {
 
 constexpr int kLines = 128;     // lines of B per tile = MMA M
 constexpr int kBoxBytes = 128;  // code bytes of a line per TMA box: 256 values
-// Boxes per unit: 512 values, eight MMAs.  (One box a unit measured 0.42 us a unit on rows
-// where memory does not bound, most of it the waits and issues of single threads.)
+// Boxes of B per unit, eight MMAs: 512 values of 128 lines, or (GATED) 256 values of 128 lines
+// of either half of B.  (One box a unit measured 0.42 us a unit on rows where memory does not
+// bound, most of it the waits and issues of single threads.)
 constexpr int kBoxes = 2;
-constexpr int kUnitBytes = kBoxes * kBoxBytes;
-constexpr int kUnitScales = kUnitBytes / 8;
-constexpr int kMmas = kUnitBytes / 32;      // K = 64 each
-constexpr int kSlotCols = 2 * 4 * kMmas;    // TMEM columns of a unit's scales: B's, A's
+template <bool GATED>
+struct Unit {
+  static constexpr int kHalves = GATED ? 2 : 1;       // of B, an accumulator each
+  static constexpr int kKBoxes = kBoxes / kHalves;    // along K
+  static constexpr int kBytes = kKBoxes * kBoxBytes;  // of a line
+  static constexpr int kScales = kBytes / 8;
+  static constexpr int kSteps = kBytes / 32;          // MMAs along K, 64 values each
+  static constexpr int kSlotCols = (kHalves + 1) * 4 * kSteps;  // TMEM columns of a unit's
+                                                                // scales: B's halves, A's
+};
 constexpr int kEpiWarps = 4;     // one per TMEM lane quarter
 constexpr int kFewThreads = 32 * (6 + kEpiWarps);
 constexpr int kMaxCtas = 160;   // bound of the grid, for the workspace
@@ -64,17 +74,18 @@ struct FewParams {
   void* d;
   bool d_bf16;
   Epilogue epi;
+  GatedOut gated;      // GATED
   uint32_t* arrivals;  // [split], zero before the kernel's first arrival
-  float4* sums;        // [split][parts][NT / 4][128] partial sums, four rows of A each
+  float4* sums;        // [split][parts][halves][NT / 4][128] partial sums, four rows of A each
   uint32_t idesc;
   int* status;
 };
 
 // Scales of a group of kGroup units, one row of shared memory per line.  The pitch is an
 // odd number of 16-byte units, so lanes reading their own lines meet no bank conflict.
-template <int kGroup>
+template <int kGroup, bool GATED>
 struct ScaleRows {
-  static constexpr int kRowBytes = kGroup * kUnitScales;
+  static constexpr int kRowBytes = kGroup * Unit<GATED>::kScales;
   static constexpr int kPitch = kRowBytes + 16;
 };
 
@@ -93,11 +104,11 @@ __device__ __forceinline__ void cp_async_wait_all() {
 //   grain 16: rows and base are 16-byte aligned; 2: the base is, and the 16-byte units that
 //   cover a row's part are copied, so that it starts 0 to 14 bytes (k16 is even) into its row
 //   of dst; no byte outside the tensor is read; 1: bytes, not asynchronously.
-template <int kGroup>
+template <class ROWS>
 __device__ __forceinline__ void copy_lines(const uint8_t* sc, int64_t k16, int64_t total,
                                            int64_t first, int lines, int64_t b0, int grain,
                                            uint8_t* dst, int t) {
-  constexpr int kRow = ScaleRows<kGroup>::kRowBytes, kPitch = ScaleRows<kGroup>::kPitch;
+  constexpr int kRow = ROWS::kRowBytes, kPitch = ROWS::kPitch;
   const int bytes = (int)min((int64_t)kRow, k16 - b0);
   const int rows = (int)min((int64_t)lines, total - first);
   // four warps issue this between units: pointers step by constants, nothing is divided
@@ -130,8 +141,10 @@ __device__ __forceinline__ void copy_lines(const uint8_t* sc, int64_t k16, int64
 
 // The scales of unit e of the group, of the line at src, as words (one per MMA); those from n
 // on zero (they belong to the next line).  shift: where in its first 16 bytes the row starts.
+template <int kMmas>
 __device__ __forceinline__ void read_scales(const uint8_t* src, int e, int shift, int n,
                                             uint32_t* w) {
+  constexpr int kUnitScales = 4 * kMmas;
   const uint8_t* p = src + kUnitScales * e;
   if (shift == 0) {
 #pragma unroll
@@ -256,27 +269,95 @@ __device__ __forceinline__ void few_store(const FewParams& p, int row, int col, 
 
 // NT: rows of A per MMA (its N); S: stages of the code ring and of the TMEM scale slots;
 // kGroup: units per scale copy (two groups in shared memory).
-template <int NT, int S, int kGroup>
+template <int NT, int S, int kGroup, bool GATED>
 struct FewGeom {
-  static constexpr int kABytes = kLines * kUnitBytes;
-  static constexpr int kStageBytes = kABytes + NT * kUnitBytes;
+  using U = Unit<GATED>;
+  static constexpr int kABytes = kLines * kBoxes * kBoxBytes;
+  static constexpr int kStageBytes = kABytes + NT * U::kBytes;
   // (32 rows at least: every lane reads one)
-  static constexpr int kScaleBytes = (kLines + (NT < 32 ? 32 : NT)) * ScaleRows<kGroup>::kPitch;
+  static constexpr int kScaleBytes =
+      (U::kHalves * kLines + (NT < 32 ? 32 : NT)) * ScaleRows<kGroup, GATED>::kPitch;
   static constexpr int kSmemBytes =
       S * kStageBytes + 2 * kScaleBytes + 512 /* barriers */ + 1024 /* alignment */;
-  static constexpr int kSfCol0 = 2 * NT;  // two accumulators, then the scale slots
+  // two accumulators (of each half), then the scale slots
+  static constexpr int kSfCol0 = 2 * U::kHalves * NT;
   static constexpr int kTmemCols = 512;
-  static_assert(kSfCol0 + kSlotCols * S <= kTmemCols, "TMEM columns");
+  static_assert(kSfCol0 + U::kSlotCols * S <= kTmemCols, "TMEM columns");
   static_assert(kStageBytes % 1024 == 0, "128B swizzle");
   static_assert(kScaleBytes % 16 == 0, "16-byte rows");
   static_assert(kSmemBytes + kEpiWarps * NT * 4 <= 232448, "shared memory");
 };
 
-template <int NT, int S, int kGroup>
+// Rows row .. row + R - 1 of one column (live: there is one) of the gated product: g and u the
+// scaled sums of its halves, d = act(g) u; cmax, the column's maximum of |d| as stored, grows.
+template <int R>
+__device__ __forceinline__ void few_store_gated(const FewParams& p, int row, int col, bool live,
+                                                float* g, float* u, const float* alpha,
+                                                const float (&beta)[2], const float (&bias)[2],
+                                                float& cmax, int lane) {
+  static_assert(R == 16, "the reduction below is of 16 rows");
+#pragma unroll
+  for (int j = 0; j < R; ++j) {
+    g[j] = __fadd_rn(__fmul_rn(__fmul_rn(g[j], alpha[j]), beta[0]), bias[0]);
+    u[j] = __fadd_rn(__fmul_rn(__fmul_rn(u[j], alpha[j]), beta[1]), bias[1]);
+  }
+  const int rows = live ? p.m - row : 0;
+  auto store = [&](void* base, int64_t at, int64_t pitch, const float* v) {
+    if (p.d_bf16) {
+      __nv_bfloat16* o = static_cast<__nv_bfloat16*>(base) + at;
+#pragma unroll
+      for (int j = 0; j < R; ++j)
+        if (j < rows) o[(int64_t)j * pitch] = __float2bfloat16_rn(v[j]);
+    } else {
+      float* o = static_cast<float*>(base) + at;
+#pragma unroll
+      for (int j = 0; j < R; ++j)
+        if (j < rows) o[(int64_t)j * pitch] = v[j];
+    }
+  };
+  if (p.gated.gu != nullptr) {
+    const int64_t at = (int64_t)row * 2 * p.n + col;
+    store(p.gated.gu, at, 2 * (int64_t)p.n, g);
+    store(p.gated.gu, at + p.n, 2 * (int64_t)p.n, u);
+  }
+  apply_act<R>(p.epi.act, g);
+#pragma unroll
+  for (int j = 0; j < R; ++j) g[j] = __fmul_rn(g[j], u[j]);
+  store(p.d, (int64_t)row * p.n + col, p.n, g);
+  if (p.gated.row_amax == nullptr && p.gated.col_amax == nullptr) return;
+#pragma unroll
+  for (int j = 0; j < R; ++j) {
+    const float as = p.d_bf16 ? __bfloat162float(__float2bfloat16_rn(g[j])) : g[j];
+    g[j] = j < rows ? fmaxf(fabsf(as), 0.0f) : 0.0f;  // NaN skipped
+    cmax = fmaxf(cmax, g[j]);
+  }
+  if (p.gated.row_amax == nullptr) return;
+  // the rows' maxima over the lanes: half of the rows go with each step, so lane l ends with row
+  // l / 2
+#pragma unroll
+  for (int d = 16, n = R / 2; n > 0; d >>= 1, n >>= 1) {
+    const bool upper = lane & d;
+#pragma unroll
+    for (int j = 0; j < n; ++j) {
+      const float give = upper ? g[j] : g[j + n], keep = upper ? g[j + n] : g[j];
+      g[j] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, d));
+    }
+  }
+  g[0] = fmaxf(g[0], __shfl_xor_sync(0xffffffffu, g[0], 1));
+  // non-negative floats are ordered like their bits, and a maximum does not depend on its order
+  const int at = row + (lane >> 1);
+  if (!(lane & 1) && at < p.m)
+    atomicMax(reinterpret_cast<int*>(p.gated.row_amax) + at, __float_as_int(g[0]));
+}
+
+template <int NT, int S, int kGroup, bool GATED>
 __global__ void __launch_bounds__(kFewThreads, 1)
     k_gemm_few(const __grid_constant__ CUtensorMap map_w, const __grid_constant__ CUtensorMap map_x,
                const FewParams p) {
-  using G = FewGeom<NT, S, kGroup>;
+  using G = FewGeom<NT, S, kGroup, GATED>;
+  using U = Unit<GATED>;
+  using Rows = ScaleRows<kGroup, GATED>;
+  constexpr int kSteps = U::kSteps;
   constexpr int kXGroups = (NT + 31) / 32;  // 32-row groups of A: TMEM columns of its scales
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
@@ -336,9 +417,11 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         mbar_expect_tx(&full[s], G::kStageBytes);
 #pragma unroll
         for (int b = 0; b < kBoxes; ++b) {  // a box past K is all zeros
-          const int x = kt * kUnitBytes + b * kBoxBytes;
-          tma_load_2d(st + b * kLines * kBoxBytes, &map_w, &full[s], x, line0, pol_w);
-          tma_load_2d(st + G::kABytes + b * NT * kBoxBytes, &map_x, &full[s], x, row0, pol_x);
+          const int x = kt * U::kBytes + b % U::kKBoxes * kBoxBytes;
+          const int line = line0 + b / U::kKBoxes * p.n;
+          tma_load_2d(st + b * kLines * kBoxBytes, &map_w, &full[s], x, line, pol_w);
+          if (b < U::kKBoxes)
+            tma_load_2d(st + G::kABytes + b * NT * kBoxBytes, &map_x, &full[s], x, row0, pol_x);
         }
       }
     }
@@ -369,13 +452,16 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         }
         tc_fence_after();
         const uint32_t st = smem_addr(smem + s * G::kStageBytes);
-        const uint32_t sf = tmem + G::kSfCol0 + kSlotCols * s;
+        const uint32_t sf = tmem + G::kSfCol0 + U::kSlotCols * s;
 #pragma unroll
-        for (int ks = 0; ks < kMmas; ++ks) {
+        for (int i = 0; i < U::kHalves * kSteps; ++i) {
+          const int ks = i / U::kHalves, half = i % U::kHalves;
           const int box = ks / 4, at = 32 * (ks % 4);
-          tc_mma_nvf4(tmem + b * NT, desc_swz128(st + box * kLines * kBoxBytes + at),
+          tc_mma_nvf4(tmem + (b * U::kHalves + half) * NT,
+                      desc_swz128(st + (half * U::kKBoxes + box) * kLines * kBoxBytes + at),
                       desc_swz128(st + G::kABytes + box * NT * kBoxBytes + at), p.idesc,
-                      sf + 4 * ks, sf + 4 * kMmas + 4 * ks, kt != w.kt || ks != 0);
+                      sf + 4 * (half * kSteps + ks), sf + 4 * (U::kHalves * kSteps + ks),
+                      kt != w.kt || ks != 0);
         }
         tc_commit(&empty[s]);
       }
@@ -389,14 +475,17 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     // the scales of the tile's rows of A
     const int q = warp & 3, t = threadIdx.x - 64;
     const uint32_t lanes = (uint32_t)(q * 32) << 16;
-    constexpr int kPitch = ScaleRows<kGroup>::kPitch;
+    constexpr int kPitch = Rows::kPitch, kBLines = U::kHalves * kLines;
     auto copy = [&](const Walk& w, int kt, int slot) {
-      const int64_t b0 = (int64_t)(kt / kGroup) * ScaleRows<kGroup>::kRowBytes;
+      const int64_t b0 = (int64_t)(kt / kGroup) * Rows::kRowBytes;
       uint8_t* dst = scale_smem + slot * G::kScaleBytes;
-      copy_lines<kGroup>(p.w_scales, p.k16, p.n, (int64_t)(w.tile / p.m_tiles) * kLines, kLines,
-                         b0, p.w_grain, dst, t);
-      copy_lines<kGroup>(p.x_scales, p.k16, p.m, (int64_t)(w.tile % p.m_tiles) * NT, NT, b0,
-                         p.x_grain, dst + kLines * kPitch, t);
+#pragma unroll
+      for (int h = 0; h < U::kHalves; ++h)
+        copy_lines<Rows>(p.w_scales, p.k16, (int64_t)(h + 1) * p.n,
+                         (int64_t)h * p.n + (int64_t)(w.tile / p.m_tiles) * kLines, kLines, b0,
+                         p.w_grain, dst + h * kLines * kPitch, t);
+      copy_lines<Rows>(p.x_scales, p.k16, p.m, (int64_t)(w.tile % p.m_tiles) * NT, NT, b0,
+                       p.x_grain, dst + kBLines * kPitch, t);
     };
     // `w` walks the copies, one group of units ahead of those written to TMEM
     Walk w(p);
@@ -423,34 +512,42 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       const int64_t line = (int64_t)(tile / p.m_tiles) * kLines + 32 * q + lane;
       const int64_t row = (int64_t)(tile % p.m_tiles) * NT + lane;
       const uint8_t* w_row = scale_smem + slot * G::kScaleBytes + (32 * q + lane) * kPitch;
-      const uint8_t* x_row = scale_smem + slot * G::kScaleBytes + (kLines + lane) * kPitch;
+      const uint8_t* x_row = scale_smem + slot * G::kScaleBytes + (kBLines + lane) * kPitch;
       // a row's part starts where the row does, 16 bytes times a whole number further on
-      const int w_shift = p.w_grain == 2 ? (int)((line * p.k16) & 15) : 0;
+      int w_shift[U::kHalves];
+#pragma unroll
+      for (int h = 0; h < U::kHalves; ++h)
+        w_shift[h] = p.w_grain == 2 ? (int)(((line + (int64_t)h * p.n) * p.k16) & 15) : 0;
       for (; kt < end; ++kt, ++it) {
         const int e = kt % kGroup;
-        const int n = (int)min((int64_t)kUnitScales, p.k16 - (int64_t)kt * kUnitScales);
-        uint32_t wa[kMmas], wb[kXGroups][kMmas];
-        read_scales(w_row, e, w_shift, n, wa);
+        const int n = (int)min((int64_t)U::kScales, p.k16 - (int64_t)kt * U::kScales);
+        uint32_t wa[U::kHalves][kSteps], wb[kXGroups][kSteps];
+#pragma unroll
+        for (int h = 0; h < U::kHalves; ++h)
+          read_scales<kSteps>(w_row + h * kLines * kPitch, e, w_shift[h], n, wa[h]);
 #pragma unroll
         for (int c = 0; c < kXGroups; ++c)
-          read_scales(x_row + (NT >= 32 ? 32 * c : 0) * kPitch, e,
-                      p.x_grain == 2 ? (int)(((row + 32 * c) * p.k16) & 15) : 0, n, wb[c]);
+          read_scales<kSteps>(x_row + (NT >= 32 ? 32 * c : 0) * kPitch, e,
+                              p.x_grain == 2 ? (int)(((row + 32 * c) * p.k16) & 15) : 0, n, wb[c]);
         const uint32_t st = it % S;
         if (ok && it >= (uint32_t)S) ok = mbar_wait_bounded(&empty[st], ((it / S) - 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) continue;  // to the group's end, where the four warps leave together
         tc_fence_after();
-        const uint32_t sf = tmem + lanes + G::kSfCol0 + kSlotCols * st;
+        const uint32_t sf = tmem + lanes + G::kSfCol0 + U::kSlotCols * st;
 #pragma unroll
-        for (int m = 0; m < kMmas; m += 4) {
+        for (int m = 0; m < kSteps; m += 4) {
           uint32_t r[16];
 #pragma unroll
-          for (int k = 0; k < 16; ++k) r[k] = wa[m + (k >> 2)];  // read at column q of each four
-          tmem_st16(sf + 4 * m, r);
+          for (int h = 0; h < U::kHalves; ++h) {
+#pragma unroll
+            for (int k = 0; k < 16; ++k) r[k] = wa[h][m + (k >> 2)];  // read at column q of each four
+            tmem_st16(sf + 4 * (h * kSteps + m), r);
+          }
 #pragma unroll
           for (int k = 0; k < 16; ++k)
             r[k] = (k & 3) < kXGroups ? wb[(k & 3) < kXGroups ? (k & 3) : 0][m + (k >> 2)] : 0u;
-          tmem_st16(sf + 4 * kMmas + 4 * m, r);
+          tmem_st16(sf + 4 * (U::kHalves * kSteps + m), r);
         }
         tmem_st_wait();
         tc_fence_before();
@@ -478,39 +575,57 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                                         p.x_finv)
                             : 0.0f;
       __syncwarp();
-      float beta = 0.0f, bias = 0.0f;
-      if (live) {
-        beta = __fmul_rn(__ldg(p.w_amax + (int64_t)col * p.w_amax_stride), p.w_finv);
-        bias = p.epi.bias_at(col);
+      float beta[U::kHalves], bias[U::kHalves], cmax = 0.0f;
+#pragma unroll
+      for (int h = 0; h < U::kHalves; ++h) {
+        beta[h] = bias[h] = 0.0f;
+        if (live) {
+          const int line = col + h * p.n;
+          beta[h] = __fmul_rn(__ldg(p.w_amax + (int64_t)line * p.w_amax_stride), p.w_finv);
+          bias[h] = p.epi.bias_at(line);
+        }
       }
       // the residual is loaded 16 rows ahead of its use, the first before the sums are ready
       // (not for a part: whoever joins the tile may be writing d, which may be the residual)
       float r[16];
-      if (live && whole) few_residual<16>(p, row0, col, r);
+      if (!GATED && live && whole) few_residual<16>(p, row0, col, r);
       const bool ready = mbar_wait_bounded(&acc_full[b], (seg >> 1) & 1);
       if (!ready) *err = 1;
       if (barrier_or<1, 32 * kEpiWarps>(!ready || *(volatile int*)err)) break;
       tc_fence_after();
-      constexpr int64_t kSums = (NT / 4) * kLines;  // of one part
+      if constexpr (GATED) {
+        if (p.gated.row_amax != nullptr || p.gated.col_amax != nullptr) pdl_wait();  // are zero
+      }
+      constexpr int64_t kHalfSums = (NT / 4) * kLines;
+      constexpr int64_t kSums = U::kHalves * kHalfSums;  // of one part
       float4* part = p.sums + ((int64_t)tile * p.parts + w.slice) * kSums + l;
 #pragma unroll 1
       for (int c = 0; c < rows; c += 16) {
         float next[16];
-        if (whole && live && c + 16 < rows) few_residual<16>(p, row0 + c + 16, col, next);
-        uint32_t v[16];
-        tmem_ld16(tmem + lanes + b * NT + c, v);
-        tmem_ld_wait();
-        float f[16];
+        if (!GATED && whole && live && c + 16 < rows)
+          few_residual<16>(p, row0 + c + 16, col, next);
+        uint32_t v[U::kHalves][16];
 #pragma unroll
-        for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(v[j]);
+        for (int h = 0; h < U::kHalves; ++h)
+          tmem_ld16(tmem + lanes + (b * U::kHalves + h) * NT + c, v[h]);
+        tmem_ld_wait();
+        float f[U::kHalves][16];
+#pragma unroll
+        for (int h = 0; h < U::kHalves; ++h)
+#pragma unroll
+          for (int j = 0; j < 16; ++j) f[h][j] = __uint_as_float(v[h][j]);
         if (!whole) {
 #pragma unroll
-          for (int g = 0; g < 4; ++g)
-            if (c + 4 * g < rows)
-              __stcg(part + (c / 4 + g) * kLines,
-                     make_float4(f[4 * g], f[4 * g + 1], f[4 * g + 2], f[4 * g + 3]));
+          for (int h = 0; h < U::kHalves; ++h)
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+              if (c + 4 * g < rows)
+                __stcg(part + h * kHalfSums + (c / 4 + g) * kLines,
+                       make_float4(f[h][4 * g], f[h][4 * g + 1], f[h][4 * g + 2], f[h][4 * g + 3]));
+        } else if constexpr (GATED) {
+          few_store_gated<16>(p, row0 + c, col, live, f[0], f[1], alpha + c, beta, bias, cmax, lane);
         } else if (live) {
-          few_store<16>(p, row0 + c, col, f, r, alpha + c, beta, bias);
+          few_store<16>(p, row0 + c, col, f[0], r, alpha + c, beta[0], bias[0]);
 #pragma unroll
           for (int j = 0; j < 16; ++j) r[j] = next[j];
         }
@@ -518,7 +633,15 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&acc_empty[b]);
-      if (whole) continue;
+      // the column's maximum, once its tile is whole
+      auto store_cmax = [&] {
+        if (GATED && live && p.gated.col_amax != nullptr)
+          atomicMax(reinterpret_cast<int*>(p.gated.col_amax) + col, __float_as_int(cmax));
+      };
+      if (whole) {
+        store_cmax();
+        continue;
+      }
       // the CTA that finishes the tile last adds its parts, in their order
       barrier_or<1, 32 * kEpiWarps>(false);  // the four warps' sums are written (and released below)
       if (warp == 6 && lane == 0) {
@@ -530,43 +653,54 @@ __global__ void __launch_bounds__(kFewThreads, 1)
       barrier_or<1, 32 * kEpiWarps>(false);
       const bool last = *(volatile int*)last_flag != 0;
       barrier_or<1, 32 * kEpiWarps>(false);  // read before it is written again
-      if (!last || !live) continue;
+      if (!last || (!GATED && !live)) continue;
       const int groups = (rows + 3) / 4;
-      few_residual<16>(p, row0, col, r);
+      if constexpr (!GATED) few_residual<16>(p, row0, col, r);
       const float4* from = p.sums + (int64_t)tile * p.parts * kSums + l;
 #pragma unroll 1
       for (int g0 = 0; g0 < groups; g0 += 4) {
-        float next[16], f[16];
-        if (g0 + 4 < groups) few_residual<16>(p, row0 + 4 * g0 + 16, col, next);
-        auto load = [&](int part, float4 (&a)[4]) {
+        float next[16], fs[U::kHalves][16];
+        if (!GATED && g0 + 4 < groups) few_residual<16>(p, row0 + 4 * g0 + 16, col, next);
 #pragma unroll
-          for (int g = 0; g < 4; ++g)
-            if (g0 + g < groups) a[g] = __ldcg(from + part * kSums + (g0 + g) * kLines);
-        };
-#pragma unroll
-        for (int j = 0; j < 16; ++j) f[j] = 0.0f;
-        // three parts in flight at a time
-#pragma unroll 1
-        for (int c = 0; c < p.parts; c += 3) {
-          float4 a[3][4];
-#pragma unroll
-          for (int k = 0; k < 3; ++k)
-            if (c + k < p.parts) load(c + k, a[k]);
-#pragma unroll
-          for (int k = 0; k < 3; ++k)
+        for (int h = 0; h < U::kHalves; ++h) {
+          float* f = fs[h];
+          auto load = [&](int part, float4 (&a)[4]) {
 #pragma unroll
             for (int g = 0; g < 4; ++g)
-              if (c + k < p.parts && g0 + g < groups) {
-                f[4 * g] = __fadd_rn(f[4 * g], a[k][g].x);
-                f[4 * g + 1] = __fadd_rn(f[4 * g + 1], a[k][g].y);
-                f[4 * g + 2] = __fadd_rn(f[4 * g + 2], a[k][g].z);
-                f[4 * g + 3] = __fadd_rn(f[4 * g + 3], a[k][g].w);
-              }
-        }
-        few_store<16>(p, row0 + 4 * g0, col, f, r, alpha + 4 * g0, beta, bias);
+              if (g0 + g < groups)
+                a[g] = __ldcg(from + part * kSums + h * kHalfSums + (g0 + g) * kLines);
+          };
 #pragma unroll
-        for (int j = 0; j < 16; ++j) r[j] = next[j];
+          for (int j = 0; j < 16; ++j) f[j] = 0.0f;
+          // three parts in flight at a time
+#pragma unroll 1
+          for (int c = 0; c < p.parts; c += 3) {
+            float4 a[3][4];
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+              if (c + k < p.parts) load(c + k, a[k]);
+#pragma unroll
+            for (int k = 0; k < 3; ++k)
+#pragma unroll
+              for (int g = 0; g < 4; ++g)
+                if (c + k < p.parts && g0 + g < groups) {
+                  f[4 * g] = __fadd_rn(f[4 * g], a[k][g].x);
+                  f[4 * g + 1] = __fadd_rn(f[4 * g + 1], a[k][g].y);
+                  f[4 * g + 2] = __fadd_rn(f[4 * g + 2], a[k][g].z);
+                  f[4 * g + 3] = __fadd_rn(f[4 * g + 3], a[k][g].w);
+                }
+          }
+        }
+        if constexpr (GATED) {
+          few_store_gated<16>(p, row0 + 4 * g0, col, live, fs[0], fs[1], alpha + 4 * g0, beta, bias,
+                              cmax, lane);
+        } else {
+          few_store<16>(p, row0 + 4 * g0, col, fs[0], r, alpha + 4 * g0, beta[0], bias[0]);
+#pragma unroll
+          for (int j = 0; j < 16; ++j) r[j] = next[j];
+        }
       }
+      store_cmax();
     }
   }
 
@@ -579,11 +713,51 @@ __global__ void __launch_bounds__(kFewThreads, 1)
   }
 }
 
-// Clears the arrival counts.  The product starts while this runs (it needs the counts only
-// at its first shared tile).
-__global__ void k_clear_arrivals(uint32_t* p, int n) {
+// Clears the arrival counts, and the maxima that the product raises.  The product starts while
+// this runs (it needs them only at its first shared tile or its first result).
+struct ClearArgs {
+  void* p[3];
+  int n[3];  // words
+};
+__global__ void __launch_bounds__(256) k_clear_words(const ClearArgs a) {
   pdl_launch_dependents();
-  for (int i = threadIdx.x; i < n; i += blockDim.x) p[i] = 0;
+#pragma unroll
+  for (int k = 0; k < 3; ++k)
+    for (int i = blockIdx.x * 256 + threadIdx.x; i < a.n[k]; i += gridDim.x * 256)
+      static_cast<uint32_t*>(a.p[k])[i] = 0;
+}
+cudaError_t launch_clear(const ClearArgs& a, cudaStream_t stream) {
+  const int64_t words = (int64_t)a.n[0] + a.n[1] + a.n[2];
+  k_clear_words<<<(unsigned)std::min<int64_t>((words + 1023) / 1024, 64), 256, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+// The gated product of an empty sum (k == 0): every row is act(bias_g) bias_u.
+__global__ void __launch_bounds__(256) k_gated_epilogue_only(const Epilogue e, const GatedOut o,
+                                                             void* d, bool bf16, int64_t m, int n) {
+  auto put = [&](void* base, int64_t i, float v) {
+    if (bf16) static_cast<__nv_bfloat16*>(base)[i] = __float2bfloat16_rn(v);
+    else static_cast<float*>(base)[i] = v;
+  };
+  const int64_t total = m * n;
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total;
+       i += (int64_t)gridDim.x * 256) {
+    const int64_t r = i / n;
+    const int c = (int)(i % n);
+    float v[2] = {e.bias_at(c), 0.0f};
+    const float u = e.bias_at(n + c);
+    if (o.gu != nullptr) {
+      put(o.gu, 2 * r * n + c, v[0]);
+      put(o.gu, (2 * r + 1) * n + c, u);
+    }
+    apply_act<2>(e.act, v);
+    const float z = __fmul_rn(v[0], u);
+    put(d, i, z);
+    const float as = bf16 ? __bfloat162float(__float2bfloat16_rn(z)) : z;
+    const int top = __float_as_int(fmaxf(fabsf(as), 0.0f));
+    if (o.row_amax != nullptr) atomicMax(reinterpret_cast<int*>(o.row_amax) + r, top);
+    if (o.col_amax != nullptr) atomicMax(reinterpret_cast<int*>(o.col_amax) + c, top);
+  }
 }
 
 int scale_grain(const uint8_t* p, int64_t k16) {
@@ -625,11 +799,11 @@ CutPlan plan_cut(int tiles, int k_tiles, int sms) {
   return best;
 }
 
-template <int NT, int S, int kGroup>
-cudaError_t run_few(const GemmArgs& a, FewParams& p, const CUtensorMap& map_w,
-                    const CUtensorMap& map_x, int grid, cudaStream_t stream) {
-  using G = FewGeom<NT, S, kGroup>;
-  auto kernel = k_gemm_few<NT, S, kGroup>;
+template <int NT, int S, int kGroup, bool GATED>
+cudaError_t run_few(FewParams& p, const CUtensorMap& map_w, const CUtensorMap& map_x, int grid,
+                    cudaStream_t stream) {
+  using G = FewGeom<NT, S, kGroup, GATED>;
+  auto kernel = k_gemm_few<NT, S, kGroup, GATED>;
   cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                        G::kSmemBytes);
   if (e != cudaSuccess) return e;
@@ -642,9 +816,11 @@ cudaError_t run_few(const GemmArgs& a, FewParams& p, const CUtensorMap& map_w,
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at.val.programmaticStreamSerializationAllowed = 1;
-  if (p.parts > 1) {
-    k_clear_arrivals<<<1, 256, 0, stream>>>(p.arrivals, p.split);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  const ClearArgs clear{{p.arrivals, p.gated.row_amax, p.gated.col_amax},
+                        {p.parts > 1 ? p.split : 0, p.gated.row_amax ? p.m : 0,
+                         p.gated.col_amax ? p.n : 0}};
+  if (clear.n[0] > 0 || clear.n[1] > 0 || clear.n[2] > 0) {
+    if ((e = launch_clear(clear, stream)) != cudaSuccess) return e;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
   }
@@ -653,6 +829,20 @@ cudaError_t run_few(const GemmArgs& a, FewParams& p, const CUtensorMap& map_w,
 
 }  // namespace
 
+cudaError_t launch_gated_epilogue_only(const Epilogue& e, const GatedOut& g, void* d, bool bf16,
+                                       int64_t m, int64_t n, const DeviceInfo& dev,
+                                       cudaStream_t stream) {
+  const int64_t grid = std::min<int64_t>((m * n + 255) / 256, 8LL * dev.num_sms);
+  const ClearArgs clear{{nullptr, g.row_amax, g.col_amax},
+                        {0, g.row_amax ? (int)m : 0, g.col_amax ? (int)n : 0}};
+  if (clear.n[1] > 0 || clear.n[2] > 0) {
+    const cudaError_t err = launch_clear(clear, stream);
+    if (err != cudaSuccess) return err;
+  }
+  k_gated_epilogue_only<<<(unsigned)grid, 256, 0, stream>>>(e, g, d, bf16, m, (int)n);
+  return cudaGetLastError();
+}
+
 // Up to 384 rows, or up to 304 tiles (two for each of 152 SMs).  Measured with bias and GELU,
 // this kernel against k_gemm_nvf4, in us: (m, n, k) = (64, 8192, 8192) 19 and 43, (384, 8192,
 // 8192) 40 and 45, (384, 28672, 8192) 101 and 108; beyond, (512, 8192, 8192) 47 and 46, (512,
@@ -660,14 +850,16 @@ cudaError_t run_few(const GemmArgs& a, FewParams& p, const CUtensorMap& map_w,
 // 7168) 18 and 31, (512, 4096, 4096) 21 and 26, (1000, 1024, 4096) 14 and 25.
 bool gemm_few(int64_t m, int64_t n) { return m <= 384 || tiles_of(m, n) <= 304; }
 
-int64_t gemm_few_workspace(int64_t m, int64_t n) {
-  return round256(4 * tiles_of(m, n)) + (int64_t)kMaxCtas * 2 * rows_of_mma(m) * kLines * 4;
+int64_t gemm_few_workspace(int64_t m, int64_t n, bool gated) {
+  return round256(4 * tiles_of(m, n)) +
+         (int64_t)(gated ? 2 : 1) * kMaxCtas * 2 * rows_of_mma(m) * kLines * 4;
 }
 
 cudaError_t launch_gemm_few(const GemmArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
   const int nt = rows_of_mma(a.M);
+  const bool gated = a.gated != nullptr;
   CUtensorMap map_w, map_x;
-  if (!make_operand_map(&map_w, a.b_codes, a.N, a.K / 2, kBoxBytes, kLines) ||
+  if (!make_operand_map(&map_w, a.b_codes, gated ? 2 * a.N : a.N, a.K / 2, kBoxBytes, kLines) ||
       !make_operand_map(&map_x, a.a_codes, a.M, a.K / 2, kBoxBytes, nt))
     return cudaErrorInvalidValue;
   FewParams p{};
@@ -684,12 +876,14 @@ cudaError_t launch_gemm_few(const GemmArgs& a, const DeviceInfo& dev, cudaStream
   p.w_finv = 1.0f / (a.b_bound * 6.0f);
   p.m = (int)a.M;
   p.n = (int)a.N;
-  p.k_tiles = (int)((a.K + 2 * kUnitBytes - 1) / (2 * kUnitBytes));
+  const int64_t unit = 2 * (gated ? Unit<true>::kBytes : Unit<false>::kBytes);  // values
+  p.k_tiles = (int)ceil_div(a.K, unit);
   p.m_tiles = (int)ceil_div(a.M, nt);
   p.tiles = (int)tiles_of(a.M, a.N);
   p.d = a.d;
   p.d_bf16 = a.d_bf16;
   p.epi = *a.epilogue;
+  if (gated) p.gated = *a.gated;
   p.arrivals = reinterpret_cast<uint32_t*>(a.workspace);
   p.sums = reinterpret_cast<float4*>(a.workspace + round256(4 * (int64_t)p.tiles));
   p.status = dev.status;
@@ -698,10 +892,17 @@ cudaError_t launch_gemm_few(const GemmArgs& a, const DeviceInfo& dev, cudaStream
   p.split = cut.split;
   p.parts = cut.parts;
   const int ctas = std::max(grid, std::min(std::min(dev.num_sms, kMaxCtas), p.split * p.parts));
+  if (gated) {
+    switch (nt) {
+      case 16: return run_few<16, 4, 4, true>(p, map_w, map_x, ctas, stream);
+      case 32: return run_few<32, 4, 4, true>(p, map_w, map_x, ctas, stream);
+      default: return run_few<64, 4, 4, true>(p, map_w, map_x, ctas, stream);
+    }
+  }
   switch (nt) {
-    case 16: return run_few<16, 4, 4>(a, p, map_w, map_x, ctas, stream);
-    case 32: return run_few<32, 4, 4>(a, p, map_w, map_x, ctas, stream);
-    default: return run_few<64, 3, 4>(a, p, map_w, map_x, ctas, stream);
+    case 16: return run_few<16, 4, 4, false>(p, map_w, map_x, ctas, stream);
+    case 32: return run_few<32, 4, 4, false>(p, map_w, map_x, ctas, stream);
+    default: return run_few<64, 3, 4, false>(p, map_w, map_x, ctas, stream);
   }
 }
 

@@ -1,0 +1,315 @@
+"""The gated product of NVFP4 operands, and the backward pass of its activation and product, on
+the GPU against the FP64 definitions.
+
+Tolerances.  The halves: as in test_gpu_bias_act, t = (k 2^-23 + 2^-20) sum|terms| each, and 2^-23
+of |z| for the bias.  d = act(g) u: 1.13 t_g |u| + t_u |act(g)| + 1.13 t_g t_u, the activation's own
+2^-20 (1 + |g|) |u|, and 2^-23 |d| for the product.  Storing rounds once.  The maxima are exactly
+those of d (of dgu) as the call stored it.
+"""
+import pytest
+import torch
+
+import nvfp4_precision_quantization_gb300 as nv
+import workloads
+from block_reference import gated_backward, operand_values
+from layer_reference import ACTS, act, at_offset, guarded, half_ulp
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda"
+RS, PT = nv.NVFP4_ROW_SCALED, nv.NVFP4_PER_TENSOR
+DTYPES = [torch.bfloat16, torch.float32]
+
+
+def _operands(m, n, k, seed, modes=(RS, RS), bounds=(448.0, 448.0), scale_offset=0):
+    """Two operands, their FP64 product [m][2n] and the sums of its terms' magnitudes; the values
+    are scaled so that the product stays within about 4."""
+    dev = []
+    for i, lines in enumerate((m, 2 * n)):
+        c, s, a = workloads.nvfp4_operand(lines, k, seed + i, modes[i] == RS)
+        dev.append(nv.Operand(c.to(DEV), at_offset(s.to(DEV), scale_offset),
+                              (a * (0.1 / a.max())).to(DEV), modes[i], bounds[i]))
+
+    def product():
+        x, w = (operand_values(o.codes, o.scales, o.amax, o.bound) for o in dev)
+        return x @ w.t(), x.abs() @ w.abs().t()
+    z, _ = product()
+    dev[1].amax = (dev[1].amax * (4.0 / z.abs().max().clamp(min=1e-6))).float()
+    return (dev, *product())
+
+
+def _check(m, n, k, dtype, name, bias=None, keep=True, maxima=True, seed=0, modes=(RS, RS),
+           bounds=(448.0, 448.0), offset=0, scale_offset=0):
+    (a, b), z, mag = _operands(m, n, k, seed, modes, bounds, scale_offset)
+    tol = (k * 2.0 ** -23 + 2.0 ** -20) * mag
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    bv = torch.randn(2 * n, generator=g, device=DEV).to(bias) if bias is not None else None
+    if bv is not None:
+        z = z + bv.double()
+        tol = tol + 2.0 ** -23 * z.abs()
+    d, ok_d = guarded((m, n), dtype, offset=offset)
+    gu, ok_gu = guarded((m, 2 * n), dtype, offset=offset)
+    ra, ok_r = guarded((m,), torch.float32)
+    ca, ok_c = guarded((n,), torch.float32)
+    nv.nvfp4_gemm_gated(a, b, d, bias=bv, act=ACTS[name], gu=gu if keep else None,
+                        row_amax=ra if maxima else None, col_amax=ca if maxima else None)
+    torch.cuda.synchronize()
+    zg, zu, tg, tu = z[:, :n], z[:, n:], tol[:, :n], tol[:, n:]
+    want, half = act(zg, name) * zu, half_ulp(dtype)
+    t = 1.13 * tg * zu.abs() + tu * act(zg, name).abs() + 1.13 * tg * tu + 2.0 ** -23 * want.abs()
+    if name in ("gelu", "silu"):
+        t = t + 2.0 ** -20 * (1 + zg.abs()) * (zu.abs() + tu)
+    assert bool(((d.double() - want).abs() <= t * (1 + half) + half * want.abs()).all())
+    if keep:
+        assert bool(((gu.double() - z).abs() <= tol * (1 + half) + half * z.abs()).all())
+    if maxima:
+        assert torch.equal(ra, d.abs().amax(dim=1).float())
+        assert torch.equal(ca, d.abs().amax(dim=0).float())
+    for ok in (ok_d, ok_gu, ok_r, ok_c):
+        ok()
+    return d
+
+
+# one token to several tiles, odd sizes on both axes, K tails of a K tile
+SIZES = [(1, 256, 256), (1, 1, 32), (1, 4097, 512), (2, 100, 96), (7, 300, 320), (8, 512, 1024),
+         (16, 1000, 544), (17, 129, 64), (31, 64, 800), (33, 640, 256), (64, 255, 288),
+         (65, 384, 512), (100, 77, 96), (128, 256, 128), (129, 257, 160), (200, 520, 992),
+         (300, 500, 320), (257, 128, 256), (385, 6000, 64), (450, 5000, 96), (1000, 2561, 160),
+         (700, 1300, 2080)]
+
+
+@pytest.mark.parametrize("m,n,k", SIZES)
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_gated_product(m, n, k, dtype):
+    name = list(ACTS)[(m + n + k // 32) % 4]
+    _check(m, n, k, dtype, name, torch.float32, seed=m + n + k)
+    _check(m, n, k, dtype, "silu", None, False, False, m + n + k + 1, (PT, RS), (256.0, 448.0))
+
+
+@pytest.mark.parametrize("name", list(ACTS))
+@pytest.mark.parametrize("bias", [None, torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("keep,maxima", [(False, True), (True, False)])
+@pytest.mark.parametrize("m,n", [(1, 272), (5, 272), (40, 272), (150, 272), (700, 6000)])
+def test_epilogue_combinations(m, n, name, bias, keep, maxima):
+    _check(m, n, 160, torch.bfloat16, name, bias, keep, maxima, 3 * m)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("m,n", [(1, 264), (9, 264), (140, 264), (640, 5000)])
+@pytest.mark.parametrize("offset", [1, 4, 8])
+def test_unaligned_outputs_and_scales(m, n, offset, dtype):
+    _check(m, n, 128, dtype, "silu", torch.float32, seed=m, offset=offset, scale_offset=offset)
+
+
+@pytest.mark.parametrize("m,n", [(1, 5000), (40, 20000), (1, 40000), (129, 10100)])
+def test_tiles_cut_along_k(m, n):
+    """More tiles than SMs with a rest that is cut along K, beside whole tiles."""
+    _check(m, n, 2080, torch.bfloat16, "gelu", torch.float32, seed=m)
+
+
+@pytest.mark.parametrize("m,n", [(1, 320), (20, 320), (130, 320), (450, 5000)])
+def test_long_k(m, n):
+    _check(m, n, 8192 + 96, torch.float32, "none", torch.float32, seed=5)
+
+
+@pytest.mark.parametrize("m,n", [(3, 384), (150, 384), (900, 5000)])
+def test_halves_are_the_product_with_either_weight(m, n):
+    """gu is nvfp4_gemm with the stacked weights, within both sums' rounding, and repeatable."""
+    (a, b), _, mag = _operands(m, n, 2048, 6)
+    both, gu = (torch.empty(m, 2 * n, device=DEV) for _ in range(2))
+    d, e = torch.empty(m, n, device=DEV), torch.empty(m, n, device=DEV)
+    ra, rb = torch.empty(m, device=DEV), torch.empty(m, device=DEV)
+    nv.nvfp4_gemm(a, b, both)
+    nv.nvfp4_gemm_gated(a, b, d, gu=gu, row_amax=ra)
+    assert bool(((both.double() - gu.double()).abs() <= 2 * 2048 * 2.0 ** -23 * mag).all())
+    for _ in range(3):
+        nv.nvfp4_gemm_gated(a, b, e, row_amax=rb)
+        assert torch.equal(d, e) and torch.equal(ra, rb)
+
+
+def test_maxima_are_the_quantizes_own():
+    """Given to the quantization of d, they change no byte."""
+    (a, b), _, _ = _operands(160, 512, 512, 2)
+    d = torch.empty(160, 512, dtype=torch.bfloat16, device=DEV)
+    ra, ca = torch.empty(160, device=DEV), torch.empty(512, device=DEV)
+    nv.nvfp4_gemm_gated(a, b, d, row_amax=ra, col_amax=ca)
+    cfg = nv.Config(RS, 448.0, 0, 0)
+    outs = []
+    for given in (False, True):
+        row, col = nv.alloc_out(160, 512, 160), nv.alloc_out(512, 160, 512)
+        if given:
+            row.amax_in, col.amax_in = ra, ca
+        nv.nvfp4_quantize_both(d, cfg, row, col)
+        outs.append((row, col))
+    torch.cuda.synchronize()
+    for one, two in zip(*outs):
+        for f in ("codes", "scales", "amax"):
+            assert torch.equal(getattr(one, f), getattr(two, f))
+
+
+def test_a_bad_line_stays_in_its_row_and_column():
+    """An infinite amax spoils its own line's products alone; maxima skip the NaN it makes."""
+    (a, b), _, _ = _operands(20, 200, 256, 8)
+    d, e = torch.empty(20, 200, device=DEV), torch.empty(20, 200, device=DEV)
+    ca = torch.empty(200, device=DEV)
+    nv.nvfp4_gemm_gated(a, b, d)
+    b.amax[7] = float("nan")  # column 7's gate
+    nv.nvfp4_gemm_gated(a, b, e, col_amax=ca)
+    assert bool(e[:, 7].isnan().all()) and float(ca[7]) == 0.0
+    keep = torch.arange(200, device=DEV) != 7
+    assert torch.equal(d[:, keep], e[:, keep])
+    assert torch.equal(ca[keep], e[:, keep].abs().amax(dim=0))
+
+
+def test_empty_sum_and_empty_outputs():
+    bias = torch.randn(80, device=DEV)
+    empty = lambda lines: nv.Operand(torch.empty(lines, 0, dtype=torch.uint8, device=DEV),  # noqa: E731
+                                     torch.empty(lines, 0, dtype=torch.uint8, device=DEV),
+                                     torch.ones(lines, device=DEV), RS, 448.0)
+    d, gu = torch.empty(3, 40, device=DEV), torch.empty(3, 80, device=DEV)
+    ra, ca = torch.full((3,), 9.0, device=DEV), torch.full((40,), 9.0, device=DEV)
+    nv.nvfp4_gemm_gated(empty(3), empty(80), d, bias=bias, act=nv.NVFP4_ACT_RELU, gu=gu,
+                        row_amax=ra, col_amax=ca)
+    want = bias[:40].clamp(min=0) * bias[40:]
+    assert torch.equal(gu, bias.expand(3, 80)) and torch.equal(d, want.expand(3, 40))
+    assert torch.equal(ca, want.abs()) and torch.equal(ra, want.abs().amax().expand(3))
+    (a, b), _, _ = _operands(4, 40, 64, 1)
+    none = nv.Operand(a.codes[:0], a.scales[:0], a.amax[:0], RS, 448.0)
+    ca.fill_(5.0)
+    nv.nvfp4_gemm_gated(none, b, torch.empty(0, 40, device=DEV), col_amax=ca)
+    assert float(ca.abs().max()) == 0.0
+    nothing = nv.Operand(b.codes[:0], b.scales[:0], b.amax[:0], RS, 448.0)
+    ra = torch.full((4,), 5.0, device=DEV)
+    nv.nvfp4_gemm_gated(a, nothing, torch.empty(4, 0, device=DEV), row_amax=ra)
+    assert float(ra.abs().max()) == 0.0
+
+
+@pytest.mark.parametrize("m,n", [(2, 512), (140, 512), (1500, 3000)])
+def test_workspace_stream_and_graph(m, n):
+    """A given workspace of the stated size, on another stream, and captured."""
+    (a, b), _, _ = _operands(m, n, 1024, 9)
+    d, e = (torch.empty(m, n, device=DEV) for _ in range(2))
+    ra, rb, cb = torch.empty(m, device=DEV), torch.empty(m, device=DEV), torch.empty(n, device=DEV)
+    nv.nvfp4_gemm_gated(a, b, d, row_amax=ra)
+    ws, ok = guarded((max(nv.nvfp4_gemm_gated_workspace_size(m, n, 1024), 256),), torch.uint8)
+    ws.random_(0, 256)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    for _ in range(2):  # what one call leaves in the workspace does not matter to the next
+        e.zero_()
+        torch.cuda.synchronize()
+        nv.nvfp4_gemm_gated(a, b, e, row_amax=rb, col_amax=cb, workspace=ws, stream=s)
+        s.synchronize()
+        assert torch.equal(d, e) and torch.equal(ra, rb)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=s):
+        nv.nvfp4_gemm_gated(a, b, e, row_amax=rb, col_amax=cb, workspace=ws)
+    for _ in range(3):
+        e.zero_()
+        rb.fill_(1e9)
+        cb.fill_(1e9)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(d, e) and torch.equal(ra, rb)
+        assert torch.equal(cb, e.abs().amax(dim=0))
+    ok()
+
+
+# ---------------------------------------------------------------- backward
+
+BACK = [(1, 1), (1, 4096), (3, 16), (5, 17), (40, 64), (1000, 8), (129, 100), (300, 512),
+        (77, 513), (64, 5000), (2000, 1024), (5, 28672), (700, 2056), (0, 8), (8, 0),
+        (3000, 1001), (999, 515), (1200, 2050)]
+
+
+def _back_inputs(rows, cols, dtype, seed):
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    gu = (3 * torch.randn(rows, 2 * cols, generator=g, device=DEV)).to(dtype)
+    return torch.randn(rows, cols, generator=g, device=DEV).to(dtype), gu
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,cols", BACK)
+def test_backward(rows, cols, dtype):
+    """dg, du: act and act' are within 2^-20 (1 + |g|) of values below 1.13 (1 + |g|), two more
+    products 2^-23; dbias: sums of `rows` terms, at most rows / CTAs + 80 additions a chain."""
+    dd, gu = _back_inputs(rows, cols, dtype, rows + cols)
+    names = list(ACTS) if rows < 700 else [list(ACTS)[(rows + cols) % 4]]
+    half = half_ulp(dtype)
+    for name in names:
+        dgu, ok_d = guarded((rows, 2 * cols), dtype)
+        db, ok_b = guarded((2 * cols,), torch.float32)
+        ra, ok_r = guarded((rows,), torch.float32)
+        ca, ok_c = guarded((2 * cols,), torch.float32)
+        nv.nvfp4_gated_backward(dd, gu, ACTS[name], dgu, dbias=db, row_amax=ra, col_amax=ca)
+        torch.cuda.synchronize()
+        want = gated_backward(dd, gu, name)
+        g, u = gu[:, :cols].double().abs(), gu[:, cols:].double().abs()
+        own = 2.0 ** -20 * (1 + g) * dd.double().abs()
+        tol = torch.cat([own * u, own], dim=1) + 2.0 ** -22 * want.abs()
+        assert bool(((dgu.double() - want).abs() <= tol * (1 + half) + half * want.abs() + 1e-37).all())
+        tol_b = tol.sum(0) + (rows + 100) * 2.0 ** -24 * want.abs().sum(0)
+        assert bool(((db.double() - want.sum(0)).abs() <= tol_b + 1e-37).all())
+        if rows and cols:
+            assert torch.equal(ra, dgu.abs().amax(dim=1).float())
+            assert torch.equal(ca, dgu.abs().amax(dim=0).float())
+        else:
+            assert not bool(ra.any()) and not bool(ca.any()) and not bool(db.any())
+        for ok in (ok_d, ok_b, ok_r, ok_c):
+            ok()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("offset", [1, 2, 4])
+def test_backward_unaligned_and_alone(dtype, offset):
+    """Any start gives the same bits, and so does a call without sums and maxima, in place."""
+    dd, gu = _back_inputs(70, 1008, dtype, 3)
+    want, dgu = torch.empty_like(gu), torch.empty_like(gu)
+    nv.nvfp4_gated_backward(dd, gu, nv.NVFP4_ACT_GELU, want, dbias=torch.empty(2016, device=DEV))
+    got, ok = guarded((70, 2016), dtype, offset=offset)
+    nv.nvfp4_gated_backward(at_offset(dd, offset), at_offset(gu, offset), nv.NVFP4_ACT_GELU, got)
+    assert torch.equal(got, want)
+    ok()
+    dgu.copy_(gu)
+    nv.nvfp4_gated_backward(dd, dgu, nv.NVFP4_ACT_GELU, dgu)
+    assert torch.equal(dgu, want)
+
+
+@pytest.mark.parametrize("name", ["relu", "gelu", "silu", "none"])
+def test_backward_at_the_ends(name):
+    """Gates far out: act' is 0 or 1, act is 0 or g, and nothing overflows on the way."""
+    big = torch.tensor([-3e38, -1e30, -1e4, -100.0, -65.0, -0.0, 0.0, 65.0, 100.0, 1e4, 1e30],
+                       device=DEV)
+    gu = torch.cat([big, torch.full_like(big, 2.0)])[None].contiguous()
+    dd, dgu = torch.ones(1, big.numel(), device=DEV), torch.empty_like(gu)
+    nv.nvfp4_gated_backward(dd, gu, ACTS[name], dgu)
+    n = big.numel()
+    if name == "none":
+        assert bool((dgu[0, :n] == 2).all()) and torch.equal(dgu[0, n:], big)
+        return
+    far = big.abs() >= 65
+    slope, value = dgu[0, :n] / 2, dgu[0, n:]
+    assert torch.equal(slope[far], (big[far] > 0).float())
+    # silu(-65) is -65 e^-65, about -4e-27
+    assert bool((value[far & (big < 0)].abs() <= 1e-26).all())
+    assert torch.equal(value[far & (big > 0)], big[far & (big > 0)])
+
+
+def test_backward_against_differences():
+    """The halves' gradients are the slopes of sum(dd act(g) u) in FP64 (tanh and exp of torch),
+    by central differences of 2^-12: third derivatives below 4 leave 2^-23, FP64 nothing."""
+    from layer_reference import act
+    dd, gu = _back_inputs(4, 40, torch.float32, 12)
+    for name in ("gelu", "silu", "none"):
+        dgu = torch.empty_like(gu)
+        nv.nvfp4_gated_backward(dd, gu, ACTS[name], dgu)
+        e, x = 2.0 ** -12, gu.double()
+
+        def loss(g, u):
+            return dd.double() * act(g, name) * u
+        g, u = x[:, :40], x[:, 40:]
+        slope = torch.cat([(loss(g + e, u) - loss(g - e, u)) / (2 * e),
+                           (loss(g, u + e) - loss(g, u - e)) / (2 * e)], dim=1)
+        mag = dd.double().abs().repeat(1, 2) * (1 + x.abs().amax())
+        assert bool(((dgu.double() - slope).abs() <= 2.0 ** -19 * mag * (1 + x.abs().amax())).all())
