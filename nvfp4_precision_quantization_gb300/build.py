@@ -22,10 +22,11 @@ SOURCES = ["api.cu", "kernels_amax.cu", "kernels_quantize.cu", "kernels_misc.cu"
            "kernels_gemm.cu", "kernels_rht.cu", "api_layer.cu", "kernels_norm.cu",
            "kernels_norm_backward.cu",
            "kernels_act.cu", "kernels_clip.cu", "kernels_gemm_few.cu", "kernels_layernorm.cu",
-           "kernels_layernorm_backward.cu", "kernels_dropout.cu", "kernels_gated_act.cu"]
+           "kernels_layernorm_backward.cu", "kernels_dropout.cu", "kernels_gated_act.cu", "kernels_gated.cu"]
 HEADERS = ["device_common.cuh", "internal.h", "tile_pipeline.cuh", "api_common.h", "row_io.cuh",
            "row_ring.cuh",
-           "activation.cuh", "tcgen05.cuh", "dropout.cuh", "norm_rows.cuh", "sector.cuh"]
+           "activation.cuh", "tcgen05.cuh", "dropout.cuh", "norm_rows.cuh", "sector.cuh",
+           "gemm_tile.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "--fmad=false", "-Xcompiler", "-fPIC",

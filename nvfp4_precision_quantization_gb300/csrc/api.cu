@@ -665,8 +665,9 @@ nvfp4_status gemm_impl(const nvfp4_operand* a, const nvfp4_operand* b, const int
   if (k_grouped && k % 256 != 0)
     return fail(NVFP4_ERR_UNSUPPORTED, "grouped wgrad GEMM: tokens must be a multiple of 256");
   GemmLayout L = gemm_layout(m, n, k, group_ends && !k_grouped ? (int64_t)num_groups * n : n);
-  const bool few = epilogue != nullptr && (gated != nullptr || gemm_few(m, n));
+  const bool few = epilogue != nullptr && (gated ? gemm_gated_few(m, n) : gemm_few(m, n));
   if (few) L.workspace_bytes = gemm_few_workspace(m, n, gated != nullptr);
+  else if (gated) L.workspace_bytes = gemm_gated_workspace(m, n, k);
   if (L.tiles_m * L.tiles_n >= (1LL << 31)) return fail(NVFP4_ERR_UNSUPPORTED, "too many tiles");
   if (static_ws) {
     if ((uint64_t)L.workspace_bytes > (uint64_t)NVFP4_GEMM_STATIC_WS_BYTES)
@@ -703,7 +704,9 @@ nvfp4_status gemm_impl(const nvfp4_operand* a, const nvfp4_operand* b, const int
   g.k_grouped = k_grouped;
   g.epilogue = epilogue;
   g.gated = gated;
-  cudaError_t e = few ? launch_gemm_few(g, dev, stream) : launch_gemm(g, dev, stream);
+  cudaError_t e = few     ? launch_gemm_few(g, dev, stream)
+                  : gated ? launch_gemm_gated(g, dev, stream)
+                          : launch_gemm(g, dev, stream);
   if (e != cudaSuccess) return cuda_fail(e, "gemm launch");
   return NVFP4_OK;
 }
@@ -757,7 +760,9 @@ nvfp4_status nvfp4_gemm_gated_workspace_size(int64_t m, int64_t n, int64_t k, ui
   nvfp4_status st;
   if ((st = check_gated_sizes(m, n)) != NVFP4_OK) return st;
   if ((st = check_sizes(k, 0)) != NVFP4_OK) return st;
-  *bytes = (m == 0 || n == 0 || k == 0) ? 0 : (uint64_t)gemm_few_workspace(m, n, true);
+  *bytes = (m == 0 || n == 0 || k == 0) ? 0
+           : gemm_gated_few(m, n)       ? (uint64_t)gemm_few_workspace(m, n, true)
+                                        : (uint64_t)gemm_gated_workspace(m, n, k);
   return NVFP4_OK;
 }
 

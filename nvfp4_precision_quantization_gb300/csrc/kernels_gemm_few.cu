@@ -850,6 +850,8 @@ cudaError_t launch_gated_epilogue_only(const Epilogue& e, const GatedOut& g, voi
 // 7168) 18 and 31, (512, 4096, 4096) 21 and 26, (1000, 1024, 4096) 14 and 25.
 bool gemm_few(int64_t m, int64_t n) { return m <= 384 || tiles_of(m, n) <= 304; }
 
+bool gemm_gated_few(int64_t m, int64_t n) { return gemm_few(m, n); }
+
 int64_t gemm_few_workspace(int64_t m, int64_t n, bool gated) {
   return round256(4 * tiles_of(m, n)) +
          (int64_t)(gated ? 2 : 1) * kMaxCtas * 2 * rows_of_mma(m) * kLines * 4;
