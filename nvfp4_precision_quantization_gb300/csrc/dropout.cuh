@@ -68,18 +68,29 @@ struct Dropper {
 #pragma unroll
     for (int i = 0; i < 8; ++i) z[i] = __funnelshift_r(x[i], x[i + 1], 16 * (shift & 1));
   }
-  // v[0 .. 16), the elements from e on: scaled where kept, zero where dropped (a NaN or an
-  // infinity too).
-  __device__ __forceinline__ void apply(int64_t e, float* v) const {
-    if (!on) return;
+  // v[0 .. 16), the elements from e on, scaled where kept and zero where dropped (a NaN or an
+  // infinity too), plus r's (where there are any): one FMA and one selection an element.
+  template <bool BF16>
+  __device__ __forceinline__ void apply(int64_t e, float* v, const Chunk<BF16>* r) const {
+    if (!on) {
+      if (r == nullptr) return;
+#pragma unroll
+      for (int i = 0; i < kChunk; i += 2) {
+        const Pair s = pair_add({v[i], v[i + 1]}, {r->get(i), r->get(i + 1)});
+        v[i] = s.x;
+        v[i + 1] = s.y;
+      }
+      return;
+    }
     uint32_t z[kChunk / 2];
     words(e, z);
     const uint32_t high = (below << 16) | 0xffffu;
 #pragma unroll
-    for (int i = 0; i < kChunk / 2; ++i) {
-      const Pair s = pair_mul({v[2 * i], v[2 * i + 1]}, {scale, scale});
-      v[2 * i] = (z[i] & 0xffffu) > below ? s.x : 0.0f;
-      v[2 * i + 1] = z[i] > high ? s.y : 0.0f;
+    for (int i = 0; i < kChunk; i += 2) {
+      const Pair b = r != nullptr ? Pair{r->get(i), r->get(i + 1)} : Pair{0.0f, 0.0f};
+      const Pair s = pair_fma({v[i], v[i + 1]}, {scale, scale}, b);
+      v[i] = (z[i / 2] & 0xffffu) > below ? s.x : b.x;
+      v[i + 1] = z[i / 2] > high ? s.y : b.y;
     }
   }
 };

@@ -37,12 +37,7 @@ __global__ void __launch_bounds__(256) k_dropout(const DropoutKernelArgs a) {
     const Chunk<BF16>& cx = lx.settle(a.g_x, stage, lane);
 #pragma unroll
     for (int i = 0; i < kChunk; ++i) v[i] = cx.get(i);
-    drop.apply(e, v);
-    if (a.res != nullptr) {
-      const Chunk<BF16>& cr = lr.settle(a.g_res, stage, lane);
-#pragma unroll
-      for (int i = 0; i < kChunk; ++i) v[i] = __fadd_rn(v[i], cr.get(i));
-    }
+    drop.apply(e, v, a.res != nullptr ? &lr.settle(a.g_res, stage, lane) : nullptr);
     Chunk<BF16> cy;
     cy.set(v);
     cy.store_warp<STAGED>(a.y, e, n, run, a.g_y, stage, lane);

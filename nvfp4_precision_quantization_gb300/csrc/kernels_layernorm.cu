@@ -14,73 +14,6 @@
 namespace nvfp4 {
 namespace {
 
-// Mean and sum of squared differences of a row whose part is in v (zeros past its end).
-template <int TPR, int NCH, bool BARRIER>
-__device__ __forceinline__ float2 team_moments(const float (&v)[NCH][kChunk], int cols, int t,
-                                               float2* red) {
-  const int lane = threadIdx.x & 31, first = t - lane;  // of this warp in its team
-  // columns of the warp that starts at thread `from` of the team
-  auto count = [&](int from) {
-    int n = 0;
-#pragma unroll
-    for (int c = 0; c < NCH; ++c) n += max(0, min(32 * kChunk, cols - (c * TPR + from) * kChunk));
-    return n;
-  };
-  Pair two = {0.0f, 0.0f};
-#pragma unroll
-  for (int c = 0; c < NCH; ++c)
-#pragma unroll
-    for (int i = 0; i < kChunk; i += 2) two = pair_add(two, {v[c][i], v[c][i + 1]});
-  float sum = __fadd_rn(two.x, two.y);
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, d));
-  const int mine = count(first);
-  const float mean = mine > 0 ? __fdiv_rn(sum, (float)mine) : 0.0f;
-  two = {0.0f, 0.0f};
-#pragma unroll
-  for (int c = 0; c < NCH; ++c) {
-    const int n = cols - (c * TPR + t) * kChunk;
-    if (n >= kChunk) {
-#pragma unroll
-      for (int i = 0; i < kChunk; i += 2) {
-        const Pair d = pair_add({v[c][i], v[c][i + 1]}, {-mean, -mean});
-        two = pair_fma(d, d, two);
-      }
-    } else if (n > 0) {
-#pragma unroll
-      for (int i = 0; i < kChunk; ++i) {
-        const float d = i < n ? __fsub_rn(v[c][i], mean) : 0.0f;
-        two.x = __fmaf_rn(d, d, two.x);
-      }
-    }
-  }
-  float sq = __fadd_rn(two.x, two.y);
-#pragma unroll
-  for (int d = 16; d > 0; d >>= 1) sq = __fadd_rn(sq, __shfl_xor_sync(0xffffffffu, sq, d));
-  if constexpr (TPR == 32) {
-    if constexpr (BARRIER) __syncthreads();
-    return make_float2(mean, sq);
-  } else {
-    constexpr int kWarps = TPR / 32;
-    constexpr int kTree = kWarps <= 2 ? 2 : kWarps <= 4 ? 4 : kWarps <= 8 ? 8 : kWarps <= 16 ? 16 : 32;
-    const int warp = threadIdx.x >> 5;
-    if (lane == 0) red[warp] = make_float2(sum, sq);
-    __syncthreads();
-    const int i = lane % kTree;
-    const float2 p = i < kWarps ? red[warp - warp % kWarps + i] : make_float2(0.0f, 0.0f);
-    const int n = i < kWarps ? count(32 * i) : 0;
-    float all = p.x;
-#pragma unroll
-    for (int d = kTree / 2; d > 0; d >>= 1) all = __fadd_rn(all, __shfl_xor_sync(0xffffffffu, all, d));
-    const float m = cols > 0 ? __fdiv_rn(all, (float)cols) : 0.0f;
-    const float off = n > 0 ? __fsub_rn(__fdiv_rn(p.x, (float)n), m) : 0.0f;
-    float s = __fmaf_rn(__fmul_rn(off, off), (float)n, p.y);
-#pragma unroll
-    for (int d = kTree / 2; d > 0; d >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, d));
-    return make_float2(m, s);
-  }
-}
-
 // Maximum over a team; red as in team_sum_max.
 template <int TPR>
 __device__ __forceinline__ float team_max(float m, float* red) {
@@ -100,29 +33,118 @@ __device__ __forceinline__ float team_max(float m, float* red) {
 
 struct LayerNorm {
   static constexpr bool kMasked = true;
+  // 24 warps an SM: with the 16 that the compiler's registers leave, a row's barriers lie open
+  // (4000 x 5000 FP32 74 us, 53 so)
   template <bool BF16, int TPR, int NCH>
   static constexpr int ring_ctas() {
-    return 1;
+    constexpr int n = 768 / (TPR < 256 ? 256 : TPR);
+    return n > 0 ? n : 1;
+  }
+  template <int TPR, int NCH>
+  struct Team;
+};
+
+template <int TPR, int NCH>
+struct LayerNorm::Team {
+  static constexpr int kWarps = TPR / 32;
+  static constexpr int kTree = kWarps <= 1 ? 1 : kWarps <= 2 ? 2 : kWarps <= 4 ? 4 : kWarps <= 8 ? 8 : kWarps <= 16 ? 16 : 32;
+  float inv_warp;   // 1 / the columns of this thread's warp (0 where it has none)
+  float n, inv_n;   // those of the team's warp `lane`, whose sums this lane joins
+  float inv_cols;
+
+  // columns of the team's warp w
+  __device__ __forceinline__ static int count(int cols, int w) {
+    int n = 0;
+#pragma unroll
+    for (int c = 0; c < NCH; ++c)
+      n += max(0, min(32 * kChunk, cols - (c * TPR + 32 * w) * kChunk));
+    return n;
+  }
+  __device__ __forceinline__ static float inverse(int n) {
+    return n > 0 ? __frcp_rn((float)n) : 0.0f;
+  }
+  __device__ __forceinline__ Team(const NormKernelArgs& a, int t) {
+    const int w = (threadIdx.x & 31) % kTree, theirs = w < kWarps ? count(a.cols, w) : 0;
+    inv_warp = inverse(count(a.cols, t / 32));
+    n = (float)theirs;
+    inv_n = inverse(theirs);
+    inv_cols = inverse(a.cols);
   }
 
-  template <bool BF16, bool NV4, int TPR, int NCH, bool STAGED, bool RING, class Release>
-  __device__ __forceinline__ static void row(const NormKernelArgs& a, int64_t row, bool live,
-                                             bool has, int t, uint8_t* stage,
-                                             float (&v)[NCH][kChunk], float2* red,
-                                             const Release& release) {
+  // Mean and sum of squared differences of a row whose part is in v (zeros past its end).
+  template <bool BARRIER>
+  __device__ __forceinline__ float2 moments(const float (&v)[NCH][kChunk], int cols, int t,
+                                            float2* red) const {
+    const int lane = threadIdx.x & 31;
+    Pair two = {0.0f, 0.0f};
+#pragma unroll
+    for (int c = 0; c < NCH; ++c)
+#pragma unroll
+      for (int i = 0; i < kChunk; i += 2) two = pair_add(two, {v[c][i], v[c][i + 1]});
+    float sum = __fadd_rn(two.x, two.y);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, d));
+    const float mean = __fmul_rn(sum, inv_warp);
+    two = {0.0f, 0.0f};
+#pragma unroll
+    for (int c = 0; c < NCH; ++c) {
+      const int left = cols - (c * TPR + t) * kChunk;
+      if (left >= kChunk) {
+#pragma unroll
+        for (int i = 0; i < kChunk; i += 2) {
+          const Pair d = pair_add({v[c][i], v[c][i + 1]}, {-mean, -mean});
+          two = pair_fma(d, d, two);
+        }
+      } else if (left > 0) {
+#pragma unroll
+        for (int i = 0; i < kChunk; ++i) {
+          const float d = i < left ? __fsub_rn(v[c][i], mean) : 0.0f;
+          two.x = __fmaf_rn(d, d, two.x);
+        }
+      }
+    }
+    float sq = __fadd_rn(two.x, two.y);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) sq = __fadd_rn(sq, __shfl_xor_sync(0xffffffffu, sq, d));
+    if constexpr (TPR == 32) {
+      if constexpr (BARRIER) __syncthreads();
+      return make_float2(mean, sq);
+    } else {
+      const int warp = threadIdx.x >> 5;
+      if (lane == 0) red[warp] = make_float2(sum, sq);
+      __syncthreads();
+      const int i = lane % kTree;
+      const float2 p = i < kWarps ? red[warp - warp % kWarps + i] : make_float2(0.0f, 0.0f);
+      float all = p.x;
+#pragma unroll
+      for (int d = kTree / 2; d > 0; d >>= 1)
+        all = __fadd_rn(all, __shfl_xor_sync(0xffffffffu, all, d));
+      const float m = __fmul_rn(all, inv_cols);
+      // (n is 0, and the difference of no account, where the warp has no columns)
+      const float off = __fsub_rn(__fmul_rn(p.x, inv_n), m);
+      float s = n > 0.0f ? __fmaf_rn(__fmul_rn(off, off), n, p.y) : 0.0f;
+#pragma unroll
+      for (int d = kTree / 2; d > 0; d >>= 1)
+        s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, d));
+      return make_float2(m, s);
+    }
+  }
+
+  template <bool BF16, bool NV4, bool STAGED, bool RING, class Release>
+  __device__ __forceinline__ void row(const NormKernelArgs& a, int64_t row, bool live, bool has,
+                                      int t, uint8_t* stage, float (&v)[NCH][kChunk], float2* red,
+                                      const Release& release) const {
     // beside red, which the next row's statistics may take while this row's maxima are read
     __shared__ float maxima[TPR < 256 ? 8 : TPR / 32];
     const int64_t base = row * a.cols;
-    // past a row's end: the mask's zeros
     if (a.h != nullptr) {
 #pragma unroll
       for (int c = 0; c < NCH; ++c)
         store_row<BF16, TPR, NCH, STAGED>(a, a.h, a.g_h, base, has, t, stage, c, v[c]);
     }
-    const float2 r = team_moments<TPR, NCH, RING>(v, a.cols, t, red);
+    const float2 r = moments<RING>(v, a.cols, t, red);
     if (!release()) return;
-    const float var = a.cols > 0 ? __fdiv_rn(r.y, (float)a.cols) : 0.0f;
-    const float s = __frsqrt_rn(__fadd_rn(var, a.eps));
+    const float s = __frsqrt_rn(__fmaf_rn(r.y, inv_cols, a.eps));
     if (live && t == 0) {
       if (a.mean != nullptr) a.mean[row] = r.x;
       if (a.rstd != nullptr) a.rstd[row] = s;

@@ -106,7 +106,7 @@ __device__ __forceinline__ void backward_emit(const LayerNormBackwardKernelArgs&
       co.set(d);
       co.store_warp<STAGED>(a.dres, base + col, n, run, a.g_dres, stage, lane);
     }
-    drop.apply(base + col, d);
+    drop.apply<BF16>(base + col, d, nullptr);
     co.set(d);
     co.store_warp<STAGED>(a.dx, base + col, n, run, a.g_dx, stage, lane);
   }

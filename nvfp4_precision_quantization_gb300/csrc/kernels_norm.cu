@@ -28,12 +28,18 @@ struct RmsNorm {
     return 1;
   }
 
+  template <int TPR, int NCH>
+  struct Team;
+};
+
+template <int TPR, int NCH>
+struct RmsNorm::Team {
+  __device__ __forceinline__ Team(const NormKernelArgs&, int) {}
   // has: the row's values arrived (they have not where a bounded wait gave up)
-  template <bool BF16, bool NV4, int TPR, int NCH, bool STAGED, bool RING, class Release>
-  __device__ __forceinline__ static void row(const NormKernelArgs& a, int64_t row, bool live,
-                                             bool has, int t, uint8_t* stage,
-                                             float (&v)[NCH][kChunk], float2* red,
-                                             const Release& release) {
+  template <bool BF16, bool NV4, bool STAGED, bool RING, class Release>
+  __device__ __forceinline__ void row(const NormKernelArgs& a, int64_t row, bool live, bool has,
+                                      int t, uint8_t* stage, float (&v)[NCH][kChunk], float2* red,
+                                      const Release& release) const {
     const int64_t base = row * a.cols;
     // h out, then h w with the sum of h^2 and the maxima of |h w|
     float bmax[NCH], ss = 0.0f, mx = 0.0f;

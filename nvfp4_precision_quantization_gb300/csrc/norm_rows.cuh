@@ -4,9 +4,10 @@
 // kernels_layernorm.cu):
 //   OP::kMasked   whether x goes through a dropout mask first
 //   OP::ring_ctas CTAs per SM that the registers of the kernel for many aligned rows allow
-//   OP::row<...>  statistics and outputs of a row whose h (x + residual) is in registers; it
-//                 calls release() after its first barrier (by then every thread has the row),
-//                 and leaves if that is false.
+//   OP::Team      what a thread of a row's team keeps from row to row; its row<...> makes the
+//                 statistics and outputs of a row whose h (x + residual) is in registers, calls
+//                 release() after its first barrier (by then every thread has the row), and
+//                 leaves if that is false.
 //
 // Bound by memory: every tensor is read or written once.  A row's team of threads holds the row
 // in registers (16 consecutive elements per thread and step), so no statistic and no amax
@@ -176,6 +177,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_norm(const NormKernel
   const int t = threadIdx.x % TPR, team = threadIdx.x / TPR, lane = threadIdx.x & 31;
   uint8_t* stage = stages[STAGED ? threadIdx.x >> 5 : 0];
   const Dropper drop(a.mask);
+  const typename OP::template Team<TPR, NCH> op(a, t);
   int buf = 0;
   for (int64_t row0 = (int64_t)blockIdx.x * kTeams; row0 < a.rows;
        row0 += (int64_t)gridDim.x * kTeams, buf ^= 1) {
@@ -197,15 +199,17 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_norm(const NormKernel
       const Chunk<BF16>& cx = lx[c].settle(a.g_x, stage, lane);
 #pragma unroll
       for (int i = 0; i < kChunk; ++i) v[c][i] = cx.get(i);
-      if constexpr (OP::kMasked) drop.apply(base + (c * TPR + t) * kChunk, v[c]);
-      if (a.res != nullptr) {
+      if constexpr (OP::kMasked) {
+        drop.apply(base + (c * TPR + t) * kChunk, v[c],
+                   a.res != nullptr ? &lr[c].settle(a.g_res, stage, lane) : nullptr);
+      } else if (a.res != nullptr) {
         const Chunk<BF16>& cr = lr[c].settle(a.g_res, stage, lane);
 #pragma unroll
         for (int i = 0; i < kChunk; ++i) v[c][i] = __fadd_rn(v[c][i], cr.get(i));
       }
     }
-    OP::template row<BF16, NV4, TPR, NCH, STAGED, false>(a, row, live, live, t, stage, v, red[buf],
-                                                         [] { return true; });
+    op.template row<BF16, NV4, STAGED, false>(a, row, live, live, t, stage, v, red[buf],
+                                              [] { return true; });
   }
 }
 
@@ -237,6 +241,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR,
   const RowRing<2, ANY> ring{full, &err, ring_smem, {a.x, a.res}, a.rows,
                              (int64_t)a.cols * kElem, kTeams, g};
   const Dropper drop(a.mask);
+  const typename OP::template Team<TPR, NCH> op(a, t);
   ring.start(step);
   int it = 0, s = 0;
   for (int64_t row0 = (int64_t)blockIdx.x * kTeams; row0 < a.rows; row0 += step, ++it) {
@@ -260,21 +265,24 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR,
       }
 #pragma unroll
       for (int i = 0; i < kChunk; ++i) v[c][i] = cx.get(i);
-      if constexpr (OP::kMasked) drop.apply(base + col, v[c]);
+      Chunk<BF16> cr;
       if (a.res != nullptr) {
-        Chunk<BF16> cr;
         if constexpr (ANY) {
           cr.load_shared_any(st + g.tensor_bytes + min(col, a.cols) * kElem, lane);
           cr.cut(n);
         } else {
           cr.load_shared(st + g.tensor_bytes + col * kElem, n, lane);
         }
+      }
+      if constexpr (OP::kMasked) {
+        drop.apply(base + col, v[c], a.res != nullptr ? &cr : nullptr);
+      } else if (a.res != nullptr) {
 #pragma unroll
         for (int i = 0; i < kChunk; ++i) v[c][i] = __fadd_rn(v[c][i], cr.get(i));
       }
     }
     bool left = false;
-    OP::template row<BF16, NV4, TPR, NCH, ANY, true>(
+    op.template row<BF16, NV4, ANY, true>(
         a, row, live, live && ok, t, out_stage, v, red[it & 1], [&] {
           if (*(volatile int*)&err) {
             ring.give_up(it, row0, step, a.status);
