@@ -130,6 +130,26 @@ struct LayerNorm::Team {
     }
   }
 
+  // v = (v - m) s w + b of 16 columns (w and b are zero past the row's end); their largest |y|.
+  template <bool WEIGHT_BF16>
+  __device__ __forceinline__ static float affine(const NormKernelArgs& a, int col, float m,
+                                                 float s, float (&v)[kChunk]) {
+    const int n = chunk_len(col, a.cols);
+    Chunk<WEIGHT_BF16> w, b;
+    w.load(a.w, col, n, a.g_w);
+    b.load(a.b, col, a.b != nullptr ? n : 0, a.g_b);
+    float top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kChunk; i += 2) {
+      const Pair d = pair_mul(pair_add({v[i], v[i + 1]}, {-m, -m}), {s, s});
+      const Pair y = pair_fma(d, {w.get(i), w.get(i + 1)}, {b.get(i), b.get(i + 1)});
+      v[i] = y.x;
+      v[i + 1] = y.y;
+      asm("max.abs.f32 %0, %0, %1, %2;" : "+f"(top) : "f"(y.x), "f"(y.y));  // NaN skipped
+    }
+    return top;
+  }
+
   template <bool BF16, bool NV4, bool STAGED, bool RING, class Release>
   __device__ __forceinline__ void row(const NormKernelArgs& a, int64_t row, bool live, bool has,
                                       int t, uint8_t* stage, float (&v)[NCH][kChunk], float2* red,
@@ -153,24 +173,8 @@ struct LayerNorm::Team {
     float bmax[NCH], mx = 0.0f;
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
-      const int col = (c * TPR + t) * kChunk, n = chunk_len(col, a.cols);
-      float w[kChunk], b[kChunk];
-      load_vector16(a.w, a.w_bf16, col, n, a.g_w, w);
-      if (a.b != nullptr) {
-        load_vector16(a.b, a.w_bf16, col, n, a.g_b, b);
-      } else {
-#pragma unroll
-        for (int i = 0; i < kChunk; ++i) b[i] = 0.0f;
-      }
-      bmax[c] = 0.0f;
-#pragma unroll
-      for (int i = 0; i < kChunk; i += 2) {  // w and b are zero past the row's end
-        const Pair n2 = pair_mul(pair_add({v[c][i], v[c][i + 1]}, {-r.x, -r.x}), {s, s});
-        const Pair y = pair_fma(n2, {w[i], w[i + 1]}, {b[i], b[i + 1]});
-        v[c][i] = y.x;
-        v[c][i + 1] = y.y;
-        if (quantized) bmax[c] = fmaxf(fmaxf(bmax[c], fabsf(y.x)), fabsf(y.y));
-      }
+      const int col = (c * TPR + t) * kChunk;
+      bmax[c] = a.w_bf16 ? affine<true>(a, col, r.x, s, v[c]) : affine<false>(a, col, r.x, s, v[c]);
       mx = fmaxf(mx, bmax[c]);
     }
     if (NV4 ? a.amax_in == nullptr : quantized && !a.q8_blocks) mx = team_max<TPR>(mx, maxima);

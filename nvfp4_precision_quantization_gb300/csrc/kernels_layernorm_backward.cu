@@ -50,6 +50,25 @@ struct ParamSums {
   }
 };
 
+// Adds 16 columns of a row to a thread's sums of the parameters' gradients (w, b) and of the row's
+// g and g n (total, dot); wc: the weights.
+template <bool BF16, bool WEIGHT_BF16>
+__device__ __forceinline__ void gather16(const Chunk<WEIGHT_BF16>& wc, float m, float s,
+                                         const Chunk<BF16>& cy, const Chunk<BF16>& ch,
+                                         Pair (&w)[kChunk / 2], Pair (&b)[kChunk / 2], Pair& total,
+                                         Pair& dot) {
+#pragma unroll
+  for (int i = 0; i < kChunk / 2; ++i) {
+    const Pair dy = chunk_pair(cy, i);
+    const Pair n = pair_mul(pair_add(chunk_pair(ch, i), {-m, -m}), {s, s});
+    const Pair g = pair_mul(dy, chunk_pair(wc, i));
+    w[i] = pair_fma(dy, n, w[i]);
+    b[i] = pair_add(dy, b[i]);
+    total = pair_add(total, g);
+    dot = pair_fma(g, n, dot);
+  }
+}
+
 // Adds a row to a thread's sums; the row's own sums of g and g n of those columns.
 template <bool BF16, int TPR, int NCH>
 __device__ __forceinline__ float2 backward_gather(const LayerNormBackwardKernelArgs& a, int t,
@@ -59,24 +78,36 @@ __device__ __forceinline__ float2 backward_gather(const LayerNormBackwardKernelA
   Pair total = {0.0f, 0.0f}, dot = {0.0f, 0.0f};
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
-    const int col = (c * TPR + t) * kChunk;
-    float w[kChunk];
-    load_vector16(a.w, a.w_bf16, col, chunk_len(col, a.cols), a.g_w, w);
-#pragma unroll
-    for (int i = 0; i < kChunk / 2; ++i) {
-      const Pair dy = chunk_pair(cy[c], i);
-      const Pair n = pair_mul(pair_add(chunk_pair(ch[c], i), {-m, -m}), {s, s});
-      const Pair g = pair_mul(dy, {w[2 * i], w[2 * i + 1]});
-      sums.w[c][i] = pair_fma(dy, n, sums.w[c][i]);
-      sums.b[c][i] = pair_add(dy, sums.b[c][i]);
-      total = pair_add(total, g);
-      dot = pair_fma(g, n, dot);
+    const int col = (c * TPR + t) * kChunk, n = chunk_len(col, a.cols);
+    if (a.w_bf16) {
+      Chunk<true> w;
+      w.load(a.w, col, n, a.g_w);
+      gather16(w, m, s, cy[c], ch[c], sums.w[c], sums.b[c], total, dot);
+    } else {
+      Chunk<false> w;
+      w.load(a.w, col, n, a.g_w);
+      gather16(w, m, s, cy[c], ch[c], sums.w[c], sums.b[c], total, dot);
     }
   }
   return make_float2(__fadd_rn(total.x, total.y), __fadd_rn(dot.x, dot.y));
 }
 
-// dr and dx of a thread's columns; cd: dh (unused without one); mg, mgn: the row's means.
+// dr of 16 columns without dh; mg, mgn: the row's means.
+template <bool BF16, bool WEIGHT_BF16>
+__device__ __forceinline__ void slope16(const Chunk<WEIGHT_BF16>& wc, float m, float s, float mg,
+                                        float mgn, const Chunk<BF16>& cy, const Chunk<BF16>& ch,
+                                        float (&d)[kChunk]) {
+#pragma unroll
+  for (int i = 0; i < kChunk / 2; ++i) {
+    const Pair n = pair_mul(pair_add(chunk_pair(ch, i), {-m, -m}), {s, s});
+    Pair g = pair_fma(chunk_pair(cy, i), chunk_pair(wc, i), {-mg, -mg});
+    g = pair_mul(pair_fma(n, {-mgn, -mgn}, g), {s, s});
+    d[2 * i] = g.x;
+    d[2 * i + 1] = g.y;
+  }
+}
+
+// dr and dx of a thread's columns; cd: dh (unused without one).
 template <bool BF16, int TPR, int NCH, bool STAGED>
 __device__ __forceinline__ void backward_emit(const LayerNormBackwardKernelArgs& a,
                                               const Dropper& drop, int64_t base, bool live, int t,
@@ -87,28 +118,35 @@ __device__ __forceinline__ void backward_emit(const LayerNormBackwardKernelArgs&
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
-    const int col = (c * TPR + t) * kChunk;
-    const int n = live ? chunk_len(col, a.cols) : 0;
+    const int col = (c * TPR + t) * kChunk, all = chunk_len(col, a.cols);
+    const int n = live ? all : 0;
     const int64_t run = live ? warp_run(col - kChunk * lane, a.cols) : 0;
-    float w[kChunk], d[kChunk];
-    load_vector16(a.w, a.w_bf16, col, chunk_len(col, a.cols), a.g_w, w);
+    float d[kChunk];
+    if (a.w_bf16) {
+      Chunk<true> w;
+      w.load(a.w, col, all, a.g_w);
+      slope16(w, m, s, mg, mgn, cy[c], ch[c], d);
+    } else {
+      Chunk<false> w;
+      w.load(a.w, col, all, a.g_w);
+      slope16(w, m, s, mg, mgn, cy[c], ch[c], d);
+    }
+    if (a.dh != nullptr) {
 #pragma unroll
-    for (int i = 0; i < kChunk / 2; ++i) {
-      const Pair nn = pair_mul(pair_add(chunk_pair(ch[c], i), {-m, -m}), {s, s});
-      Pair g = pair_fma(chunk_pair(cy[c], i), {w[2 * i], w[2 * i + 1]}, {-mg, -mg});
-      g = pair_mul(pair_fma(nn, {-mgn, -mgn}, g), {s, s});
-      if (a.dh != nullptr) g = pair_add(g, chunk_pair(cd[c], i));
-      d[2 * i] = g.x;
-      d[2 * i + 1] = g.y;
+      for (int i = 0; i < kChunk; i += 2) {
+        const Pair g = pair_add({d[i], d[i + 1]}, chunk_pair(cd[c], i / 2));
+        d[i] = g.x;
+        d[i + 1] = g.y;
+      }
     }
     Chunk<BF16> co;
     if (a.dres != nullptr) {
       co.set(d);
-      co.store_warp<STAGED>(a.dres, base + col, n, run, a.g_dres, stage, lane);
+      co.template store_warp<STAGED>(a.dres, base + col, n, run, a.g_dres, stage, lane);
     }
     drop.apply<BF16>(base + col, d, nullptr);
     co.set(d);
-    co.store_warp<STAGED>(a.dx, base + col, n, run, a.g_dx, stage, lane);
+    co.template store_warp<STAGED>(a.dx, base + col, n, run, a.g_dx, stage, lane);
   }
 }
 
@@ -201,7 +239,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
   for (int64_t row0 = (int64_t)blockIdx.x * kTeams; row0 < a.rows;
        row0 += (int64_t)gridDim.x * kTeams, buf ^= 1) {
     const int64_t row = row0 + team;
-    const bool live = row < a.rows;
+    const bool live = kTeams == 1 || row < a.rows;
     const int64_t base = row * a.cols;
     const float m = live ? a.mean[row] : 0.0f, s = live ? a.rstd[row] : 0.0f;
     Chunk<BF16> cy[NCH], ch[NCH], cd[NCH];
@@ -232,9 +270,14 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
   backward_partials<TPR, NCH>(a, t, team, sums, s_sum);
 }
 
+constexpr int backward_ctas(int threads) {
+  const int n = 512 / (threads < 256 ? 256 : threads);
+  return n > 0 ? n : 1;
+}
+
 // Many rows through a shared-memory ring.  ANY: rows that are not 16-byte aligned (RowRing).
 template <bool BF16, int TPR, int NCH, bool ANY>
-__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
+__global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, backward_ctas(TPR))
     k_layernorm_backward_ring(const LayerNormBackwardKernelArgs a, const RingArgs g) {
   if (a.part != nullptr) pdl_launch_dependents();  // as above
   constexpr int kThreads = TPR < 256 ? 256 : TPR;
@@ -255,10 +298,17 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
   ring.start(step);
   ParamSums<NCH> sums;
   int it = 0, st = 0;
+  // a row's statistics are loaded a row ahead: nothing else of it comes from far
+  float next_m = 0.0f, next_s = 0.0f;
+  auto fetch = [&](int64_t row) {
+    if (row < a.rows) next_m = a.mean[row], next_s = a.rstd[row];
+  };
+  fetch((int64_t)blockIdx.x * kTeams + team);
   for (int64_t row0 = (int64_t)blockIdx.x * kTeams; row0 < a.rows; row0 += step, ++it) {
     const int64_t row = row0 + team;
-    const bool live = row < a.rows;
-    const float m = live ? a.mean[row] : 0.0f, s = live ? a.rstd[row] : 0.0f;
+    const bool live = kTeams == 1 || row < a.rows;
+    const float m = live ? next_m : 0.0f, s = live ? next_s : 0.0f;
+    fetch(row + step);
     const uint8_t* p = ring.stage(st) + ring.shift(row0) + team * a.cols * kElem;
     const bool ok = ring.wait(st, it);
     ring.finish(st, row0);

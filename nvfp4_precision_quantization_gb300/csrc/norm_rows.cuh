@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR) k_norm(const NormKernel
   for (int64_t row0 = (int64_t)blockIdx.x * kTeams; row0 < a.rows;
        row0 += (int64_t)gridDim.x * kTeams, buf ^= 1) {
     const int64_t row = row0 + team;
-    const bool live = row < a.rows;
+    const bool live = kTeams == 1 || row < a.rows;
     const int64_t base = row * a.cols;
     float v[NCH][kChunk];
     ChunkLoad<BF16, STAGED> lx[NCH], lr[NCH];
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR,
   int it = 0, s = 0;
   for (int64_t row0 = (int64_t)blockIdx.x * kTeams; row0 < a.rows; row0 += step, ++it) {
     const int64_t row = row0 + team;
-    const bool live = row < a.rows;
+    const bool live = kTeams == 1 || row < a.rows;
     const int64_t base = row * a.cols;
     const uint8_t* st = ring.stage(s) + ring.shift(row0) + team * a.cols * kElem;
     const bool ok = ring.wait(s, it);

@@ -506,5 +506,8 @@ __device__ __forceinline__ int chunk_len(int64_t c, int64_t cols) {
   const int64_t left = cols - c;
   return left >= kChunk ? kChunk : (left > 0 ? (int)left : 0);
 }
+__device__ __forceinline__ int chunk_len(int c, int cols) {
+  return max(0, min(kChunk, cols - c));
+}
 
 }  // namespace nvfp4
