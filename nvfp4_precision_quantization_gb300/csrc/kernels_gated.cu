@@ -11,18 +11,26 @@
 //
 // Structure (persistent: pair c walks the tiles c, c + pairs, ..., groups of 16 M tiles side by
 // side so their A tiles stay in L2):
-//   warp 0    producer, in both CTAs: TMA loads of codes (128 B of K per row, 128B swizzle) and of
-//             scales in the layout of their TMEM copies, into a ring of kStages stages; all
-//             complete on the leader's (rank 0's) barriers;
-//   warp 1    TMEM; in the leader, one thread copies each stage's scales to both CTAs' tensor
-//             memory and issues the MMAs, then releases the stage and, after a tile, the
-//             accumulators, in both CTAs (tcgen05.commit, multicast);
-//   warps 2-9 epilogue, in both CTAs, two per TMEM lane quarter (64 columns of D each):
-//             accumulators to registers, TMEM handed back to the leader, then bias,
-//             activation, product, maxima and stores while the next tile's MMAs run.
+//   warp 0     producer, in both CTAs: loads of codes (TMA, 128 B of K per row, 128B swizzle),
+//              which complete on the leader's (rank 0's) barriers, and of scales, on the CTA's
+//              own, into a ring of kStages stages;
+//   warp 1     TMEM; in the leader, one thread issues the MMAs, then releases the stage and,
+//              after a tile, the accumulators, in both CTAs (tcgen05.commit, multicast);
+//   warps 4-7  scales, in both CTAs, one per TMEM lane quarter: from the stage through
+//              registers into tensor memory;
+//   warps 8-15 epilogue, in both CTAs, two per TMEM lane quarter (64 columns of D each):
+//              accumulators to registers, TMEM handed back to the leader, then bias,
+//              activation, product, maxima and stores while the next tile's MMAs run.
 // A pre-pass (k_gated_scales) rewrites the compact scales into 512-byte pieces of 128 lines x 4
-// scales, line l at byte (l % 32) 16 + (l / 32) 4, one tcgen05.cp .32x128b.warpx4 each, and
-// clears the maxima.
+// scales, line l at byte (l % 32) 16 + (l / 32) 4: what lane l % 32 of every lane quarter holds for
+// a K step, and clears the maxima.
+//
+// The scales go through registers because a tcgen05.cp takes about 50 cycles of the MMAs' own
+// in-order pipe whatever it moves, and a K tile would need twelve (six of the largest form): 8192 x
+// 14336 x 8192 takes 1122 us so, 646 this way, 649 with the copies left out.  Measured, SILU: 16384
+// x 14336 x 8192 1458 us with [g | u] and the maxima kept, 5.3 PFLOP/s; 8192 rows without them
+// 646 us, 6.0 PFLOP/s, of which 60 us are the epilogue's; what is left is the ring (0.38 us a K tile
+// of 76 KB a pair, 15 TB/s from L2, with or without the MMAs).
 //
 // Every wait is bounded, as in kernels_gemm.cu; the CTAs of a pair meet before either leaves.
 #include <cuda_bf16.h>
@@ -49,9 +57,15 @@ constexpr int kPiece = 512;                // scales of 128 lines and one K step
 constexpr int kSfaBytes = kKSteps * kPiece;
 constexpr int kSfbBytes = 2 * kSfaBytes;   // of all 256 lines
 constexpr int kStageBytes_ = kABytes + kBBytes + kSfaBytes + kSfbBytes;
-constexpr int kEpilogueWarps = 8;
+constexpr int kScaleWarp0 = 4, kScaleWarps = 4;  // one per TMEM lane quarter
+constexpr int kEpilogueWarp0 = 8, kEpilogueWarps = 8;
 constexpr int kWarpCols = kCols / 2;       // columns of D per epilogue warp
-constexpr int kThreads = 64 + 32 * kEpilogueWarps;
+constexpr int kThreads = 32 * (kEpilogueWarp0 + kEpilogueWarps);
+// Registers by warpgroup (producer and MMA, scales, epilogue twice): an epilogue thread holds 128
+// accumulators, so the others give theirs up.  The shares add up to what the block is launched
+// with, 128 each.
+constexpr int kRegsIssue = 64, kRegsScales = 96, kRegsEpilogue = 176;
+static_assert(kRegsIssue + kRegsScales + 2 * kRegsEpilogue == 4 * 65536 / kThreads, "registers");
 constexpr uint32_t kTmemCols = 512;
 constexpr int kSfCol0 = 2 * kCols;         // scale columns follow the accumulators
 constexpr int kSfCols = 12 * kKSteps;      // per stage: 4 of A and 8 of B per K step
@@ -65,6 +79,8 @@ static_assert(kSmemBytes <= 232448, "shared memory");
 constexpr int kRasterGroup = 16;  // M tiles walked together so their A tiles stay in L2
 
 struct GatedParams {
+  const uint8_t* sfa;  // the pre-pass's scales
+  const uint8_t* sfb;
   const float* a_amax;
   const float* b_amax;
   int a_amax_stride, b_amax_stride;  // 1 (per line) or 0 (per tensor)
@@ -78,6 +94,12 @@ struct GatedParams {
   uint32_t idesc;
   int* status;
 };
+
+// The low bits that the rows of D and gu start with.
+__host__ __device__ inline uintptr_t alignment(const GatedParams& p) {
+  return reinterpret_cast<uintptr_t>(p.d) | reinterpret_cast<uintptr_t>(p.out.gu) |
+         (uintptr_t)p.n * (p.d_bf16 ? 2 : 4);
+}
 
 __device__ __forceinline__ void tile_at(const GatedParams& p, int tile, int& tm, int& tn) {
   const int group = tile / (kRasterGroup * p.tiles_n), first = group * kRasterGroup;
@@ -95,7 +117,7 @@ struct ScaleArgs {
   int64_t m, n, k16;
   int k_tiles;
   int a_blocks, b_blocks;  // of 128 lines: A's; B's, gate and up by turns
-  uint8_t* out;            // [a_blocks + b_blocks][k_tiles][kKSteps][512]
+  uint8_t* out;            // [a_blocks][k_tiles], then [b_blocks / 2][k_tiles][2] times kSfaBytes
   float* row_amax;         // cleared, as is col_amax
   float* col_amax;
 };
@@ -116,7 +138,7 @@ __global__ void __launch_bounds__(256) k_gated_scales(const ScaleArgs a) {
     }
   }
   // lines [first, end) of sc
-  const bool is_a = blk < a.a_blocks;
+  const bool is_a = blk < a.a_blocks;  // [a_blocks][k_tiles]; [b_blocks / 2][k_tiles][2]
   const int bb = blk - a.a_blocks, half = bb & 1;
   const uint8_t* sc = is_a ? a.a : a.b;
   const int64_t first = is_a ? (int64_t)blk * kRows : half * a.n + (int64_t)(bb >> 1) * kRows;
@@ -148,11 +170,16 @@ __global__ void __launch_bounds__(256) k_gated_scales(const ScaleArgs a) {
     for (int j = 0; j < 4; ++j) words[l][4 * c + j] = w[j];
   }
   __syncthreads();
-  uint4* out = reinterpret_cast<uint4*>(a.out + ((int64_t)blk * a.k_tiles + kt0) * kSfaBytes);
+  // a block's K tiles follow one another (A) or alternate with the other half's (B)
+  const int64_t tile0 = is_a ? (int64_t)blk * a.k_tiles + kt0
+                             : (int64_t)a.a_blocks * a.k_tiles +
+                                   ((int64_t)(bb >> 1) * a.k_tiles + kt0) * 2 + half;
+  uint4* out = reinterpret_cast<uint4*>(a.out + tile0 * kSfaBytes);
   const int steps = min(kScaleTiles, a.k_tiles - kt0) * kKSteps;
   for (int i = threadIdx.x; i < 32 * steps; i += 256) {
-    const int ks = i >> 5, r = i & 31;
-    out[i] = make_uint4(words[r][ks], words[r + 32][ks], words[r + 64][ks], words[r + 96][ks]);
+    const int ks = i >> 5, r = i & 31, kt = ks / kKSteps;
+    out[i + (is_a ? 0 : kt * kSfaBytes / 16)] =
+        make_uint4(words[r][ks], words[r + 32][ks], words[r + 64][ks], words[r + 96][ks]);
   }
 }
 
@@ -185,13 +212,38 @@ __device__ __forceinline__ void raise(float* to, float v) {
   atomicMax(reinterpret_cast<int*>(to), __float_as_int(v));
 }
 
+// 32 consecutive output columns of one row (`cols` of them exist, a whole number of 16-byte
+// units), in 32-byte (v8) or 16-byte stores.
+__device__ __forceinline__ void store_cols32(void* base, bool bf16, int64_t off, const float* v,
+                                             int cols, bool v8) {
+  if (cols >= 32) {
+    store_run32(base, bf16, off, v, v8);
+    return;
+  }
+  if (bf16) {
+#pragma unroll
+    for (int j = 0; j < 32; j += 8)
+      if (j < cols)
+        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(base) + off + j) =
+            make_uint4(bf16x2_bits(v[j], v[j + 1]), bf16x2_bits(v[j + 2], v[j + 3]),
+                       bf16x2_bits(v[j + 4], v[j + 5]), bf16x2_bits(v[j + 6], v[j + 7]));
+  } else {
+#pragma unroll
+    for (int j = 0; j < 32; j += 4)
+      if (j < cols)
+        *reinterpret_cast<float4*>(static_cast<float*>(base) + off + j) =
+            make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+  }
+}
+
 // A warp's 32 rows (one per lane) x 32 columns of D inside D (rows, cols of them): g and u are
-// the projections with their bias.  v16: whole, 16-byte aligned runs, moved by each lane in its
-// own row; otherwise blocks are transposed and a request covers 32 neighbouring columns of a row.
-// rmax: the lane's row's maximum (v16) so far.
+// the projections with their bias.  ALIGNED: rows of D and gu start on 16 bytes, and each lane
+// moves its own; otherwise blocks are transposed and a request covers 32 neighbouring columns of
+// a row.  rmax: the lane's row's maximum (ALIGNED) so far.
+template <bool ALIGNED>
 __device__ __forceinline__ void gated_block32(const GatedParams& p, int row0, int col0, int rows,
-                                              int cols, float* g, float* u, bool v16, bool v8,
-                                              int lane, float& rmax) {
+                                              int cols, float* g, float* u, bool v8, int lane,
+                                              float& rmax) {
   const bool maxima = p.out.row_amax != nullptr || p.out.col_amax != nullptr;
   auto finish = [&] {  // g = act(g) u
     apply_act<32>(p.epi.act, g);
@@ -201,70 +253,75 @@ __device__ __forceinline__ void gated_block32(const GatedParams& p, int row0, in
   auto stored = [&](float v) {  // as D holds it, NaN skipped
     return fmaxf(fabsf(p.d_bf16 ? __bfloat162float(__float2bfloat16_rn(v)) : v), 0.0f);
   };
-  if (v16) {
+  if constexpr (ALIGNED) {
     const bool live = lane < rows;
     const int64_t off = (int64_t)(row0 + lane) * p.n + col0;
     if (p.out.gu != nullptr && live) {
       const int64_t at = (int64_t)(row0 + lane) * 2 * p.n + col0;
-      store_run32(p.out.gu, p.d_bf16, at, g, v8);
-      store_run32(p.out.gu, p.d_bf16, at + p.n, u, v8);
+      store_cols32(p.out.gu, p.d_bf16, at, g, cols, v8);
+      store_cols32(p.out.gu, p.d_bf16, at + p.n, u, cols, v8);
     }
     finish();
-    if (live) store_run32(p.d, p.d_bf16, off, g, v8);
+    if (live) store_cols32(p.d, p.d_bf16, off, g, cols, v8);
     if (!maxima) return;
 #pragma unroll
     for (int j = 0; j < 32; ++j) {
-      g[j] = live ? stored(g[j]) : 0.0f;
+      g[j] = live && j < cols ? stored(g[j]) : 0.0f;
       rmax = fmaxf(rmax, g[j]);
     }
-    if (p.out.col_amax != nullptr) raise(p.out.col_amax + col0 + lane, lanes_max32(g, lane));
-    return;
-  }
-  transpose32(g, lane);  // g[i]: row row0 + i, column col0 + lane
-  transpose32(u, lane);
-  const bool live = lane < cols;
-  auto store = [&](void* base, int64_t at, int64_t pitch, const float* v) {
+    if (p.out.col_amax != nullptr) {
+      const float m = lanes_max32(g, lane);
+      if (lane < cols) raise(p.out.col_amax + col0 + lane, m);
+    }
+  } else {
+    transpose32(g, lane);  // g[i]: row row0 + i, column col0 + lane
+    transpose32(u, lane);
+    const bool live = lane < cols;
+    auto store = [&](void* base, int64_t at, int64_t pitch, const float* v) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i) {
+        if (!live || i >= rows) continue;
+        if (p.d_bf16) static_cast<__nv_bfloat16*>(base)[at + i * pitch] = __float2bfloat16_rn(v[i]);
+        else static_cast<float*>(base)[at + i * pitch] = v[i];
+      }
+    };
+    if (p.out.gu != nullptr) {
+      const int64_t at = (int64_t)row0 * 2 * p.n + col0 + lane;
+      store(p.out.gu, at, 2 * (int64_t)p.n, g);
+      store(p.out.gu, at + p.n, 2 * (int64_t)p.n, u);
+    }
+    finish();
+    store(p.d, (int64_t)row0 * p.n + col0 + lane, p.n, g);
+    if (!maxima) return;
+    float cmax = 0.0f;
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
-      if (!live || i >= rows) continue;
-      if (p.d_bf16) static_cast<__nv_bfloat16*>(base)[at + i * pitch] = __float2bfloat16_rn(v[i]);
-      else static_cast<float*>(base)[at + i * pitch] = v[i];
+      g[i] = live && i < rows ? stored(g[i]) : 0.0f;
+      cmax = fmaxf(cmax, g[i]);
     }
-  };
-  if (p.out.gu != nullptr) {
-    const int64_t at = (int64_t)row0 * 2 * p.n + col0 + lane;
-    store(p.out.gu, at, 2 * (int64_t)p.n, g);
-    store(p.out.gu, at + p.n, 2 * (int64_t)p.n, u);
-  }
-  finish();
-  store(p.d, (int64_t)row0 * p.n + col0 + lane, p.n, g);
-  if (!maxima) return;
-  float cmax = 0.0f;
-#pragma unroll
-  for (int i = 0; i < 32; ++i) {
-    g[i] = live && i < rows ? stored(g[i]) : 0.0f;
-    cmax = fmaxf(cmax, g[i]);
-  }
-  if (p.out.col_amax != nullptr && live) raise(p.out.col_amax + col0 + lane, cmax);
-  if (p.out.row_amax != nullptr) {
-    const float m = lanes_max32(g, lane);
-    if (lane < rows) raise(p.out.row_amax + row0 + lane, m);
+    if (p.out.col_amax != nullptr && live) raise(p.out.col_amax + col0 + lane, cmax);
+    if (p.out.row_amax != nullptr) {
+      const float m = lanes_max32(g, lane);
+      if (lane < rows) raise(p.out.row_amax + row0 + lane, m);
+    }
   }
 }
 
 // ---------------------------------------------------------------- the product
 
+template <bool ALIGNED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     k_gemm_gated(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_b,
-                 const __grid_constant__ CUtensorMap map_sfa,
-                 const __grid_constant__ CUtensorMap map_sfb, const GatedParams p) {
+                 const GatedParams p) {
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>(
       (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
   float* factors = reinterpret_cast<float*>(smem + kStages * kStageBytes_);
   uint64_t* full = reinterpret_cast<uint64_t*>(reinterpret_cast<uint8_t*>(factors) + kFactorBytes);
   uint64_t* empty = full + kStages;
-  uint64_t* acc_full = empty + kStages;
+  uint64_t* sf_full = empty + kStages;    // the CTA's scales are in shared memory
+  uint64_t* sf_ready = sf_full + kStages;  // the pair's are in tensor memory (the leader's count)
+  uint64_t* acc_full = sf_ready + kStages;
   uint64_t* acc_empty = acc_full + 1;
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 1);
   int* err = reinterpret_cast<int*>(tmem_slot + 1);
@@ -278,6 +335,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
+      mbar_init(&sf_full[s], 1);
+      mbar_init(&sf_ready[s], 2 * kScaleWarps);
     }
     mbar_init(acc_full, 1);
     mbar_init(acc_empty, 2 * kEpilogueWarps);
@@ -285,8 +344,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
     fence_mbar_init();
     prefetch_tmap(&map_a);
     prefetch_tmap(&map_b);
-    prefetch_tmap(&map_sfa);
-    prefetch_tmap(&map_sfb);
   }
   if (warp == 1) {
     pair_tmem_alloc(tmem_slot, kTmemCols);
@@ -298,88 +355,120 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
 
-  if (warp == 0 && lane == 0) {
-    // ---------------- producer
-    pdl_wait();  // the scales are rewritten
-    const uint64_t pol_a = policy_evict_last(), pol_b = policy_evict_normal();
-    uint32_t it = 0;  // K tiles issued, over all tiles of this pair
-    bool ok = true;
-    for (int tile = pair; ok && tile < num_tiles; tile += pairs) {
-      int tm, tn;
-      tile_at(p, tile, tm, tn);
-      const int row = (2 * tm + rank) * kRows, line = rank * p.n + tn * kCols;
-      for (int kt = 0; kt < p.k_tiles; ++kt, ++it) {
-        const uint32_t s = it % kStages;
-        if (it >= (uint32_t)kStages && !mbar_wait_bounded(&empty[s], ((it / kStages) - 1) & 1))
-          *err = 1;
-        if (*(volatile int*)err) {
-          ok = false;
-          break;
+  if (warp < kScaleWarp0) {
+    setmaxnreg_dec<kRegsIssue>();
+    if (warp == 0 && lane == 0) {
+      // ---------------- producer
+      pdl_wait();  // the scales are rewritten
+      const uint64_t pol_a = policy_evict_last(), pol_b = policy_evict_normal();
+      uint32_t it = 0;  // K tiles issued, over all tiles of this pair
+      bool ok = true;
+      for (int tile = pair; ok && tile < num_tiles; tile += pairs) {
+        int tm, tn;
+        tile_at(p, tile, tm, tn);
+        const int row = (2 * tm + rank) * kRows, line = rank * p.n + tn * kCols;
+        for (int kt = 0; kt < p.k_tiles; ++kt, ++it) {
+          const uint32_t s = it % kStages;
+          if (it >= (uint32_t)kStages && !mbar_wait_bounded(&empty[s], ((it / kStages) - 1) & 1))
+            *err = 1;
+          if (*(volatile int*)err) {
+            ok = false;
+            break;
+          }
+          uint8_t* st = smem + s * kStageBytes_;
+          uint8_t* sf = st + kABytes + kBBytes;
+          const uint32_t bar = cluster_addr(&full[s], 0);
+          mbar_expect_tx(&sf_full[s], kSfaBytes + kSfbBytes);
+          bulk_load(sf, p.sfa + ((int64_t)(2 * tm + rank) * p.k_tiles + kt) * kSfaBytes, kSfaBytes,
+                    &sf_full[s], pol_a);
+          bulk_load(sf + kSfaBytes, p.sfb + ((int64_t)tn * p.k_tiles + kt) * kSfbBytes, kSfbBytes,
+                    &sf_full[s], pol_b);
+          if (rank == 0) mbar_expect_tx(&full[s], 2 * (kABytes + kBBytes));
+          pair_tma_load_2d(st, &map_a, bar, kt * kKBytes, row, pol_a);
+          pair_tma_load_2d(st + kABytes, &map_b, bar, kt * kKBytes, line, pol_b);
         }
-        uint8_t* st = smem + s * kStageBytes_;
-        uint8_t* sf = st + kABytes + kBBytes;
-        const uint32_t bar = cluster_addr(&full[s], 0);
-        if (rank == 0) mbar_expect_tx(&full[s], 2 * kStageBytes_);
-        pair_tma_load_2d(st, &map_a, bar, kt * kKBytes, row, pol_a);
-        pair_tma_load_2d(st + kABytes, &map_b, bar, kt * kKBytes, line, pol_b);
-        // 256-byte rows: 8 of a block of A's and 16 of the two blocks of B's, of one K tile
-        pair_tma_load_2d(sf, &map_sfa, bar, 0, ((2 * tm + rank) * p.k_tiles + kt) * 8, pol_a);
-        pair_tma_load_2d(sf + kSfaBytes, &map_sfb, bar, 0, (2 * tn * p.k_tiles + kt) * 8, pol_b);
-        pair_tma_load_2d(sf + 2 * kSfaBytes, &map_sfb, bar, 0, ((2 * tn + 1) * p.k_tiles + kt) * 8,
-                         pol_b);
       }
-    }
-    // drain: every copy issued must have landed before the CTAs may exit
-    if (rank == 0)
-      for (uint32_t j = it > (uint32_t)kStages ? it - kStages : 0; j < it; ++j)
-        if (!mbar_wait_bounded(&full[j % kStages], (j / kStages) & 1)) *err = 1;
-  } else if (warp == 1 && lane == 0 && rank == 0) {
-    // ---------------- MMA issuer
-    uint32_t it = 0, t = 0;
-    bool ok = true;
-    for (int tile = pair; ok && tile < num_tiles; tile += pairs, ++t) {
-      // both CTAs' epilogues of the previous tile have copied the accumulators out
-      if (t > 0 && !mbar_wait_bounded(acc_empty, (t - 1) & 1)) {
-        *err = 1;
-        break;
+      // drain: every copy issued must have landed before the CTAs may exit
+      for (uint32_t j = it > (uint32_t)kStages ? it - kStages : 0; j < it; ++j) {
+        const uint32_t s = j % kStages, ph = (j / kStages) & 1;
+        if (!mbar_wait_bounded(&sf_full[s], ph) || (rank == 0 && !mbar_wait_bounded(&full[s], ph)))
+          *err = 1;
       }
-      tc_fence_after();
-      for (int kt = 0; kt < p.k_tiles; ++kt, ++it) {
-        const uint32_t s = it % kStages;
-        if (!mbar_wait_bounded(&full[s], (it / kStages) & 1)) *err = 1;
-        if (*(volatile int*)err) {
-          ok = false;
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+      // ---------------- MMA issuer
+      uint32_t it = 0, t = 0;
+      bool ok = true;
+      for (int tile = pair; ok && tile < num_tiles; tile += pairs, ++t) {
+        // both CTAs' epilogues of the previous tile have copied the accumulators out
+        if (t > 0 && !mbar_wait_bounded(acc_empty, (t - 1) & 1)) {
+          *err = 1;
           break;
         }
         tc_fence_after();
-        const uint32_t st = smem_addr(smem + s * kStageBytes_), sf = st + kABytes + kBBytes;
-        const uint32_t sfa = tmem + kSfCol0 + s * kSfCols, sfb = sfa + 4 * kKSteps;
+        for (int kt = 0; kt < p.k_tiles; ++kt, ++it) {
+          const uint32_t s = it % kStages;
+          const uint32_t ph = (it / kStages) & 1;
+          if (!mbar_wait_bounded(&sf_ready[s], ph) || !mbar_wait_bounded(&full[s], ph)) *err = 1;
+          if (*(volatile int*)err) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t st = smem_addr(smem + s * kStageBytes_);
+          const uint32_t sfa = tmem + kSfCol0 + s * kSfCols, sfb = sfa + 4 * kKSteps;
+#pragma unroll
+          for (int ks = 0; ks < kKSteps; ++ks)
+            pair_mma_nvf4(tmem, desc_swz128(st + ks * 32), desc_swz128(st + kABytes + ks * 32), p.idesc,
+                          sfa + 4 * ks, sfb + 8 * ks, kt != 0 || ks != 0);
+          pair_commit(&empty[s]);
+        }
+        // the accumulators of this tile are complete (or abandoned) once all issued MMAs are
+        pair_commit(acc_full);
+      }
+      // everything issued must be done before TMEM is freed
+      if (t > 0 && !mbar_wait_bounded(acc_full, (t - 1) & 1)) *err = 1;
+    }
+  } else if (warp < kEpilogueWarp0) {
+    setmaxnreg_dec<kRegsScales>();
+    // ---------------- scales: lane l of a quarter holds the words of lines l, l + 32, ... of a
+    // piece, the same in every quarter
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const int tiles = (num_tiles - pair + pairs - 1) / pairs;
+    const uint32_t all = (uint32_t)tiles * p.k_tiles;
+    for (uint32_t it = 0; it < all; ++it) {
+      const uint32_t s = it % kStages, ph = (it / kStages) & 1;
+      // (the producer refills the stage only when the MMAs that read the slot are done)
+      bool ok = mbar_wait_bounded(&sf_full[s], ph);
+      if (!ok) *err = 1;
+      if (__any_sync(0xffffffffu, !ok || *(volatile int*)err)) break;
+      tc_fence_after();
+      const uint4* from = reinterpret_cast<const uint4*>(smem + s * kStageBytes_ + kABytes + kBBytes) + lane;
+      const uint32_t sf = tmem + lanes + kSfCol0 + s * kSfCols;
+      uint32_t w[3][16];
+#pragma unroll
+      for (int c = 0; c < 3; ++c)
 #pragma unroll
         for (int ks = 0; ks < kKSteps; ++ks) {
-          pair_cp_32x128b(sfa + 4 * ks, desc_plain(sf + ks * kPiece, 0, 128));
-          pair_cp_32x128b(sfb + 8 * ks, desc_plain(sf + kSfaBytes + ks * kPiece, 0, 128));
-          pair_cp_32x128b(sfb + 8 * ks + 4, desc_plain(sf + 2 * kSfaBytes + ks * kPiece, 0, 128));
+          // columns: A's K steps; B's by K step, the gate's lines and then up's
+          const int piece = c == 0 ? ks : kKSteps * (1 + (ks & 1)) + 2 * (c - 1) + (ks >> 1);
+          const uint4 v = from[piece * (kPiece / 16)];
+          w[c][4 * ks] = v.x, w[c][4 * ks + 1] = v.y, w[c][4 * ks + 2] = v.z, w[c][4 * ks + 3] = v.w;
         }
 #pragma unroll
-        for (int ks = 0; ks < kKSteps; ++ks)
-          pair_mma_nvf4(tmem, desc_swz128(st + ks * 32), desc_swz128(st + kABytes + ks * 32), p.idesc,
-                        sfa + 4 * ks, sfb + 8 * ks, kt != 0 || ks != 0);
-        pair_commit(&empty[s]);
-      }
-      // the accumulators of this tile are complete (or abandoned) once all issued MMAs are
-      pair_commit(acc_full);
+      for (int c = 0; c < 3; ++c) tmem_st16(sf + 16 * c, w[c]);
+      tmem_st_wait();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) cluster_arrive(cluster_addr(&sf_ready[s], 0));
     }
-    // everything issued must be done before TMEM is freed
-    if (t > 0 && !mbar_wait_bounded(acc_full, (t - 1) & 1)) *err = 1;
-  } else if (warp >= 2) {
+  } else {
+    setmaxnreg_inc<kRegsEpilogue>();
     // ---------------- epilogue: lane quarter q (rows 32q ..), column half `half`
-    const int q = warp & 3, half = (warp - 2) >> 2;
-    float* beta = factors + (warp - 2) * 4 * kWarpCols;  // [gate, up][64], then their bias
+    const int q = warp & 3, half = (warp - kEpilogueWarp0) >> 2;
+    float* beta = factors + (warp - kEpilogueWarp0) * 4 * kWarpCols;  // [gate, up][64], then their bias
     float* bias = beta + 2 * kWarpCols;
     const uint32_t hand_back = cluster_addr(acc_empty, 0);
-    const int esize = p.d_bf16 ? 2 : 4;
-    uintptr_t align = reinterpret_cast<uintptr_t>(p.d) | reinterpret_cast<uintptr_t>(p.out.gu) |
-                      (uintptr_t)p.n * esize;
+    const bool v8 = (alignment(p) & 31) == 0;
     bool cleared = false;
     uint32_t t = 0;
     for (int tile = pair; tile < num_tiles; tile += pairs, ++t) {
@@ -424,7 +513,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       if (rows <= 0 || cols <= 0) continue;
       if (!cleared && (p.out.row_amax != nullptr || p.out.col_amax != nullptr)) pdl_wait();
       cleared = true;
-      const bool v16 = cols == kWarpCols && (align & 15) == 0, v8 = (align & 31) == 0;
       float rmax = 0.0f;
 #pragma unroll
       for (int c = 0; c < kWarpCols; c += 32) {
@@ -443,9 +531,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
               z[h][j4 + j] = __fadd_rn(
                   __fmul_rn(__fmul_rn(__uint_as_float(v[h][c + j4 + j]), alpha), bj[j]), aj[j]);
           }
-        gated_block32(p, row0, col0 + c, rows, min(32, cols - c), z[0], z[1], v16, v8, lane, rmax);
+        gated_block32<ALIGNED>(p, row0, col0 + c, rows, min(32, cols - c), z[0], z[1], v8, lane, rmax);
       }
-      if (v16 && p.out.row_amax != nullptr && lane < rows) raise(p.out.row_amax + row0 + lane, rmax);
+      if (ALIGNED && p.out.row_amax != nullptr && lane < rows) raise(p.out.row_amax + row0 + lane, rmax);
     }
   }
 
@@ -470,24 +558,14 @@ struct Layout {
         bytes(a_bytes + 2 * tiles_n * k_tiles * kSfaBytes) {}
 };
 
-}  // namespace
-
-int64_t gemm_gated_workspace(int64_t m, int64_t n, int64_t k) { return Layout(m, n, k).bytes; }
-
-cudaError_t launch_gemm_gated(const GemmArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
-  const Layout L(a.M, a.N, a.K);
-  uint8_t* sf = a.workspace;
-  CUtensorMap map_a, map_b, map_sfa, map_sfb;
-  if (!make_operand_map(&map_a, a.a_codes, a.M, a.K / 2, kKBytes, kRows) ||
-      !make_operand_map(&map_b, a.b_codes, 2 * a.N, a.K / 2, kKBytes, kCols) ||
-      !make_byte_map(&map_sfa, sf, L.a_bytes / 256, 256, 256, kSfaBytes / 256) ||
-      !make_byte_map(&map_sfb, sf + L.a_bytes, (L.bytes - L.a_bytes) / 256, 256, 256,
-                     kSfaBytes / 256))
-    return cudaErrorInvalidValue;
+template <bool ALIGNED>
+cudaError_t run(const CUtensorMap& map_a, const CUtensorMap& map_b, const GatedParams& p,
+                int64_t tiles, const DeviceInfo& dev, cudaStream_t stream) {
+  const auto kernel = k_gemm_gated<ALIGNED>;
   static int pairs_of[64] = {};  // clusters that are resident at once, by device
   int pairs = dev.device < 64 ? pairs_of[dev.device] : 0;
   if (pairs == 0) {
-    cudaError_t e = cudaFuncSetAttribute(k_gemm_gated, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          kSmemBytes);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
@@ -500,11 +578,27 @@ cudaError_t launch_gemm_gated(const GemmArgs& a, const DeviceInfo& dev, cudaStre
     at.val.clusterDim.y = at.val.clusterDim.z = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    e = cudaOccupancyMaxActiveClusters(&pairs, k_gemm_gated, &cfg);
+    e = cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg);
     if (e != cudaSuccess) return e;
     if (pairs < 1) return cudaErrorInvalidConfiguration;
     if (dev.device < 64) pairs_of[dev.device] = pairs;
   }
+  kernel<<<(unsigned)(2 * std::min<int64_t>(tiles, pairs)), kThreads, kSmemBytes, stream>>>(
+      map_a, map_b, p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+int64_t gemm_gated_workspace(int64_t m, int64_t n, int64_t k) { return Layout(m, n, k).bytes; }
+
+cudaError_t launch_gemm_gated(const GemmArgs& a, const DeviceInfo& dev, cudaStream_t stream) {
+  const Layout L(a.M, a.N, a.K);
+  uint8_t* sf = a.workspace;
+  CUtensorMap map_a, map_b;
+  if (!make_operand_map(&map_a, a.a_codes, a.M, a.K / 2, kKBytes, kRows) ||
+      !make_operand_map(&map_b, a.b_codes, 2 * a.N, a.K / 2, kKBytes, kCols))
+    return cudaErrorInvalidValue;
   ScaleArgs s{a.a_scales, a.b_scales, a.M, a.N, a.K / 16, (int)L.k_tiles, (int)(2 * L.tiles_m),
               (int)(2 * L.tiles_n), sf, a.gated->row_amax, a.gated->col_amax};
   const int64_t ctas =
@@ -513,6 +607,8 @@ cudaError_t launch_gemm_gated(const GemmArgs& a, const DeviceInfo& dev, cudaStre
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
   GatedParams p{};
+  p.sfa = sf;
+  p.sfb = sf + L.a_bytes;
   p.a_amax = a.a_amax;
   p.b_amax = a.b_amax;
   p.a_amax_stride = a.a_row_scaled ? 1 : 0;
@@ -531,9 +627,8 @@ cudaError_t launch_gemm_gated(const GemmArgs& a, const DeviceInfo& dev, cudaStre
   p.idesc = make_idesc_nvf4(2 * kRows, 2 * kCols);
   p.status = dev.status;
   const int64_t tiles = L.tiles_m * L.tiles_n;
-  k_gemm_gated<<<(unsigned)(2 * std::min<int64_t>(tiles, pairs)), kThreads, kSmemBytes, stream>>>(
-      map_a, map_b, map_sfa, map_sfb, p);
-  return cudaGetLastError();
+  return alignment(p) % 16 == 0 ? run<true>(map_a, map_b, p, tiles, dev, stream)
+                                : run<false>(map_a, map_b, p, tiles, dev, stream);
 }
 
 }  // namespace nvfp4

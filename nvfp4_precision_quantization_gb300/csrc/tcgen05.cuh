@@ -134,8 +134,11 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, uint32_t rank) {
   asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_addr(p)), "r"(rank));
   return a;
 }
+// Arrive on a barrier of either CTA, for what tcgen05 loads and stores did before (their waits
+// and fences order it; a release to the whole cluster as well would wait for every store of
+// the thread: 1 us a K tile of the gated product).
 __device__ __forceinline__ void cluster_arrive(uint32_t bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void pair_tmem_alloc(uint32_t* dst_smem, uint32_t ncols) {
   asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
@@ -167,12 +170,6 @@ __device__ __forceinline__ void pair_commit(uint64_t* bar) {
       "h"((uint16_t)3)
       : "memory");
 }
-// In both CTAs, from their shared memory to their tensor memory: 32 lanes x 128 bits,
-// replicated into all four lane quarters.
-__device__ __forceinline__ void pair_cp_32x128b(uint32_t taddr, uint64_t sdesc) {
-  asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(sdesc)
-               : "memory");
-}
 __device__ __forceinline__ void pair_mma_nvf4(uint32_t d_taddr, uint64_t adesc, uint64_t bdesc,
                                               uint32_t idesc, uint32_t sfa_taddr,
                                               uint32_t sfb_taddr, uint32_t accumulate) {
@@ -183,6 +180,17 @@ __device__ __forceinline__ void pair_mma_nvf4(uint32_t d_taddr, uint64_t adesc, 
       " [%0], %1, %2, %3, [%5], [%6], p;\n\t}" ::"r"(d_taddr),
       "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(sfa_taddr), "r"(sfb_taddr)
       : "memory");
+}
+
+// Registers per thread of this warpgroup from here on: up from what the block was launched with,
+// by what its other warpgroups give up.
+template <int N>
+__device__ __forceinline__ void setmaxnreg_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void setmaxnreg_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 // Instruction descriptor of kind::mxf4nvf4 (dense, K = 64): A and B E2M1 (format
