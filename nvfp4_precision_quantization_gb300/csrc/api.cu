@@ -13,6 +13,7 @@
 // Unlike the wrapper reviewed in PR #3454, amax buffers are never cleared by a
 // host-side memset: clearing happens in a kernel that first checks the noop
 // flag, so a skipped call leaves existing amax metadata untouched.
+#include <algorithm>
 #include <cstring>
 #include <mutex>
 #include <string>
@@ -612,6 +613,11 @@ nvfp4_status nvfp4_gemm_workspace_size(int64_t m, int64_t n, int64_t k, uint64_t
 }
 
 namespace {
+// Of either kernel: which one runs also depends on the alignment of what it writes.
+int64_t gated_workspace(int64_t m, int64_t n, int64_t k) {
+  return std::max(gemm_few_workspace(m, n, true), gemm_gated_workspace(m, n, k));
+}
+
 // workspace == NULL: the static workspace of the current device (nvfp4_gemm_static_ws)
 // group_ends != NULL: the grouped GEMM (num_groups groups of A's rows, B = [groups*n][k])
 nvfp4_status gemm_impl(const nvfp4_operand* a, const nvfp4_operand* b, const int64_t* group_ends,
@@ -665,9 +671,12 @@ nvfp4_status gemm_impl(const nvfp4_operand* a, const nvfp4_operand* b, const int
   if (k_grouped && k % 256 != 0)
     return fail(NVFP4_ERR_UNSUPPORTED, "grouped wgrad GEMM: tokens must be a multiple of 256");
   GemmLayout L = gemm_layout(m, n, k, group_ends && !k_grouped ? (int64_t)num_groups * n : n);
-  const bool few = epilogue != nullptr && (gated ? gemm_gated_few(m, n) : gemm_few(m, n));
-  if (few) L.workspace_bytes = gemm_few_workspace(m, n, gated != nullptr);
-  else if (gated) L.workspace_bytes = gemm_gated_workspace(m, n, k);
+  const uintptr_t row_bits = reinterpret_cast<uintptr_t>(d) | (uintptr_t)n * esize |
+                             (gated ? reinterpret_cast<uintptr_t>(gated->gu) : 0);
+  const bool few = epilogue != nullptr &&
+                   (gated ? gemm_gated_few(m, n, k, row_bits % 16 == 0) : gemm_few(m, n));
+  if (gated) L.workspace_bytes = gated_workspace(m, n, k);
+  else if (few) L.workspace_bytes = gemm_few_workspace(m, n, false);
   if (L.tiles_m * L.tiles_n >= (1LL << 31)) return fail(NVFP4_ERR_UNSUPPORTED, "too many tiles");
   if (static_ws) {
     if ((uint64_t)L.workspace_bytes > (uint64_t)NVFP4_GEMM_STATIC_WS_BYTES)
@@ -760,9 +769,7 @@ nvfp4_status nvfp4_gemm_gated_workspace_size(int64_t m, int64_t n, int64_t k, ui
   nvfp4_status st;
   if ((st = check_gated_sizes(m, n)) != NVFP4_OK) return st;
   if ((st = check_sizes(k, 0)) != NVFP4_OK) return st;
-  *bytes = (m == 0 || n == 0 || k == 0) ? 0
-           : gemm_gated_few(m, n)       ? (uint64_t)gemm_few_workspace(m, n, true)
-                                        : (uint64_t)gemm_gated_workspace(m, n, k);
+  *bytes = (m == 0 || n == 0 || k == 0) ? 0 : (uint64_t)gated_workspace(m, n, k);
   return NVFP4_OK;
 }
 

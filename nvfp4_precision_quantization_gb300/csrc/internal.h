@@ -261,8 +261,9 @@ struct GemmArgs {
 bool gemm_few(int64_t m, int64_t n);
 int64_t gemm_few_workspace(int64_t m, int64_t n, bool gated);  // bytes
 cudaError_t launch_gemm_few(const GemmArgs& a, const DeviceInfo& dev, cudaStream_t stream);
-// The gated product of many rows (kernels_gated.cu); few: launch_gemm_few.
-bool gemm_gated_few(int64_t m, int64_t n);
+// The gated product of many rows (kernels_gated.cu); few: launch_gemm_few.  aligned: the rows of
+// D and gu start on 16 bytes.
+bool gemm_gated_few(int64_t m, int64_t n, int64_t k, bool aligned);
 int64_t gemm_gated_workspace(int64_t m, int64_t n, int64_t k);  // bytes
 cudaError_t launch_gemm_gated(const GemmArgs& a, const DeviceInfo& dev, cudaStream_t stream);
 struct GemmLayout {

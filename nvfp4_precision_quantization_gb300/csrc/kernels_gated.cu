@@ -127,6 +127,7 @@ struct ScaleArgs {
 constexpr int kScaleTiles = 4;
 __global__ void __launch_bounds__(256) k_gated_scales(const ScaleArgs a) {
   __shared__ uint32_t words[kRows][kScaleTiles * kKSteps + 1];
+  pdl_launch_dependents();  // the product is set up meanwhile
   const int groups = (a.k_tiles + kScaleTiles - 1) / kScaleTiles;
   const int blk = blockIdx.x / groups, kt0 = blockIdx.x % groups * kScaleTiles;
   for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < a.m + a.n;
@@ -497,26 +498,35 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       const bool ready = mbar_wait_bounded(acc_full, t & 1);
       if (!ready) *err = 1;
       tc_fence_after();
-      uint32_t v[2][kWarpCols];
+      // All accumulators at once, so that TMEM may take the next tile's MMAs during the rest; rows
+      // that are not aligned have no registers for that beside their transpositions (4 bytes of
+      // spills a value, measured twice as slow), and hand TMEM back after their last block.
+      constexpr int kHeld = ALIGNED ? kWarpCols : 32;
+      uint32_t v[2][kHeld];
+      auto load = [&](int from) {
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+        for (int h = 0; h < 2; ++h)
 #pragma unroll
-        for (int c = 0; c < kWarpCols; c += 32)
-          tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + h * kCols + half * kWarpCols + c, v[h] + c);
-      tmem_ld_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) cluster_arrive(hand_back);  // TMEM may take the next tile's MMAs
+          for (int c = 0; c < kHeld; c += 32)
+            tmem_ld32(tmem + ((uint32_t)(q * 32) << 16) + h * kCols + half * kWarpCols + from + c,
+                      v[h] + c);
+        tmem_ld_wait();
+        if (from + kHeld < kWarpCols) return;
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) cluster_arrive(hand_back);
+      };
+      load(0);
       // the warp leaves together: what follows (shuffles, the next tile's TMEM loads) takes
       // every lane, and each lane's wait gives up by its own clock
       if (__any_sync(0xffffffffu, !ready || *(volatile int*)err)) break;
-      if (rows <= 0 || cols <= 0) continue;
       if (!cleared && (p.out.row_amax != nullptr || p.out.col_amax != nullptr)) pdl_wait();
       cleared = true;
       float rmax = 0.0f;
 #pragma unroll
       for (int c = 0; c < kWarpCols; c += 32) {
-        if (c >= cols) break;
+        if (c > 0 && !ALIGNED) load(c);
+        if (rows <= 0 || c >= cols) continue;
         float z[2][32];
         // fl(fl(acc * alpha) * beta) + bias
 #pragma unroll
@@ -529,7 +539,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int j = 0; j < 4; ++j)
               z[h][j4 + j] = __fadd_rn(
-                  __fmul_rn(__fmul_rn(__uint_as_float(v[h][c + j4 + j]), alpha), bj[j]), aj[j]);
+                  __fmul_rn(__fmul_rn(__uint_as_float(v[h][c % kHeld + j4 + j]), alpha), bj[j]),
+                  aj[j]);
           }
         gated_block32<ALIGNED>(p, row0, col0 + c, rows, min(32, cols - c), z[0], z[1], v8, lane, rmax);
       }
@@ -583,9 +594,17 @@ cudaError_t run(const CUtensorMap& map_a, const CUtensorMap& map_b, const GatedP
     if (pairs < 1) return cudaErrorInvalidConfiguration;
     if (dev.device < 64) pairs_of[dev.device] = pairs;
   }
-  kernel<<<(unsigned)(2 * std::min<int64_t>(tiles, pairs)), kThreads, kSmemBytes, stream>>>(
-      map_a, map_b, p);
-  return cudaGetLastError();
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(2 * std::min<int64_t>(tiles, pairs)));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = stream;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, map_a, map_b, p);
 }
 
 }  // namespace

@@ -850,7 +850,17 @@ cudaError_t launch_gated_epilogue_only(const Epilogue& e, const GatedOut& g, voi
 // 7168) 18 and 31, (512, 4096, 4096) 21 and 26, (1000, 1024, 4096) 14 and 25.
 bool gemm_few(int64_t m, int64_t n) { return m <= 384 || tiles_of(m, n) <= 304; }
 
-bool gemm_gated_few(int64_t m, int64_t n) { return gemm_few(m, n); }
+// Up to one MMA's rows; up to a tile a CTA of short sums, where the other kernel's pre-pass is
+// what counts; and, in up to two rounds of the other kernel, rows of D that are not 16-byte
+// aligned, which its epilogue has to transpose.  This kernel and k_gemm_gated, in us: (m, n, k) =
+// (1, 28672, 8192) 48 and 84, (64, 14336, 8192) 30 and 42; (64, 8192, 8192) 28 and 26, (128, 14336,
+// 8192) 41 and 43, (256, 8192, 8192) 49 and 28; (256, 1024, 1024) 8.8 and 10.2, (256, 2048, 2048)
+// 11.8 both, (2048, 1024, 1024) 14.8 and 11.6; unaligned (500, 1001, 1024) 8.9 and 13.7, (300,
+// 5001, 7168) 37 and 41, (2000, 5001, 2048) 63 and 51.
+bool gemm_gated_few(int64_t m, int64_t n, int64_t k, bool aligned) {
+  return m <= 64 || (k <= 1024 && tiles_of(m, n) <= 152) ||
+         (!aligned && ceil_div(m, 256) * ceil_div(n, 128) <= 152);
+}
 
 int64_t gemm_few_workspace(int64_t m, int64_t n, bool gated) {
   return round256(4 * tiles_of(m, n)) +
