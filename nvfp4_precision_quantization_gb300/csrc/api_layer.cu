@@ -27,8 +27,10 @@ nvfp4_status make_mask(const nvfp4_mask* m, DropMask* out) {
   if (!(m->p >= 0.0f && m->p <= 1.0f)) return fail(NVFP4_ERR_INVALID, "mask->p must be in [0, 1]");
   if (!aligned(m->offset_add, 8))
     return fail(NVFP4_ERR_INVALID, "mask->offset_add is not 8-byte aligned");
-  out->key0 = (uint32_t)m->seed;
-  out->key1 = (uint32_t)(m->seed >> 32);
+  for (uint32_t r = 0; r < 10; ++r) {  // Philox's key schedule
+    out->key0[r] = (uint32_t)m->seed + r * 0x9E3779B9u;
+    out->key1[r] = (uint32_t)(m->seed >> 32) + r * 0xBB67AE85u;
+  }
   out->threshold = (uint32_t)((double)m->p * 65536.0 + 0.5);
   // (everything dropped: the scale is never used)
   out->scale = out->threshold < 65536 ? (float)(65536.0 / (65536 - out->threshold)) : 0.0f;

@@ -276,7 +276,7 @@ cudaError_t launch_gemm(const GemmArgs& a, const DeviceInfo& dev, cudaStream_t s
 
 // A dropout mask (dropout.cuh): an element is dropped where its 16 bits are below threshold.
 struct DropMask {
-  uint32_t key0, key1;   // of the seed
+  uint32_t key0[10], key1[10];  // of the seed, by round
   uint32_t threshold;    // 0 (nothing is dropped) .. 65536 (everything is)
   float scale;           // of what is kept
   uint64_t offset;

@@ -906,7 +906,7 @@ cudaError_t launch_gemm_few(const GemmArgs& a, const DeviceInfo& dev, cudaStream
   const int ctas = std::max(grid, std::min(std::min(dev.num_sms, kMaxCtas), p.split * p.parts));
   if (gated) {
     switch (nt) {
-      case 16: return run_few<16, 4, 4, true>(p, map_w, map_x, ctas, stream);
+      case 16: return run_few<16, 4, 8, true>(p, map_w, map_x, ctas, stream);
       case 32: return run_few<32, 4, 4, true>(p, map_w, map_x, ctas, stream);
       default: return run_few<64, 4, 4, true>(p, map_w, map_x, ctas, stream);
     }

@@ -62,12 +62,16 @@ def test_values(shape, offset, dtype):
     assert torch.equal(y, z)
 
 
-def test_elements_past_32_bits():
-    """4.3 billion elements: the last ones have the bits of their own index."""
-    n = (1 << 32) + 4099
+@pytest.mark.parametrize("bits", [32, 35])
+def test_elements_past_32_bits(bits):
+    """4.3 and 34.4 billion elements: the last ones have the bits of their own index, whose
+    blocks' upper counter word is 0 and 1."""
+    n = (1 << bits) + 4099
+    if torch.cuda.mem_get_info()[0] < 2 * n + (8 << 30):
+        pytest.skip("not enough memory")
     x = torch.ones(n, dtype=torch.bfloat16, device=DEV)
     nv.nvfp4_dropout(x, nv.Mask(0.5, 11, 12), x)
-    first = (1 << 32) - 37
+    first = (1 << bits) - 37
     got = (x[first:] != 0).cpu().numpy()
     assert np.array_equal(got, keep_mask(n - first, 0.5, 11, 12, first))
     assert not np.array_equal(got[37:], (x[:4099] != 0).cpu().numpy())
