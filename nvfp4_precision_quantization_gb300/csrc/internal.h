@@ -348,6 +348,7 @@ constexpr int64_t kNormBackwardParts = 608;  // at most this many CTAs, one part
 int64_t add_rmsnorm_backward_workspace(int64_t rows, int64_t cols);
 cudaError_t launch_add_rmsnorm_backward(const NormBackwardArgs& a, const DeviceInfo& dev,
                                         cudaStream_t stream);
+constexpr int64_t kLayerNormBackwardParts = 320;  // two CTAs on each of up to 160 SMs
 int64_t add_layernorm_backward_workspace(int64_t rows, int64_t cols);
 cudaError_t launch_add_layernorm_backward(const NormBackwardArgs& a, const DeviceInfo& dev,
                                           cudaStream_t stream);

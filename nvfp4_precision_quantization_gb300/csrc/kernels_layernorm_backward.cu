@@ -50,22 +50,29 @@ struct ParamSums {
   }
 };
 
+// What a row's values become, kept across its reduction: n = (h - m) s and g = dy w.
+template <int NCH>
+struct RowTerms {
+  Pair n[NCH][kChunk / 2], g[NCH][kChunk / 2];
+};
+
 // Adds 16 columns of a row to a thread's sums of the parameters' gradients (w, b) and of the row's
 // g and g n (total, dot); wc: the weights.
 template <bool BF16, bool WEIGHT_BF16>
 __device__ __forceinline__ void gather16(const Chunk<WEIGHT_BF16>& wc, float m, float s,
                                          const Chunk<BF16>& cy, const Chunk<BF16>& ch,
+                                         Pair (&n)[kChunk / 2], Pair (&g)[kChunk / 2],
                                          Pair (&w)[kChunk / 2], Pair (&b)[kChunk / 2], Pair& total,
                                          Pair& dot) {
 #pragma unroll
   for (int i = 0; i < kChunk / 2; ++i) {
     const Pair dy = chunk_pair(cy, i);
-    const Pair n = pair_mul(pair_add(chunk_pair(ch, i), {-m, -m}), {s, s});
-    const Pair g = pair_mul(dy, chunk_pair(wc, i));
-    w[i] = pair_fma(dy, n, w[i]);
+    n[i] = pair_mul(pair_add(chunk_pair(ch, i), {-m, -m}), {s, s});
+    g[i] = pair_mul(dy, chunk_pair(wc, i));
+    w[i] = pair_fma(dy, n[i], w[i]);
     b[i] = pair_add(dy, b[i]);
-    total = pair_add(total, g);
-    dot = pair_fma(g, n, dot);
+    total = pair_add(total, g[i]);
+    dot = pair_fma(g[i], n[i], dot);
   }
 }
 
@@ -74,7 +81,7 @@ template <bool BF16, int TPR, int NCH>
 __device__ __forceinline__ float2 backward_gather(const LayerNormBackwardKernelArgs& a, int t,
                                                   float m, float s, const Chunk<BF16> (&cy)[NCH],
                                                   const Chunk<BF16> (&ch)[NCH],
-                                                  ParamSums<NCH>& sums) {
+                                                  RowTerms<NCH>& terms, ParamSums<NCH>& sums) {
   Pair total = {0.0f, 0.0f}, dot = {0.0f, 0.0f};
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
@@ -82,62 +89,36 @@ __device__ __forceinline__ float2 backward_gather(const LayerNormBackwardKernelA
     if (a.w_bf16) {
       Chunk<true> w;
       w.load(a.w, col, n, a.g_w);
-      gather16(w, m, s, cy[c], ch[c], sums.w[c], sums.b[c], total, dot);
+      gather16(w, m, s, cy[c], ch[c], terms.n[c], terms.g[c], sums.w[c], sums.b[c], total, dot);
     } else {
       Chunk<false> w;
       w.load(a.w, col, n, a.g_w);
-      gather16(w, m, s, cy[c], ch[c], sums.w[c], sums.b[c], total, dot);
+      gather16(w, m, s, cy[c], ch[c], terms.n[c], terms.g[c], sums.w[c], sums.b[c], total, dot);
     }
   }
   return make_float2(__fadd_rn(total.x, total.y), __fadd_rn(dot.x, dot.y));
 }
 
-// dr of 16 columns without dh; mg, mgn: the row's means.
-template <bool BF16, bool WEIGHT_BF16>
-__device__ __forceinline__ void slope16(const Chunk<WEIGHT_BF16>& wc, float m, float s, float mg,
-                                        float mgn, const Chunk<BF16>& cy, const Chunk<BF16>& ch,
-                                        float (&d)[kChunk]) {
-#pragma unroll
-  for (int i = 0; i < kChunk / 2; ++i) {
-    const Pair n = pair_mul(pair_add(chunk_pair(ch, i), {-m, -m}), {s, s});
-    Pair g = pair_fma(chunk_pair(cy, i), chunk_pair(wc, i), {-mg, -mg});
-    g = pair_mul(pair_fma(n, {-mgn, -mgn}, g), {s, s});
-    d[2 * i] = g.x;
-    d[2 * i + 1] = g.y;
-  }
-}
-
-// dr and dx of a thread's columns; cd: dh (unused without one).
+// dr and dx of a thread's columns; mg, mgn: the row's means; cd: dh (unused without one).
 template <bool BF16, int TPR, int NCH, bool STAGED>
 __device__ __forceinline__ void backward_emit(const LayerNormBackwardKernelArgs& a,
                                               const Dropper& drop, int64_t base, bool live, int t,
-                                              uint8_t* stage, float m, float s, float mg,
-                                              float mgn, const Chunk<BF16> (&cy)[NCH],
-                                              const Chunk<BF16> (&ch)[NCH],
+                                              uint8_t* stage, float s, float mg, float mgn,
+                                              const RowTerms<NCH>& terms,
                                               const Chunk<BF16> (&cd)[NCH]) {
   const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int c = 0; c < NCH; ++c) {
-    const int col = (c * TPR + t) * kChunk, all = chunk_len(col, a.cols);
-    const int n = live ? all : 0;
+    const int col = (c * TPR + t) * kChunk;
+    const int n = live ? chunk_len(col, a.cols) : 0;
     const int64_t run = live ? warp_run(col - kChunk * lane, a.cols) : 0;
     float d[kChunk];
-    if (a.w_bf16) {
-      Chunk<true> w;
-      w.load(a.w, col, all, a.g_w);
-      slope16(w, m, s, mg, mgn, cy[c], ch[c], d);
-    } else {
-      Chunk<false> w;
-      w.load(a.w, col, all, a.g_w);
-      slope16(w, m, s, mg, mgn, cy[c], ch[c], d);
-    }
-    if (a.dh != nullptr) {
 #pragma unroll
-      for (int i = 0; i < kChunk; i += 2) {
-        const Pair g = pair_add({d[i], d[i + 1]}, chunk_pair(cd[c], i / 2));
-        d[i] = g.x;
-        d[i + 1] = g.y;
-      }
+    for (int i = 0; i < kChunk / 2; ++i) {
+      Pair g = pair_fma(terms.n[c][i], {-mgn, -mgn}, pair_add(terms.g[c][i], {-mg, -mg}));
+      g = a.dh != nullptr ? pair_fma(g, {s, s}, chunk_pair(cd[c], i)) : pair_mul(g, {s, s});
+      d[2 * i] = g.x;
+      d[2 * i + 1] = g.y;
     }
     Chunk<BF16> co;
     if (a.dres != nullptr) {
@@ -235,6 +216,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
   uint8_t* stage = stages[STAGED ? threadIdx.x >> 5 : 0];
   const Dropper drop(a.mask);
   ParamSums<NCH> sums;
+  const float inv_cols = __frcp_rn((float)a.cols);
   int buf = 0;
   for (int64_t row0 = (int64_t)blockIdx.x * kTeams; row0 < a.rows;
        row0 += (int64_t)gridDim.x * kTeams, buf ^= 1) {
@@ -261,19 +243,19 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR)
         if (a.dh != nullptr) cd[c] = ld[c].settle(a.g_dh, stage, lane);
       }
     }
-    float2 r = backward_gather<BF16, TPR, NCH>(a, t, m, s, cy, ch, sums);
+    RowTerms<NCH> terms;
+    float2 r = backward_gather<BF16, TPR, NCH>(a, t, m, s, cy, ch, terms, sums);
     r = team_sum2<TPR, false>(r, red[buf]);
-    backward_emit<BF16, TPR, NCH, STAGED>(a, drop, base, live, t, stage, m, s,
-                                          __fdiv_rn(r.x, (float)a.cols),
-                                          __fdiv_rn(r.y, (float)a.cols), cy, ch, cd);
+    backward_emit<BF16, TPR, NCH, STAGED>(a, drop, base, live, t, stage, s,
+                                          __fmul_rn(r.x, inv_cols), __fmul_rn(r.y, inv_cols),
+                                          terms, cd);
   }
   backward_partials<TPR, NCH>(a, t, team, sums, s_sum);
 }
 
-constexpr int backward_ctas(int threads) {
-  const int n = 512 / (threads < 256 ? 256 : threads);
-  return n > 0 ? n : 1;
-}
+// CTAs per SM that the registers have to allow: two of up to 320 threads, one of more (bounded to
+// 24 warps a row's accumulators spill).
+constexpr int backward_ctas(int threads) { return threads <= 320 ? 2 : 1; }
 
 // Many rows through a shared-memory ring.  ANY: rows that are not 16-byte aligned (RowRing).
 template <bool BF16, int TPR, int NCH, bool ANY>
@@ -297,6 +279,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, backward_ctas(TPR))
   const Dropper drop(a.mask);
   ring.start(step);
   ParamSums<NCH> sums;
+  const float inv_cols = __frcp_rn((float)a.cols);
   int it = 0, st = 0;
   // a row's statistics are loaded a row ahead: nothing else of it comes from far
   float next_m = 0.0f, next_s = 0.0f;
@@ -330,7 +313,8 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, backward_ctas(TPR))
         if (a.dh != nullptr) cd[c].load_shared(p + 2 * g.tensor_bytes + col * kElem, n, lane);
       }
     }
-    float2 r = backward_gather<BF16, TPR, NCH>(a, t, m, s, cy, ch, sums);
+    RowTerms<NCH> terms;
+    float2 r = backward_gather<BF16, TPR, NCH>(a, t, m, s, cy, ch, terms, sums);
     r = team_sum2<TPR, true>(r, red[it & 1]);
     if (*(volatile int*)&err) {
       ring.give_up(it, row0, step, a.status);
@@ -338,9 +322,9 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, backward_ctas(TPR))
     }
     if (threadIdx.x == 0 && row0 + g.stages * step < a.rows)
       ring.fetch(st, row0 + g.stages * step);
-    backward_emit<BF16, TPR, NCH, ANY>(a, drop, row * a.cols, live, t, out_stage, m, s,
-                                       __fdiv_rn(r.x, (float)a.cols),
-                                       __fdiv_rn(r.y, (float)a.cols), cy, ch, cd);
+    backward_emit<BF16, TPR, NCH, ANY>(a, drop, row * a.cols, live, t, out_stage, s,
+                                       __fmul_rn(r.x, inv_cols), __fmul_rn(r.y, inv_cols), terms,
+                                       cd);
     if (++st == g.stages) st = 0;
   }
   backward_partials<TPR, NCH>(a, t, team, sums, s_sum);
@@ -424,6 +408,7 @@ cudaError_t pick(const LayerNormBackwardKernelArgs& k, int max_parts, const Devi
   if (c <= 1024) return run<BF16, 64, 1>(k, max_parts, dev, stream, parts);
   if (c <= 2048) return run<BF16, 128, 1>(k, max_parts, dev, stream, parts);
   if (c <= 4096) return run<BF16, 256, 1>(k, max_parts, dev, stream, parts);
+  if (c <= 5120) return run<BF16, 320, 1>(k, max_parts, dev, stream, parts);
   if (c <= 6144) return run<BF16, 384, 1>(k, max_parts, dev, stream, parts);
   if (c <= 8192) return run<BF16, 512, 1>(k, max_parts, dev, stream, parts);
   if (c <= 16384) return run<BF16, 1024, 1>(k, max_parts, dev, stream, parts);
@@ -433,8 +418,8 @@ cudaError_t pick(const LayerNormBackwardKernelArgs& k, int max_parts, const Devi
 }  // namespace
 
 int64_t add_layernorm_backward_workspace(int64_t rows, int64_t cols) {
-  // one row of partial sums per CTA; no more CTAs than kNormBackwardParts, nor than rows
-  return 8 * cols * std::min<int64_t>(rows, kNormBackwardParts);
+  // one row of partial sums per CTA; no more CTAs than kLayerNormBackwardParts, nor than rows
+  return 8 * cols * std::min<int64_t>(rows, kLayerNormBackwardParts);
 }
 
 cudaError_t launch_add_layernorm_backward(const NormBackwardArgs& a, const DeviceInfo& dev,
@@ -475,7 +460,7 @@ cudaError_t launch_add_layernorm_backward(const NormBackwardArgs& a, const Devic
                      reinterpret_cast<uintptr_t>(a.dh)) % 16 == 0;
   k.status = dev.status;
   int parts = 0;
-  const int max_parts = (int)std::min<int64_t>(a.rows, kNormBackwardParts);
+  const int max_parts = (int)std::min<int64_t>(a.rows, kLayerNormBackwardParts);
   cudaError_t err = a.in == InType::BF16 ? pick<true>(k, max_parts, dev, stream, &parts)
                                          : pick<false>(k, max_parts, dev, stream, &parts);
   if (err != cudaSuccess || k.part == nullptr) return err;
