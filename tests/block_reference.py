@@ -31,17 +31,15 @@ def threshold(p):
 
 def keep_mask(n, p, seed, offset, first=0):
     """Which of the elements first .. first + n - 1 are kept, as numpy booleans."""
-    e = np.arange(first, first + n, dtype=np.uint64)
-    block = e >> np.uint64(3)
+    block = np.arange(first // 8, (first + n + 7) // 8, dtype=np.uint64)  # eight elements each
     low = np.uint64(0xFFFFFFFF)
     offset &= (1 << 64) - 1
     words = philox4x32((block & low, block >> np.uint64(32),
                         np.full_like(block, offset & 0xFFFFFFFF), np.full_like(block, offset >> 32)),
                        (seed & 0xFFFFFFFF, (seed >> 32) & 0xFFFFFFFF))
-    half = (e & np.uint64(7)).astype(np.int64)
-    w = np.stack(words)[half // 2, np.arange(n)]
-    bits = np.where(half % 2 == 1, w >> np.uint64(16), w & np.uint64(0xFFFF))
-    return bits >= threshold(p)
+    halves = [h for w in words for h in (w & np.uint64(0xFFFF), w >> np.uint64(16))]
+    kept = np.stack([h >= np.uint64(threshold(p)) for h in halves], axis=1).reshape(-1)
+    return kept[first % 8:first % 8 + n]
 
 
 def drop(x, p, seed, offset):

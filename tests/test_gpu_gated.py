@@ -86,6 +86,26 @@ def test_gated_product(m, n, k, dtype):
     _check(m, n, k, dtype, "silu", None, False, False, m + n + k + 1, (PT, RS), (256.0, 448.0))
 
 
+# what goes to the pairs of SMs: long sums of more than 64 rows, at the borders of their tiles (256
+# rows, 128 columns, 256 values) and below them; and many tiles, whose rows need not be aligned
+@pytest.mark.parametrize("m,n,k", [(65, 8, 1056), (100, 136, 1120), (129, 128, 4096), (256, 128, 1280),
+                                   (257, 264, 2080), (300, 1000, 1312), (513, 72, 1056),
+                                   (2500, 2561, 96), (5200, 1001, 64), (2600, 2500, 288)])
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_pairs_of_sms(m, n, k, dtype):
+    name = list(ACTS)[(m + n + k // 32) % 4]
+    _check(m, n, k, dtype, name, torch.float32, seed=m + n)
+    _check(m, n, k, dtype, "silu", None, False, False, m + n + 1, (RS, PT), (448.0, 256.0))
+    if m < 600:
+        _check(m, n, k, dtype, "gelu", torch.bfloat16, False, True, m + 2, (PT, PT), scale_offset=2)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("offset", [1, 4, 8])
+def test_many_tiles_of_unaligned_rows(offset, dtype):
+    _check(2600, 2512, 96, dtype, "silu", torch.float32, seed=3, offset=offset, scale_offset=1)
+
+
 @pytest.mark.parametrize("name", list(ACTS))
 @pytest.mark.parametrize("bias", [None, torch.bfloat16, torch.float32])
 @pytest.mark.parametrize("keep,maxima", [(False, True), (True, False)])
@@ -112,7 +132,7 @@ def test_long_k(m, n):
     _check(m, n, 8192 + 96, torch.float32, "none", torch.float32, seed=5)
 
 
-@pytest.mark.parametrize("m,n", [(3, 384), (150, 384), (900, 5000)])
+@pytest.mark.parametrize("m,n", [(3, 384), (150, 384), (900, 5000), (2600, 2501)])
 def test_halves_are_the_product_with_either_weight(m, n):
     """gu is nvfp4_gemm with the stacked weights, within both sums' rounding, and repeatable."""
     (a, b), _, mag = _operands(m, n, 2048, 6)
