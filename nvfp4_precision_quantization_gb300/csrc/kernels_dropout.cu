@@ -2,7 +2,8 @@
 // addition: y = residual + (kept ? x / (1 - p) : 0).  The gradient is the same call on dy.
 //
 // Bound by memory: two reads and a write (one read without a residual); a thread makes the 16
-// elements of a chunk from two Philox blocks.
+// elements of a chunk from two Philox blocks.  Measured: 16384 x 8192 BF16 with a residual 118 us, 6.8
+// TB/s, the rate of a copy.
 #include <algorithm>
 
 #include "dropout.cuh"
@@ -52,8 +53,13 @@ cudaError_t launch_dropout(const DropoutArgs& a, const DeviceInfo& dev, cudaStre
                       row_grain(a.residual, 0), row_grain(a.y, 0)};
   int grain = std::min(k.g_x, k.g_y);
   if (a.residual) grain = std::min(grain, k.g_res);
-  const int64_t grid = std::min<int64_t>((a.n + 256 * kChunk - 1) / (256 * kChunk), 1 << 20);
   const bool bf16 = a.in == InType::BF16;
+  // BF16: eight CTAs an SM that walk (what is the call's own is made once, and issue slots are what
+  // this is short of beside memory: 134 M elements with a residual 118 us, 131 with a chunk a
+  // thread; without one 99 and 115).  FP32 moves twice the bytes for the same instructions and does
+  // better without the walk (67 M with a residual 114 us, 123 so).
+  const int64_t grid = std::min<int64_t>((a.n + 256 * kChunk - 1) / (256 * kChunk),
+                                         bf16 ? 8LL * dev.num_sms : 1 << 20);
   const auto kernel = bf16 ? (grain >= 16 ? k_dropout<true, false> : k_dropout<true, true>)
                            : (grain >= 16 ? k_dropout<false, false> : k_dropout<false, true>);
   kernel<<<(unsigned)grid, 256, 0, stream>>>(k);

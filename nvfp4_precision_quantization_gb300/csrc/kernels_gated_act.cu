@@ -7,6 +7,9 @@
 // Bound by memory (three reads, two writes per element of d).  As in kernels_act.cu a warp
 // walks down consecutive rows with 32 bytes of columns per lane, here those of dd and the
 // same columns of g and u; act and act' share their exponential and reciprocal.
+//
+// Measured: 16384 x 14336 BF16 SiLU, sums and maxima 360 us, 6.5 TB/s, 0.96 of a copy; 4000 x 5000
+// FP32 GELU 71 us, 5.6 TB/s (ramp and the joining launch).
 #include <algorithm>
 
 #include "activation.cuh"

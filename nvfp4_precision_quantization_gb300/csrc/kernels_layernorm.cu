@@ -9,6 +9,11 @@
 // computing sample variances", 1979), so one barrier is enough and a row far from zero loses
 // nothing.  The scale of a whole row needs max|y|, which b makes known only after s: a second
 // barrier, for those outputs alone.  The rest is norm_rows.cuh's.
+//
+// Measured (residual, bias): 4000 x 5000 FP32 53 us, 6.0 TB/s; 16384 x 8192 BF16 with E4M3 codes 182
+// us, 5.2 TB/s, and 232 us with dropout.  BF16 rows are bound by issue slots: 30 instructions an
+// element (the RMS norm's 24 take 147 us) and 11 more for the mask, at the 60 % of the slots that
+// 24 warps an SM with two barriers a row fill.  One row of 8192 4 us.
 #include "norm_rows.cuh"
 
 namespace nvfp4 {
