@@ -11,8 +11,8 @@
 // barrier, for those outputs alone.  The rest is norm_rows.cuh's.
 //
 // Measured (residual, bias): 4000 x 5000 FP32 53 us, 6.0 TB/s; 16384 x 8192 BF16 with E4M3 codes 182
-// us, 5.2 TB/s, and 232 us with dropout.  BF16 rows are bound by issue slots: 30 instructions an
-// element (the RMS norm's 24 take 147 us) and 11 more for the mask, at the 60 % of the slots that
+// us, 5.2 TB/s, and 232 us with dropout.  BF16 rows are bound by issue slots: 29 instructions an
+// element (the RMS norm's 23 take 147 us) and 12 more for the mask, at the 60 % of the slots that
 // 24 warps an SM with two barriers a row fill.  One row of 8192 4 us.
 #include "norm_rows.cuh"
 
