@@ -28,7 +28,7 @@
 // The scales go through registers because a tcgen05.cp takes about 50 cycles of the MMAs' own
 // in-order pipe whatever it moves, and a K tile would need twelve (six of the largest form): 8192 x
 // 14336 x 8192 takes 1122 us so, 646 this way, 649 with the copies left out.  Measured, SILU: 16384
-// x 14336 x 8192 1458 us with [g | u] and the maxima kept, 5.3 PFLOP/s; 8192 rows without them
+// x 14336 x 8192 1449 us with [g | u] and the maxima kept, 5.3 PFLOP/s; 8192 rows without them
 // 646 us, 6.0 PFLOP/s, of which 60 us are the epilogue's.  What is left is the pair's walk through the
 // ring: a K tile takes 0.42 us, 0.37 with one MMA instead of four, 0.36 without the scales' stores; half
 // of B's bytes, four stages instead of five or a second producer change nothing.

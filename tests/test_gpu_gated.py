@@ -235,6 +235,30 @@ def test_workspace_stream_and_graph(m, n):
     ok()
 
 
+def test_two_calls_at_once():
+    """Calls on two streams with a workspace each, many rows and few, again and again."""
+    cases = [(1500, 3000, 1056), (7, 9000, 2048)]
+    ops = [_operands(m, n, k, 11)[0] for m, n, k in cases]
+    want = [torch.empty(m, n, device=DEV) for m, n, _ in cases]
+    for (a, b), d in zip(ops, want):
+        nv.nvfp4_gemm_gated(a, b, d)
+    got = [torch.empty_like(d) for d in want for _ in range(2)]
+    maxima = [torch.empty(d.shape[0], device=DEV) for d in got]
+    ws = [torch.empty(nv.nvfp4_gemm_gated_workspace_size(*cases[i // 2]), dtype=torch.uint8, device=DEV)
+          for i in range(4)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for i in range(4):
+            a, b = ops[i // 2]
+            nv.nvfp4_gemm_gated(a, b, got[i], row_amax=maxima[i], workspace=ws[i], stream=streams[i % 2])
+    torch.cuda.synchronize()
+    for i in range(4):
+        assert torch.equal(got[i], want[i // 2])
+        assert torch.equal(maxima[i], got[i].abs().amax(dim=1))
+    assert nv.nvfp4_device_status() == 0
+
+
 # ---------------------------------------------------------------- backward
 
 BACK = [(1, 1), (1, 4096), (3, 16), (5, 17), (40, 64), (1000, 8), (129, 100), (300, 512),
