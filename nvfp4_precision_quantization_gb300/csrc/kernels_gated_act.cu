@@ -35,9 +35,16 @@ struct GatedKernelArgs {
   int g_dd, g_gu, g_dgu;
 };
 
+// Staged BF16 takes half a sector a lane: units of two bytes take a register each, and 32 bytes of
+// three tensors beside the sums spill (16000 x 3001 606 us, 146 so).
+constexpr __host__ __device__ int sector_words(bool bf16, bool staged) {
+  return bf16 && staged ? 4 : 8;
+}
+
 template <bool BF16, int ACT, bool STAGED>
 __global__ void __launch_bounds__(kGatedThreads, 2) k_gated_backward(const GatedKernelArgs a) {
-  using S = Sector<BF16>;
+  constexpr int W = sector_words(BF16, STAGED);
+  using S = Sector<BF16, W>;
   constexpr int kCols = S::kCols, kStrip = 32 * kCols;
   __shared__ float s_sum[2][kStrip], s_max[2][kStrip];
   __shared__ __align__(16) uint8_t stages[STAGED ? kGatedWarps : 1][kStageBytes];
@@ -57,16 +64,16 @@ __global__ void __launch_bounds__(kGatedThreads, 2) k_gated_backward(const Gated
   const int64_t warps = (int64_t)a.row_parts * kGatedWarps, w = (int64_t)part * kGatedWarps + warp;
   const int64_t r0 = a.rows * w / warps, r1 = a.rows * (w + 1) / warps;
   Pair sum[2][kCols / 2];
-  uint32_t mx[2][8];  // word by word, as dgu is stored
+  uint32_t mx[2][W];  // word by word, as dgu is stored
 #pragma unroll
   for (int k = 0; k < 2; ++k) {
 #pragma unroll
     for (int i = 0; i < kCols / 2; ++i) sum[k][i] = {0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < 8; ++i) mx[k][i] = 0;
+    for (int i = 0; i < W; ++i) mx[k][i] = 0;
   }
   // the next row's words are loaded before this row's are used
-  SectorLoad<BF16, STAGED> nd, ng, nu;
+  SectorLoad<BF16, STAGED, W> nd, ng, nu;
   auto fetch = [&](int64_t r) {
     const int n = r < r1 ? n_col : 0;
     const int64_t have = r < r1 ? run : 0;
@@ -99,14 +106,14 @@ __global__ void __launch_bounds__(kGatedThreads, 2) k_gated_backward(const Gated
     g.template store_warp<STAGED>(a.dgu, 2 * r * a.cols + col, n, have, a.g_dgu, stage, lane);
     u.template store_warp<STAGED>(a.dgu, (2 * r + 1) * a.cols + col, n, have, a.g_dgu, stage, lane);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < W; ++i) {
       mx[0][i] = word_absmax<BF16>(mx[0][i], g.w[i]);
       mx[1][i] = word_absmax<BF16>(mx[1][i], u.w[i]);
     }
     if (a.row_max != nullptr) {
       uint32_t m = 0;
 #pragma unroll
-      for (int i = 0; i < 8; ++i) m = word_absmax<BF16>(word_absmax<BF16>(m, g.w[i]), u.w[i]);
+      for (int i = 0; i < W; ++i) m = word_absmax<BF16>(word_absmax<BF16>(m, g.w[i]), u.w[i]);
       // as bits: non-negative values are ordered like them
       uint32_t bits = __float_as_uint(word_value<BF16>(m));
       if (a.lanes == 32) {
@@ -167,6 +174,11 @@ int64_t max_row_parts(int64_t cols, bool bf16) {
   return std::max<int64_t>(1, kGatedMaxCtas / strips_of(cols, bf16));
 }
 
+// Whether some tensor's rows do not allow 16-byte accesses.
+bool staged(const GatedKernelArgs& k) {
+  return std::min(k.g_dd, std::min(k.g_gu, k.g_dgu)) < 16;
+}
+
 template <bool BF16, int ACT, bool STAGED>
 cudaError_t run_as(GatedKernelArgs& k, const DeviceInfo& dev, cudaStream_t stream) {
   static const int resident = [] {
@@ -190,9 +202,8 @@ cudaError_t run_as(GatedKernelArgs& k, const DeviceInfo& dev, cudaStream_t strea
 
 template <bool BF16, int ACT>
 cudaError_t run(GatedKernelArgs& k, const DeviceInfo& dev, cudaStream_t stream) {
-  return std::min(k.g_dd, std::min(k.g_gu, k.g_dgu)) >= 16
-             ? run_as<BF16, ACT, false>(k, dev, stream)
-             : run_as<BF16, ACT, true>(k, dev, stream);
+  return staged(k) ? run_as<BF16, ACT, true>(k, dev, stream)
+                   : run_as<BF16, ACT, false>(k, dev, stream);
 }
 
 template <bool BF16>
@@ -237,12 +248,13 @@ cudaError_t launch_gated_backward(const GatedBackwardArgs& a, const DeviceInfo& 
   k.row_max = a.row_amax ? reinterpret_cast<float*>(ws + 2 * col_bytes) : nullptr;
   k.rows = a.rows;
   k.cols = a.cols;
-  k.strips = (int)strips_of(a.cols, bf16);
-  k.lanes = 32;
-  while (k.lanes > 1 && (int64_t)(k.lanes / 2) * (bf16 ? 16 : 8) >= a.cols) k.lanes /= 2;
   k.g_dd = row_grain(a.dd, a.cols * e);
   k.g_gu = row_grain(a.gu, a.cols * e);  // u starts `cols` into the row
   k.g_dgu = row_grain(a.dgu, a.cols * e);
+  const int words = sector_words(bf16, staged(k)), lane_cols = bf16 ? 2 * words : words;
+  k.strips = (int)strips_of(a.cols, bf16, words == 4);
+  k.lanes = 32;
+  while (k.lanes > 1 && (int64_t)(k.lanes / 2) * lane_cols >= a.cols) k.lanes /= 2;
   cudaError_t err = bf16 ? pick<true>(a.act, k, dev, stream) : pick<false>(a.act, k, dev, stream);
   if (err != cudaSuccess || !(a.dbias || a.col_amax || a.row_amax)) return err;
   ActReduceArgs r{};

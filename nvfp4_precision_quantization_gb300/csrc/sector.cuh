@@ -8,21 +8,21 @@
 namespace nvfp4 {
 namespace {
 
-// 32 bytes of a row, one lane's columns: 16 BF16 or 8 FP32.
-template <bool BF16>
+// 32 bytes of a row (W words, 8 or 4), one lane's columns: 16 BF16 or 8 FP32.
+template <bool BF16, int W = 8>
 struct Sector {
-  static constexpr int kCols = BF16 ? 16 : 8;
-  uint32_t w[8];
+  static constexpr int kCols = BF16 ? 2 * W : W;
+  uint32_t w[W];
   __device__ __forceinline__ void load(const void* base, int64_t off, int n, int grain) {
     const char* p = static_cast<const char*>(base) + off * (BF16 ? 2 : 4);
-    if (n == kCols && grain == 32) {
+    if (W == 8 && n == kCols && grain == 32) {
       ldg_v8(p, w);
-    } else if (n == kCols && grain == 16) {
-      ldg_v4(p, w);
-      ldg_v4(p + 16, w + 4);
+    } else if (n == kCols && grain >= 16) {
+#pragma unroll
+      for (int i = 0; i < W; i += 4) ldg_v4(p + 4 * i, w + i);
     } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) w[i] = 0;
+      for (int i = 0; i < W; ++i) w[i] = 0;
 #pragma unroll
       for (int i = 0; i < kCols; ++i)
         if (i < n) {
@@ -35,11 +35,12 @@ struct Sector {
   }
   __device__ __forceinline__ void store(void* base, int64_t off, int n, int grain) const {
     char* p = static_cast<char*>(base) + off * (BF16 ? 2 : 4);
-    if (n == kCols && grain == 32) {
+    if (W == 8 && n == kCols && grain == 32) {
       stg_v8(p, w);
-    } else if (n == kCols && grain == 16) {
-      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-      *reinterpret_cast<uint4*>(p + 16) = make_uint4(w[4], w[5], w[6], w[7]);
+    } else if (n == kCols && grain >= 16) {
+#pragma unroll
+      for (int i = 0; i < W; i += 4)
+        *reinterpret_cast<uint4*>(p + 4 * i) = make_uint4(w[i], w[i + 1], w[i + 2], w[i + 3]);
     } else {
 #pragma unroll
       for (int i = 0; i < kCols; ++i)
@@ -61,7 +62,7 @@ struct Sector {
       store(base, off, n, grain);
       return;
     }
-    staged_store<8, 32, kElem, 8>(static_cast<char*>(base) + (off - (int64_t)kCols * lane) * kElem,
+    staged_store<W, 4 * W, kElem, 8>(static_cast<char*>(base) + (off - (int64_t)kCols * lane) * kElem,
                         (int)run * kElem, grain, smem, lane, w);
   }
   // columns 2k and 2k + 1
@@ -80,19 +81,18 @@ struct Sector {
 };
 
 // The load of such a warp: issue() for every tensor, settle() when the values are needed.
-template <bool BF16, bool STAGED>
+template <bool BF16, bool STAGED, int W = 8>
 struct SectorLoad {
-  Sector<BF16> s;
-  StagedLoad<8, 32, BF16 ? 2 : 4> raw;
+  Sector<BF16, W> s;
+  StagedLoad<W, 4 * W, BF16 ? 2 : 4> raw;
   __device__ __forceinline__ void issue(const void* base, int64_t off, int n, int64_t run,
                                         int grain, const uint8_t* smem, int lane) {
     constexpr int kElem = BF16 ? 2 : 4;
     if (!STAGED || grain >= 16 || smem == nullptr) s.load(base, off, n, grain);
     else
-      raw.issue(static_cast<const char*>(base) + (off - (int64_t)Sector<BF16>::kCols * lane) * kElem,
-                (int)run * kElem, grain, lane);
+      raw.issue(static_cast<const char*>(base) + (off - (int64_t)s.kCols * lane) * kElem, (int)run * kElem, grain, lane);
   }
-  __device__ __forceinline__ const Sector<BF16>& settle(int grain, uint8_t* smem, int lane) {
+  __device__ __forceinline__ const Sector<BF16, W>& settle(int grain, uint8_t* smem, int lane) {
     if constexpr (STAGED) {
       if (grain < 16 && smem != nullptr) raw.settle(grain, smem, lane, s.w);
     }
@@ -163,9 +163,9 @@ __global__ void __launch_bounds__(256) k_act_join(const ActReduceArgs a) {
   }
 }
 
-// strips of 32 lanes: 512 BF16 or 256 FP32 columns
-int64_t strips_of(int64_t cols, bool bf16) {
-  const int strip = bf16 ? 32 * Sector<true>::kCols : 32 * Sector<false>::kCols;
+// strips of 32 lanes: 512 BF16 or 256 FP32 columns (half of them with half sectors)
+int64_t strips_of(int64_t cols, bool bf16, bool half = false) {
+  const int strip = (bf16 ? 32 * Sector<true>::kCols : 32 * Sector<false>::kCols) / (half ? 2 : 1);
   return (cols + strip - 1) / strip;
 }
 int64_t round16(int64_t v) { return (v + 15) / 16 * 16; }
