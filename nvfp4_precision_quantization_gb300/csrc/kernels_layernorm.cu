@@ -39,10 +39,11 @@ __device__ __forceinline__ float team_max(float m, float* red) {
 struct LayerNorm {
   static constexpr bool kMasked = true;
   // 24 warps an SM: with the 16 that the compiler's registers leave, a row's barriers lie open
-  // (4000 x 5000 FP32 74 us, 53 so)
+  // (4000 x 5000 FP32 74 us, 53 so); 16 for two FP32 chunks a thread, which spill (16000 x 8192 FP32
+  // 460 us with 24, 416 with 16)
   template <bool BF16, int TPR, int NCH>
   static constexpr int ring_ctas() {
-    constexpr int n = 768 / (TPR < 256 ? 256 : TPR);
+    constexpr int n = (!BF16 && NCH == 2 ? 512 : 768) / (TPR < 256 ? 256 : TPR);
     return n > 0 ? n : 1;
   }
   template <int TPR, int NCH>

@@ -380,6 +380,10 @@ cudaError_t pick_norm(const NormKernelArgs& k, const DeviceInfo& dev, cudaStream
   if (c <= 6144) return run_norm<OP, BF16, NV4, 384, 1, kAnyRows>(k, dev, stream);
   if (c <= 8192 && !few) return run_norm<OP, BF16, NV4, 256, 2, kManyAligned>(k, dev, stream);
   if (c <= 8192) return run_norm<OP, BF16, NV4, 512, 1, kFewAlignedOrUnaligned>(k, dev, stream);
+  // fuller teams for an OP of more instructions (8000 x 12000 BF16 with a mask 246 us, 181 so)
+  if constexpr (OP::kMasked) {
+    if (c <= 12288 && !few) return run_norm<OP, BF16, NV4, 384, 2, kManyAligned>(k, dev, stream);
+  }
   if (c <= 16384 && !few) return run_norm<OP, BF16, NV4, 512, 2, kManyAligned>(k, dev, stream);
   if (c <= 16384) return run_norm<OP, BF16, NV4, 1024, 1, kFewAlignedOrUnaligned>(k, dev, stream);
   return run_norm<OP, BF16, NV4, 1024, 2, kAnyRows>(k, dev, stream);
