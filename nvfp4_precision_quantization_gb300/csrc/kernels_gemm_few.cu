@@ -724,7 +724,8 @@ __global__ void __launch_bounds__(256) k_clear_words(const ClearArgs a) {
   pdl_launch_dependents();
 #pragma unroll
   for (int k = 0; k < 3; ++k)
-    for (int i = blockIdx.x * 256 + threadIdx.x; i < a.n[k]; i += gridDim.x * 256)
+    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < a.n[k];
+         i += (int64_t)gridDim.x * 256)  // (a count near 2^31 leaves no room for an int's last step)
       static_cast<uint32_t*>(a.p[k])[i] = 0;
 }
 cudaError_t launch_clear(const ClearArgs& a, cudaStream_t stream) {

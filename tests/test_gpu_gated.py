@@ -204,6 +204,22 @@ def test_empty_sum_and_empty_outputs():
     assert float(ra.abs().max()) == 0.0
 
 
+def test_empty_sum_of_the_most_rows():
+    """A row count whose last step past the end leaves 32 bits: the rows' maxima are cleared and
+    raised, and nothing in front of them or behind them is touched."""
+    m, pad = (1 << 31) - 8192, 1 << 16
+    bias = torch.tensor([1.5, -2.0], device=DEV)
+    none = torch.empty(m, 0, dtype=torch.uint8, device=DEV)
+    a = nv.Operand(none, none, torch.ones(1, device=DEV), PT, 448.0)
+    b = nv.Operand(none[:2], none[:2], torch.ones(1, device=DEV), PT, 448.0)
+    buf = torch.full((m + 2 * pad,), 9.0, device=DEV)
+    d = torch.empty(m, 1, dtype=torch.bfloat16, device=DEV)
+    nv.nvfp4_gemm_gated(a, b, d, bias=bias, act=nv.NVFP4_ACT_RELU, row_amax=buf[pad:pad + m])
+    torch.cuda.synchronize()
+    assert bool((buf[:pad] == 9.0).all()) and bool((buf[pad + m:] == 9.0).all())
+    assert bool((buf[pad:pad + m] == 3.0).all()) and bool((d == -3.0).all())
+
+
 @pytest.mark.parametrize("m,n", [(2, 512), (140, 512), (1500, 3000)])
 def test_workspace_stream_and_graph(m, n):
     """A given workspace of the stated size, on another stream, and captured."""
