@@ -46,6 +46,10 @@ struct LayerNorm {
     constexpr int n = (!BF16 && NCH == 2 ? 512 : 768) / (TPR < 256 ? 256 : TPR);
     return n > 0 ? n : 1;
   }
+  template <int NCH>
+  static constexpr int third_cta() {
+    return 2;
+  }
   template <int TPR, int NCH>
   struct Team;
 };

@@ -4,6 +4,7 @@
 // kernels_layernorm.cu):
 //   OP::kMasked   whether x goes through a dropout mask first
 //   OP::ring_ctas CTAs per SM that the registers of the kernel for many aligned rows allow
+//   OP::third_cta the stages of the ring that a third CTA of an SM must leave each of them
 //   OP::Team      what a thread of a row's team keeps from row to row; its row<...> makes the
 //                 statistics and outputs of a row whose h (x + residual) is in registers, calls
 //                 release() after its first barrier (by then every thread has the row), and
@@ -265,18 +266,24 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR,
       }
 #pragma unroll
       for (int i = 0; i < kChunk; ++i) v[c][i] = cx.get(i);
-      Chunk<BF16> cr;
-      if (a.res != nullptr) {
+      auto residual = [&] {
+        Chunk<BF16> cr;
         if constexpr (ANY) {
           cr.load_shared_any(st + g.tensor_bytes + min(col, a.cols) * kElem, lane);
           cr.cut(n);
         } else {
           cr.load_shared(st + g.tensor_bytes + col * kElem, n, lane);
         }
-      }
+        return cr;
+      };
       if constexpr (OP::kMasked) {
+        Chunk<BF16> cr;
+        if (a.res != nullptr) cr = residual();
         drop.apply(base + col, v[c], a.res != nullptr ? &cr : nullptr);
       } else if (a.res != nullptr) {
+        // (loaded under this condition alone: as above it costs 10 to 18 registers more, and rows of
+        // more than 16384 columns, 64 a thread, spill: 4000 x 28672 BF16 149 us, 168 so)
+        const Chunk<BF16> cr = residual();
 #pragma unroll
         for (int i = 0; i < kChunk; ++i) v[c][i] = __fadd_rn(v[c][i], cr.get(i));
       }
@@ -318,7 +325,8 @@ cudaError_t run_norm_ring(const NormKernelArgs& k, int64_t groups, const DeviceI
   auto ring = k_norm_ring<OP, BF16, NV4, TPR, NCH, ANY>;
   static const RingKernel limits = ring_kernel(ring, kThreads);
   const RingPlan p = plan_ring(limits, k.res ? 2 : 1,
-                               (int64_t)(kThreads / TPR) * k.cols * (BF16 ? 2 : 4), ANY);
+                               (int64_t)(kThreads / TPR) * k.cols * (BF16 ? 2 : 4), ANY,
+                               OP::template third_cta<NCH>());
   const int64_t fill = (int64_t)p.ctas * dev.num_sms;
   if (p.ctas == 0 || groups <= 2 * fill) return cudaSuccess;
   *done = true;

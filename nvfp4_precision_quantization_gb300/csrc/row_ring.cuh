@@ -182,7 +182,9 @@ struct RingPlan {
   int ctas;
   RingArgs g;
 };
-RingPlan plan_ring(const RingKernel& k, int tensors, int64_t group_bytes, bool any = false) {
+// third: the stages that each CTA has to keep for a third one to run beside two.
+RingPlan plan_ring(const RingKernel& k, int tensors, int64_t group_bytes, bool any = false,
+                   int third = 2) {
   RingPlan p{};
   if (group_bytes <= 0) return p;
   // any: up to 30 bytes of the units around the rows, and a lane's reads past a row's end
@@ -191,7 +193,7 @@ RingPlan plan_ring(const RingKernel& k, int tensors, int64_t group_bytes, bool a
     // an SM's 228 KB, of which every CTA takes 1 KB beside its own
     const int64_t room =
         std::min<int64_t>(kCtaSmem, (228 << 10) / c - (1 << 10)) - k.static_bytes;
-    if (room < 2 * stage) continue;
+    if (room < (c > 2 ? third : 2) * stage) continue;
     p.ctas = c;
     p.g.stages = (int)std::min<int64_t>(kRingStages, room / stage);
     p.g.tensor_bytes = (int)tensor;
