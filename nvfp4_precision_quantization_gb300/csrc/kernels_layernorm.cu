@@ -3,11 +3,17 @@
 //   h = residual + drop(x),  m = mean(h),  s = 1 / sqrt(mean((h - m)^2) + eps),
 //   y = (h - m) s w + b
 //
-// The variance is that of the differences, not a difference of moments: each warp takes its
-// own mean from registers, sums the squares around it, and the warps' (sum, squares) join
-// around the row's mean (Chan, Golub, LeVeque, "Updating formulae and a pairwise algorithm for
-// computing sample variances", 1979), so one barrier is enough and a row far from zero loses
-// nothing.  The scale of a whole row needs max|y|, which b makes known only after s: a second
+// The variance is that of the differences, not a difference of moments.  Each warp takes its own mean m_w
+// from registers, then the sums e_w of its n_w differences to it and Q_w of their squares.  With m
+// the mean of the team's first warp and off = m_w - m, the row's are
+//   sum (h - m) = e_w + n_w off,   sum (h - m)^2 = Q_w + 2 off e_w + n_w off^2
+// (Chan, Golub, LeVeque, "Updating formulae and a pairwise algorithm for computing sample
+// variances", 1979, where e_w is 0; m_w is rounded here, and without e_w rows of 65536 +- 1 lost 2e-4
+// of their variance), and the first moves m to the row's mean and takes its part off the second.  m is
+// the mean of a share f of the row, so within sqrt(1 / f - 1) of its standard deviations: what is
+// taken off is at most 1 / f - 1 times what is left, f being 1/32 or more, and next to nothing in a
+// row whose columns are alike.  One barrier is enough, and a row far from zero loses nothing but its
+// own rounding.  The scale of a whole row needs max|y|, which b makes known only after s: a second
 // barrier, for those outputs alone.  The rest is norm_rows.cuh's.
 //
 // Measured (residual, bias): 4000 x 5000 FP32 53 us, 6.0 TB/s; 16384 x 8192 BF16 with E4M3 codes 182
@@ -38,6 +44,7 @@ __device__ __forceinline__ float team_max(float m, float* red) {
 
 struct LayerNorm {
   static constexpr bool kMasked = true;
+  using Sums = float4;  // its mean, the sums of squared differences to it and of differences
   // 24 warps an SM: with the 16 that the compiler's registers leave, a row's barriers lie open
   // (4000 x 5000 FP32 74 us, 53 so); 16 for two FP32 chunks a thread, which spill (16000 x 8192 FP32
   // 460 us with 24, 416 with 16)
@@ -59,7 +66,7 @@ struct LayerNorm::Team {
   static constexpr int kWarps = TPR / 32;
   static constexpr int kTree = kWarps <= 1 ? 1 : kWarps <= 2 ? 2 : kWarps <= 4 ? 4 : kWarps <= 8 ? 8 : kWarps <= 16 ? 16 : 32;
   float inv_warp;   // 1 / the columns of this thread's warp (0 where it has none)
-  float n, inv_n;   // those of the team's warp `lane`, whose sums this lane joins
+  float n;          // the columns of the team's warp `lane`, whose sums this lane joins
   float inv_cols;
 
   // columns of the team's warp w
@@ -77,14 +84,36 @@ struct LayerNorm::Team {
     const int w = (threadIdx.x & 31) % kTree, theirs = w < kWarps ? count(a.cols, w) : 0;
     inv_warp = inverse(count(a.cols, t / 32));
     n = (float)theirs;
-    inv_n = inverse(theirs);
     inv_cols = inverse(a.cols);
+  }
+
+  // A sum over the lanes of two values at once, N lanes each: lane l gets that of a where l & (N / 2)
+  // is 0, and that of b elsewhere.
+  template <int N>
+  __device__ __forceinline__ static float sum_of_two(float a, float b, int lane) {
+    const bool upper = lane & (N / 2);
+    const float keep = upper ? b : a, give = upper ? a : b;
+    float s = __fadd_rn(keep, __shfl_xor_sync(0xffffffffu, give, N / 2));
+#pragma unroll
+    for (int d = N / 4; d > 0; d >>= 1) s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, d));
+    return s;
+  }
+  __device__ __forceinline__ static bool finite(float x) {
+    return fabsf(x) < __int_as_float(0x7f800000);
+  }
+  // Mean and sum of squared differences to it, from those to a finite m: rest = sum (v - m), sq =
+  // sum (v - m)^2 (which is not below rest^2 / cols but for its rounding; a NaN stays).
+  __device__ __forceinline__ float2 around_mean(float m, float rest, float sq) const {
+    const float d = __fmul_rn(rest, inv_cols);
+    float s = __fmaf_rn(-rest, d, sq);
+    asm("max.NaN.f32 %0, %0, 0f00000000;" : "+f"(s));
+    return make_float2(__fadd_rn(m, d), s);
   }
 
   // Mean and sum of squared differences of a row whose part is in v (zeros past its end).
   template <bool BARRIER>
   __device__ __forceinline__ float2 moments(const float (&v)[NCH][kChunk], int cols, int t,
-                                            float2* red) const {
+                                            Sums* red) const {
     const int lane = threadIdx.x & 31;
     Pair two = {0.0f, 0.0f};
 #pragma unroll
@@ -95,6 +124,7 @@ struct LayerNorm::Team {
 #pragma unroll
     for (int d = 16; d > 0; d >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(0xffffffffu, sum, d));
     const float mean = __fmul_rn(sum, inv_warp);
+    Pair rest = {0.0f, 0.0f};
     two = {0.0f, 0.0f};
 #pragma unroll
     for (int c = 0; c < NCH; ++c) {
@@ -103,40 +133,46 @@ struct LayerNorm::Team {
 #pragma unroll
         for (int i = 0; i < kChunk; i += 2) {
           const Pair d = pair_add({v[c][i], v[c][i + 1]}, {-mean, -mean});
+          rest = pair_add(rest, d);
           two = pair_fma(d, d, two);
         }
       } else if (left > 0) {
 #pragma unroll
         for (int i = 0; i < kChunk; ++i) {
           const float d = i < left ? __fsub_rn(v[c][i], mean) : 0.0f;
+          rest.x = __fadd_rn(rest.x, d);
           two.x = __fmaf_rn(d, d, two.x);
         }
       }
     }
-    float sq = __fadd_rn(two.x, two.y);
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) sq = __fadd_rn(sq, __shfl_xor_sync(0xffffffffu, sq, d));
+    // squares in the lower lanes, differences in the upper ones
+    const float both =
+        sum_of_two<32>(__fadd_rn(two.x, two.y), __fadd_rn(rest.x, rest.y), lane);
     if constexpr (TPR == 32) {
       if constexpr (BARRIER) __syncthreads();
-      return make_float2(mean, sq);
+      const float other = __shfl_xor_sync(0xffffffffu, both, 16);
+      const float sq = lane < 16 ? both : other, rest = lane < 16 ? other : both;
+      return finite(mean) ? around_mean(mean, rest, sq) : around_mean(0.0f, mean, sq);
     } else {
-      const int warp = threadIdx.x >> 5;
-      if (lane == 0) red[warp] = make_float2(sum, sq);
+      const int warp = threadIdx.x >> 5, first = warp - warp % kWarps;
+      if (lane == 0) red[warp].x = mean;
+      if (lane % 16 == 0) (lane == 0 ? red[warp].y : red[warp].z) = both;
       __syncthreads();
+      // this lane's warp's differences, to the mean of the team's first warp
       const int i = lane % kTree;
-      const float2 p = i < kWarps ? red[warp - warp % kWarps + i] : make_float2(0.0f, 0.0f);
-      float all = p.x;
-#pragma unroll
-      for (int d = kTree / 2; d > 0; d >>= 1)
-        all = __fadd_rn(all, __shfl_xor_sync(0xffffffffu, all, d));
-      const float m = __fmul_rn(all, inv_cols);
-      // (n is 0, and the difference of no account, where the warp has no columns)
-      const float off = __fsub_rn(__fmul_rn(p.x, inv_n), m);
-      float s = n > 0.0f ? __fmaf_rn(__fmul_rn(off, off), n, p.y) : 0.0f;
-#pragma unroll
-      for (int d = kTree / 2; d > 0; d >>= 1)
-        s = __fadd_rn(s, __shfl_xor_sync(0xffffffffu, s, d));
-      return make_float2(m, s);
+      const float4 p = red[first + (i < kWarps ? i : 0)];
+      float m = red[first].x;
+      if (!finite(m)) m = 0.0f;
+      const float off = __fsub_rn(p.x, m);
+      // (the differences to a mean that is no number are none: it stands for them.  n is 0, and the
+      // differences of no account, where the warp has no columns)
+      const float sq = n > 0.0f ? __fmaf_rn(__fmul_rn(off, off), n,
+                                            __fmaf_rn(__fadd_rn(off, off), p.z, p.y)) : 0.0f;
+      float rest = n > 0.0f ? __fmaf_rn(off, n, p.z) : 0.0f;
+      if (!finite(p.x)) rest = p.x;
+      const float joined = sum_of_two<kTree>(sq, rest, lane);
+      const float other = __shfl_xor_sync(0xffffffffu, joined, kTree / 2);
+      return (lane & (kTree / 2)) ? around_mean(m, joined, other) : around_mean(m, other, joined);
     }
   }
 
@@ -162,7 +198,7 @@ struct LayerNorm::Team {
 
   template <bool BF16, bool NV4, bool STAGED, bool RING, class Release>
   __device__ __forceinline__ void row(const NormKernelArgs& a, int64_t row, bool live, bool has,
-                                      int t, uint8_t* stage, float (&v)[NCH][kChunk], float2* red,
+                                      int t, uint8_t* stage, float (&v)[NCH][kChunk], Sums* red,
                                       const Release& release) const {
     // beside red, which the next row's statistics may take while this row's maxima are read
     __shared__ float maxima[TPR < 256 ? 8 : TPR / 32];

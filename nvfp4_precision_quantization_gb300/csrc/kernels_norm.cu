@@ -23,6 +23,7 @@ __device__ __forceinline__ float amax_times(float m, float s) {
 
 struct RmsNorm {
   static constexpr bool kMasked = false;
+  using Sums = float2;
   template <bool BF16, int TPR, int NCH>
   static constexpr int ring_ctas() {
     return 1;

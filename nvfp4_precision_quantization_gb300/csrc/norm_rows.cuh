@@ -3,6 +3,7 @@
 // y, E4M3 with scales or NVFP4 rows.  What is computed of a row is OP's (kernels_norm.cu,
 // kernels_layernorm.cu):
 //   OP::kMasked   whether x goes through a dropout mask first
+//   OP::Sums      what a warp of a team gives the others
 //   OP::ring_ctas CTAs per SM that the registers of the kernel for many aligned rows allow
 //   OP::third_cta the stages of the ring that a third CTA of an SM must leave each of them
 //   OP::Team      what a thread of a row's team keeps from row to row; its row<...> makes the
@@ -175,7 +176,7 @@ template <class OP, bool BF16, bool NV4, int TPR, int NCH, bool STAGED>
 __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR, TPR == 1024 ? 1 : 0) k_norm(const NormKernelArgs a) {
   constexpr int kThreads = TPR < 256 ? 256 : TPR;
   constexpr int kTeams = kThreads / TPR;
-  __shared__ float2 red[2][kThreads / 32];
+  __shared__ typename OP::Sums red[2][kThreads / 32];
   __shared__ __align__(16) uint8_t stages[STAGED ? kThreads / 32 : 1][kStageBytes];
   const int t = threadIdx.x % TPR, team = threadIdx.x / TPR, lane = threadIdx.x & 31;
   uint8_t* stage = stages[STAGED ? threadIdx.x >> 5 : 0];
@@ -234,7 +235,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR,
   constexpr int kTeams = kThreads / TPR;
   constexpr int kElem = BF16 ? 2 : 4;
   extern __shared__ __align__(128) uint8_t ring_smem[];
-  __shared__ float2 red[2][kThreads / 32];
+  __shared__ typename OP::Sums red[2][kThreads / 32];
   __shared__ __align__(8) uint64_t full[kRingStages];
   __shared__ int err;
   __shared__ __align__(16) uint8_t stages[ANY ? kThreads / 32 : 1][kStageBytes];

@@ -183,6 +183,42 @@ def test_rows_far_from_zero_keep_their_variance():
         _inside(rstd, es, (2.0 ** -11 + 2.0 ** -18) * es, "rstd")
 
 
+@pytest.mark.parametrize("far", [2.0 ** 12, 2.0 ** 14, 2.0 ** 16, -2.0 ** 16])
+@pytest.mark.parametrize("cols", [64, 511, 1000, 1024, 2056, 5000, 8192, 12000, 20000, 32768])
+@pytest.mark.parametrize("rows", [6, 4100])
+def test_variance_does_not_depend_on_the_mean(rows, cols, far):
+    """Values far + {-1, 0, 1}: every difference to a mean near them is exact in FP32.
+
+    A chain adds at most 16 pairs in a thread, its two halves, 5 steps in a warp, 2 and 5 in the join: g =
+    29 2^-24.  A warp's mean is within shift = g |far| of its own, so its squares are within g (sigma + off
+    + shift)^2 and its differences within g (mean|c| + off + shift), off being the distance of a warp's
+    mean from the row's: no more than that of some 512 columns in a row.  The join moves them by at
+    most 2 off + shift, to the first warp's mean, in products within 2^-21.  rstd takes half of the
+    variance's error and 2^-23; the mean is rounded once and carries the differences' error."""
+    if rows * cols > 5_000_000 and cols not in (2056, 20000):
+        rows = 700
+    g = torch.Generator(device=DEV)
+    g.manual_seed(cols)
+    x = far + torch.randint(-1, 2, (rows, cols), generator=g, device=DEV).float()
+    w = torch.ones(cols, device=DEV)
+    mean, rstd, y = torch.empty(rows, device=DEV), torch.empty(rows, device=DEV), torch.empty_like(x)
+    nv.nvfp4_add_layernorm(x, w, 0.0, y=y, mean=mean, rstd=rstd)
+    _, em, es, _ = layernorm(x, None, w, None, 0.0)
+    c = x.double() - em[:, None]
+    var, spread = c.square().mean(dim=1), c.abs().mean(dim=1)
+    block = torch.nn.functional.pad(c, (0, -cols % 512)).unflatten(1, (-1, 512)).sum(dim=2)
+    count = torch.full((block.shape[1],), 512.0, dtype=torch.float64, device=DEV)
+    count[-1] -= -cols % 512
+    chain = 29 * 2.0 ** -24
+    off = (block / count).abs().amax(dim=1)
+    shift = chain * abs(far)
+    moved = 2 * off + shift
+    rel = ((chain + 2.0 ** -21) * (var.sqrt() + moved) ** 2
+           + 2 * moved * chain * (spread + off + shift)) / var
+    _inside(rstd, es, (rel / 2 + 2.0 ** -23) * es, "rstd")
+    _inside(mean, em, 2.0 ** -24 * em.abs() + chain * (spread + off + shift) + 2.0 ** -21 * moved, "mean")
+
+
 @pytest.mark.parametrize("cols", [2048, 1003])
 def test_fused_is_the_two_operators(cols):
     """The fused sum is bit for bit that of nvfp4_dropout with the same mask, and in place."""
@@ -233,6 +269,19 @@ def test_bad_values_stay_in_their_row():
     h = torch.empty_like(x)
     nv.nvfp4_add_layernorm(x, w, EPS, bias=b, residual=r, mask=nv.Mask(1.0, 1, 1), h=h, y=y3)
     assert torch.equal(h, r) and not bool(y3.isnan().any())
+
+
+@pytest.mark.parametrize("cols", [48, 640, 8192])
+def test_infinite_rows(cols):
+    """The mean of a row with an infinity is that infinity (with both a NaN), its rstd and y are NaN."""
+    x, _, w, b = _inputs(4, cols, torch.float32, 10)
+    inf = float("inf")
+    x[0, 0], x[1, cols - 1], x[2, 1], x[2, cols - 2] = inf, -inf, inf, -inf
+    y, mean, rstd = torch.empty_like(x), torch.empty(4, device=DEV), torch.empty(4, device=DEV)
+    nv.nvfp4_add_layernorm(x, w, EPS, bias=b, y=y, mean=mean, rstd=rstd)
+    assert float(mean[0]) == inf and float(mean[1]) == -inf and bool(mean[2].isnan())
+    assert bool(rstd[:3].isnan().all()) and bool(y[:3].isnan().all())
+    assert bool(y[3].isfinite().all()) and bool(rstd[3].isfinite())
 
 
 def test_rows_without_columns():
