@@ -37,6 +37,7 @@
 #include <cuda_bf16.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "activation.cuh"
 #include "gemm_tile.cuh"
@@ -574,8 +575,10 @@ template <bool ALIGNED>
 cudaError_t run(const CUtensorMap& map_a, const CUtensorMap& map_b, const GatedParams& p,
                 int64_t tiles, const DeviceInfo& dev, cudaStream_t stream) {
   const auto kernel = k_gemm_gated<ALIGNED>;
-  static int pairs_of[64] = {};  // clusters that are resident at once, by device
-  int pairs = dev.device < 64 ? pairs_of[dev.device] : 0;
+  // clusters that are resident at once, by device (0: not asked yet).  Threads that make their first calls
+  // at once all ask; who reads a count also has the attribute that was set before it
+  static std::atomic<int> pairs_of[64];
+  int pairs = dev.device < 64 ? pairs_of[dev.device].load(std::memory_order_acquire) : 0;
   if (pairs == 0) {
     cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          kSmemBytes);
@@ -593,7 +596,7 @@ cudaError_t run(const CUtensorMap& map_a, const CUtensorMap& map_b, const GatedP
     e = cudaOccupancyMaxActiveClusters(&pairs, kernel, &cfg);
     if (e != cudaSuccess) return e;
     if (pairs < 1) return cudaErrorInvalidConfiguration;
-    if (dev.device < 64) pairs_of[dev.device] = pairs;
+    if (dev.device < 64) pairs_of[dev.device].store(pairs, std::memory_order_release);
   }
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(2 * std::min<int64_t>(tiles, pairs)));

@@ -6,6 +6,10 @@ of |z| for the bias.  d = act(g) u: 1.13 t_g |u| + t_u |act(g)| + 1.13 t_g t_u, 
 2^-20 (1 + |g|) |u|, and 2^-23 |d| for the product.  Storing rounds once.  The maxima are exactly
 those of d (of dgu) as the call stored it.
 """
+import os
+import subprocess
+import sys
+
 import pytest
 import torch
 
@@ -273,6 +277,46 @@ def test_two_calls_at_once():
         assert torch.equal(got[i], want[i // 2])
         assert torch.equal(maxima[i], got[i].abs().amax(dim=1))
     assert nv.nvfp4_device_status() == 0
+
+
+FIRST_CALLS = """
+import threading, torch, test_gpu_gated as t
+nv = t.nv
+m, sizes = 300, [(640, 1056), (1001, 1056)]  # aligned rows of d, and not
+ops = [t._operands(m, n, k, 4)[0] for n, k in sizes]
+got = [torch.empty(m, sizes[i % 2][0], device="cuda") for i in range(8)]
+ws = [torch.empty(nv.nvfp4_gemm_gated_workspace_size(m, *sizes[i % 2]), dtype=torch.uint8, device="cuda")
+      for i in range(8)]
+streams = [torch.cuda.Stream() for _ in range(8)]
+torch.cuda.synchronize()
+start, errors = threading.Barrier(8), []
+def call(i):
+    try:
+        torch.cuda.set_device(0)
+        start.wait()
+        nv.nvfp4_gemm_gated(*ops[i % 2], got[i], workspace=ws[i], stream=streams[i])
+    except Exception as e:
+        errors.append(e)
+threads = [threading.Thread(target=call, args=(i,)) for i in range(8)]
+[x.start() for x in threads]
+[x.join() for x in threads]
+torch.cuda.synchronize()
+assert not errors, errors
+for i, d in enumerate(got):
+    want = torch.empty_like(d)
+    nv.nvfp4_gemm_gated(*ops[i % 2], want)
+    assert torch.equal(d, want)
+print("same")
+"""
+
+
+def test_first_calls_of_several_threads():
+    """Eight threads make a process's first gated products at once."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    path = os.pathsep.join([here, os.path.dirname(here), os.environ.get("PYTHONPATH", "")])
+    r = subprocess.run([sys.executable, "-c", FIRST_CALLS], capture_output=True, text=True, timeout=300,
+                       env={**os.environ, "PYTHONPATH": path}, cwd=os.path.dirname(here))
+    assert r.returncode == 0 and r.stdout.strip().endswith("same"), r.stderr[-2000:]
 
 
 # ---------------------------------------------------------------- backward
