@@ -686,8 +686,14 @@ nvfp4_status gemm_impl(const nvfp4_operand* a, const nvfp4_operand* b, const int
   } else {
     if (workspace == nullptr || reinterpret_cast<uintptr_t>(workspace) % 256 != 0)
       return fail(NVFP4_ERR_INVALID, "workspace must be non-NULL and 256-byte aligned");
-    if (workspace_bytes < (uint64_t)L.workspace_bytes)
-      return fail(NVFP4_ERR_INVALID, "workspace smaller than nvfp4_gemm_workspace_size");
+    if (workspace_bytes < (uint64_t)L.workspace_bytes) {
+      const char* size = gated                      ? "nvfp4_gemm_gated_workspace_size"
+                         : epilogue                 ? "nvfp4_gemm_bias_act_workspace_size"
+                         : group_ends && !k_grouped ? "nvfp4_grouped_gemm_workspace_size"
+                                                    : "nvfp4_gemm_workspace_size";
+      return fail(NVFP4_ERR_INVALID, "workspace of " + std::to_string(workspace_bytes) + " bytes, " +
+                                         std::to_string(L.workspace_bytes) + " needed (" + size + ")");
+    }
   }
   DeviceInfo dev;
   if ((st = current_device(&dev)) != NVFP4_OK) return st;

@@ -113,6 +113,26 @@ def test_gated_product_refusals(lib):
     assert lib.nvfp4_gemm_gated_workspace_size(4, 4, 64, None) == INV
 
 
+def test_small_workspaces_name_their_size(lib):
+    """The refusal states the bytes that are needed, as the call's own size function gives them."""
+    m, n, k = 300, 512, 4096
+    op = R(nv._COperand(256, 256, 256, nv.NVFP4_ROW_SCALED, 448.0))
+    epi = R(nv._CEpilogue(None, FP, 0, None, None))
+    gated = R(nv._CGatedEpilogue(None, FP, 0, None, None, None))
+    for name, need, call in (
+            ("nvfp4_gemm_workspace_size", nv.nvfp4_gemm_workspace_size(m, n, k),
+             lambda size: lib.nvfp4_gemm(op, op, m, n, k, BASE, 0, 1 << 12, size, None)),
+            ("nvfp4_grouped_gemm_workspace_size", nv.nvfp4_grouped_gemm_workspace_size(m, n, k, 2),
+             lambda size: lib.nvfp4_grouped_gemm(op, op, BASE, 2, m, n, k, BASE, 0, 1 << 12, size, None)),
+            ("nvfp4_gemm_bias_act_workspace_size", nv.nvfp4_gemm_bias_act_workspace_size(m, n, k),
+             lambda size: lib.nvfp4_gemm_bias_act(op, op, m, n, k, epi, BASE, 0, 1 << 12, size, None)),
+            ("nvfp4_gemm_gated_workspace_size", nv.nvfp4_gemm_gated_workspace_size(m, n, k),
+             lambda size: lib.nvfp4_gemm_gated(op, op, m, n, k, gated, BASE, 0, 1 << 12, size, None))):
+        assert call(need - 1) == INV
+        said = nv.nvfp4_last_error()
+        assert f"{need} needed ({name})" in said and str(need - 1) in said, said
+
+
 def test_gated_backward_refusals(lib):
     def call(dd=BASE, gu=2 * BASE, dtype=BF, act=1, rows=4, cols=64, dgu=3 * BASE, db=4 * BASE,
              ws=7 * BASE, size=1 << 24):
