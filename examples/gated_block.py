@@ -40,6 +40,14 @@ def _both(t: torch.Tensor, row_amax=None, col_amax=None):
     return _operand(row), _operand(col)
 
 
+def _columns(t: torch.Tensor):
+    """Columnwise NVFP4 alone, for a weight gradient."""
+    rows, cols = t.shape
+    col = nv.alloc_out(cols, rows, cols, t.device)
+    nv.nvfp4_quantize_columnwise(t, CFG, col)
+    return _operand(col)
+
+
 class GatedBlock:
     """Weights in FP32; their NVFP4 forms are made again after every update."""
 
@@ -110,8 +118,7 @@ class GatedBlock:
         ca = torch.empty(2 * hidden, device=dev)
         nv.nvfp4_gated_backward(da, gu, nv.NVFP4_ACT_SILU, gu, row_amax=ra, col_amax=ca)
         row, col = _both(gu, ra, ca)
-        _, y_cols = _both(y)
-        nv.nvfp4_gemm(col, y_cols, g["w1"])
+        nv.nvfp4_gemm(col, _columns(y), g["w1"])
         dy = torch.empty_like(y)
         nv.nvfp4_gemm(row, self.w1_t, dy)
         dx, dr = torch.empty_like(h), torch.empty_like(h) if mask is not None else None

@@ -89,3 +89,12 @@ def test_training_step_in_a_graph():
         ex, er = block.backward(d, saved)
         for a, b in zip(got, (one, ex, er, block.grads["w1"])):
             assert torch.equal(a, b)
+
+
+def test_columns_alone_are_those_of_both_directions():
+    """The weight gradient's operand, quantized without the rows that nothing reads."""
+    import gated_block
+    y = torch.randn(192, 320, device="cuda").bfloat16()
+    one, two = gated_block._columns(y), gated_block._both(y)[1]
+    for f in ("codes", "scales", "amax"):
+        assert torch.equal(getattr(one, f), getattr(two, f))
