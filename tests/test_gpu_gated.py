@@ -136,6 +136,42 @@ def test_long_k(m, n):
     _check(m, n, 8192 + 96, torch.float32, "none", torch.float32, seed=5)
 
 
+def _integer_operands(m, n, k, seed):
+    """Row-scaled operands whose values are E2M1 values times 1 or 2: every product is a multiple of 1/4 of
+    at most 144."""
+    dev = []
+    g = torch.Generator(device=DEV)
+    g.manual_seed(seed)
+    for lines in (m, 2 * n):
+        codes = torch.randint(0, 256, (lines, k // 2), generator=g, device=DEV).to(torch.uint8)
+        twice = torch.randint(0, 2, (lines, k // 16), generator=g, device=DEV)
+        scales = torch.where(twice == 1, 0x40, 0x38).to(torch.uint8)  # E4M3 2 and 1
+        dev.append(nv.Operand(codes, scales, torch.full((lines,), 448.0 * 6, device=DEV), RS, 448.0))
+    return dev
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 320, 8288), (20, 320, 8288), (64, 257, 8288), (130, 320, 8288),
+                                   (450, 1000, 8288), (300, 1001, 4128), (700, 2000, 2080),
+                                   (1, 5000, 8192), (3, 20000, 2080), (257, 264, 16416)])
+@pytest.mark.parametrize("keep", [False, True])
+def test_long_sums_are_exact(m, n, k, keep):
+    """Sums of products that are multiples of 1/4 are exact in FP32 while they stay below 2^22 (the largest
+    possible sum of 16416 terms is 2.4 million), and alpha and beta are 1 (448 * 6 times its rounded
+    reciprocal rounds to 1): a lost or doubled value, scale or block of a sum shows.  d = g u rounds once."""
+    f = torch.tensor(448.0 * 6)
+    assert float(f * (1.0 / f)) == 1.0
+    a, b = _integer_operands(m, n, k, m + n)
+    d = torch.empty(m, n, device=DEV)
+    gu = torch.empty(m, 2 * n, device=DEV) if keep else None
+    nv.nvfp4_gemm_gated(a, b, d, act=nv.NVFP4_ACT_NONE, gu=gu)
+    z = operand_values(a.codes, a.scales, a.amax, 448.0) @ operand_values(b.codes, b.scales, b.amax,
+                                                                          448.0).t()
+    z = (4.0 * z).round() / 4.0  # operand_values' FP64 factor amax / (bound * 6) is 1 or next to it
+    assert torch.equal(d, (z[:, :n] * z[:, n:]).float())
+    if keep:
+        assert torch.equal(gu.double(), z)
+
+
 @pytest.mark.parametrize("m,n", [(3, 384), (150, 384), (900, 5000), (2600, 2501)])
 def test_halves_are_the_product_with_either_weight(m, n):
     """gu is nvfp4_gemm with the stacked weights, within both sums' rounding, and repeatable."""
@@ -378,6 +414,42 @@ def test_backward_unaligned_and_alone(dtype, offset):
     dgu.copy_(gu)
     nv.nvfp4_gated_backward(dd, dgu, nv.NVFP4_ACT_GELU, dgu)
     assert torch.equal(dgu, want)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,cols,offset", [(3000, 1001, 0), (999, 515, 0), (1200, 2050, 0), (500, 3001, 1),
+                                              (40, 33, 0), (2000, 1008, 3), (7, 5000, 2)])
+def test_backward_in_place_of_unaligned_rows(rows, cols, offset, dtype):
+    """dgu over gu where rows share 16-byte units with their neighbours, again and again: the same bits
+    as out of place, and nothing beside it changes."""
+    dd, gu = _back_inputs(rows, cols, dtype, 4)
+    dd = at_offset(dd, offset)
+    want = torch.empty_like(gu)
+    db, dc, ra = torch.empty(2 * cols, device=DEV), torch.empty(2 * cols, device=DEV), torch.empty(rows, device=DEV)
+    nv.nvfp4_gated_backward(dd, gu, nv.NVFP4_ACT_SILU, want, dbias=db)
+    got, ok = guarded((rows, 2 * cols), dtype, offset=offset)
+    for _ in range(4):
+        got.copy_(gu)
+        nv.nvfp4_gated_backward(dd, got, nv.NVFP4_ACT_SILU, got, dbias=dc, row_amax=ra)
+        assert torch.equal(got, want) and torch.equal(db, dc)
+        assert torch.equal(ra, want.abs().amax(dim=1).float())
+    ok()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,cols", [(3000, 1001), (999, 515), (16000, 64), (2000, 1024), (777, 2056),
+                                       (9001, 24), (5, 5000)])
+def test_backward_sums_of_small_integers_are_exact(rows, cols, dtype):
+    """g = dd u and u's gradient dd g of small integers (no activation): every partial sum is an integer
+    below 2^24, so dbias is exact whatever the order of its additions."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(rows)
+    dd = torch.randint(-2, 3, (rows, cols), generator=g, device=DEV).to(dtype)
+    gu = torch.randint(-3, 4, (rows, 2 * cols), generator=g, device=DEV).to(dtype)
+    dgu, db = torch.empty_like(gu), torch.empty(2 * cols, device=DEV)
+    nv.nvfp4_gated_backward(dd, gu, nv.NVFP4_ACT_NONE, dgu, dbias=db)
+    want = torch.cat([dd.double() * gu[:, cols:].double(), dd.double() * gu[:, :cols].double()], dim=1)
+    assert torch.equal(dgu.double(), want) and torch.equal(db.double(), want.sum(0))
 
 
 @pytest.mark.parametrize("name", ["relu", "gelu", "silu", "none"])

@@ -152,6 +152,29 @@ def test_nvfp4_output_is_the_quantize_of_y(rows, cols, bound, fos):
         ok()
 
 
+@pytest.mark.parametrize("masked", [False, True])
+@pytest.mark.parametrize("rows,cols", [(1, 8192), (40, 512), (7003, 512), (3001, 1001), (4004, 1024),
+                                       (2777, 2048), (2000, 4096), (1501, 5001), (1000, 8192),
+                                       (1500, 8200), (701, 12000), (320, 20000), (330, 17001)])
+def test_bf16_rows_to_nvfp4(rows, cols, masked):
+    """BF16 rows, few ones and enough of them for the ring: the codes, scales and amax are the oracle's of
+    the FP32 y.  That y is the one that the FP32 kernels give for the same values: a BF16 x is exact
+    in FP32, and at these lengths neither the rows' teams nor the order of their sums depend on the type."""
+    x, r, w, b = _inputs(rows, cols, torch.bfloat16, 3 * rows + cols)
+    mask = nv.Mask(0.25, 9, cols) if masked else None
+    out = nv.alloc_out(rows, cols, rows)
+    cfg = nv.Config(nv.NVFP4_ROW_SCALED, 448.0, 0, 0)
+    nv.nvfp4_add_layernorm(x, w, EPS, bias=b, residual=r, mask=mask, row=out, cfg=cfg)
+    y = torch.empty(rows, cols, device=DEV)
+    nv.nvfp4_add_layernorm(x.float(), w, EPS, bias=b, residual=r.float(), mask=mask, y=y)
+    torch.cuda.synchronize()
+    ref = oracle.quantize(y.cpu().numpy(), "fp32", mode=oracle.ROW_SCALED, bound=448.0,
+                          columnwise=False)["row"]
+    assert np.array_equal(out.amax.cpu().numpy().view(np.uint32), ref[2].view(np.uint32))
+    assert np.array_equal(out.scales.cpu().numpy(), ref[1])
+    assert np.array_equal(out.codes.cpu().numpy(), ref[0])
+
+
 def test_given_amax():
     x, _, w, b = _inputs(9, 320, torch.float32, 5)
     y = torch.empty_like(x)
@@ -335,6 +358,26 @@ def test_backward(rows, cols, dtype):
         _inside(db, eb, terms * dy.double().abs().sum(0), "dbias")
         for ok in (ok_x, ok_r, ok_w, ok_b):
             ok()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows,cols", [(9001, 24), (9001, 25), (7003, 512), (5003, 1000), (3001, 1001),
+                                       (3001, 2048), (2777, 4096), (1501, 5008), (1501, 4097),
+                                       (1300, 8192), (701, 12000), (401, 17001), (400, 20000), (5, 100)])
+def test_parameter_gradients_of_small_integers_are_exact(rows, cols, dtype):
+    """dy in {-2 .. 2}, h in {-3 .. 3}, mean 0, rstd 1, weight 1: n is h and every partial sum an integer
+    below 6 * 9001 < 2^24, so no addition rounds, whatever their order: a row that is left out, counted
+    twice or taken from its neighbour shows."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(rows + cols)
+    dy = torch.randint(-2, 3, (rows, cols), generator=g, device=DEV).to(dtype)
+    h = torch.randint(-3, 4, (rows, cols), generator=g, device=DEV).to(dtype)
+    w = torch.ones(cols, device=DEV, dtype=dtype)
+    mean, rstd = torch.zeros(rows, device=DEV), torch.ones(rows, device=DEV)
+    dw, db, dx = torch.empty(cols, device=DEV), torch.empty(cols, device=DEV), torch.empty_like(h)
+    nv.nvfp4_add_layernorm_backward(dy, h, w, mean, rstd, dx, dweight=dw, dbias=db)
+    assert torch.equal(dw.double(), (dy.double() * h.double()).sum(0))
+    assert torch.equal(db.double(), dy.double().sum(0))
 
 
 def test_backward_against_differences():
