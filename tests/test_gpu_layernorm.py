@@ -307,6 +307,26 @@ def test_infinite_rows(cols):
     assert bool(y[3].isfinite().all()) and bool(rstd[3].isfinite())
 
 
+@pytest.mark.parametrize("far", [0.0, 1e27])
+@pytest.mark.parametrize("cols", [48, 640, 1000, 5000, 8192, 20000])
+def test_rows_whose_squares_overflow(cols, far):
+    """Spreads above 2e19: the variance is infinite in FP32, so rstd is 0 and y the bias; the mean is not
+    touched by that.  One block of columns far from the others overflows in the join alone.  (A row
+    may come out as one value: its variance is 0, and its y the bias too.)"""
+    x, _, w, b = _inputs(5, cols, torch.float32, 12)
+    spread = torch.tensor([1e20, 1e22, 1e25, 1e30, 0.0], device=DEV)[:, None]
+    x = far + torch.sign(x) * (1 + x.abs().clamp(max=1)) * spread
+    x[4, cols // 2:] = -1e30
+    y, mean, rstd = torch.empty_like(x), torch.empty(5, device=DEV), torch.empty(5, device=DEV)
+    nv.nvfp4_add_layernorm(x, w, EPS, bias=b, y=y, mean=mean, rstd=rstd)
+    _, em, es, _ = layernorm(x, None, w, b, EPS)
+    same = (x == x[:, :1]).all(dim=1)
+    assert bool((rstd[~same] == 0).all()) and int(same.sum()) <= 1
+    _inside(rstd[same], es[same], 2.0 ** -22 * es[same], "rstd")
+    assert torch.equal(y, b.expand(5, cols))
+    _inside(mean, em, 2.0 ** -18 * x.double().abs().mean(dim=1), "mean")
+
+
 def test_rows_without_columns():
     x, w = torch.empty(3, 0, device=DEV), torch.empty(0, device=DEV)
     mean, rstd = torch.ones(3, device=DEV), torch.empty(3, device=DEV)
