@@ -27,11 +27,13 @@
 //
 // The scales go through registers because a tcgen05.cp takes about 50 cycles of the MMAs' own
 // in-order pipe whatever it moves, and a K tile would need twelve (six of the largest form): 8192 x
-// 14336 x 8192 takes 1122 us so, 646 this way, 649 with the copies left out.  Measured, SILU: 16384
-// x 14336 x 8192 1449 us with [g | u] and the maxima kept, 5.3 PFLOP/s; 8192 rows without them
-// 646 us, 6.0 PFLOP/s, of which 60 us are the epilogue's.  What is left is the pair's walk through the
-// ring: a K tile takes 0.42 us, 0.37 with one MMA instead of four, 0.36 without the scales' stores; half
-// of B's bytes, four stages instead of five or a second producer change nothing.
+// 14336 x 8192 takes 1122 us so, 646 this way, 649 with the copies left out.  Measured, SILU: 16384 x
+// 14336 x 8192 with [g | u] and the maxima kept 1390 us in bursts of tens of calls, 5.5 PFLOP/s, and 1500
+// once they follow one another for more than a second (at 1.35 kW the SM clock goes from 2070 to 1790
+// MHz); 8192 rows without them 646 us, 6.0 PFLOP/s, of which 60 us are the epilogue's.  What is left is
+// the pair's walk through the ring: a K tile takes 0.42 us, 0.37 with one MMA instead of four, 0.36
+// without the scales' stores; half of B's bytes, four stages instead of five or a second producer
+// change nothing.
 //
 // Every wait is bounded, as in kernels_gemm.cu; the CTAs of a pair meet before either leaves.
 #include <cuda_bf16.h>
@@ -502,7 +504,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1)
       tc_fence_after();
       // All accumulators at once, so that TMEM may take the next tile's MMAs during the rest; rows
       // that are not aligned have no registers for that beside their transpositions (4 bytes of
-      // spills a value, measured twice as slow), and hand TMEM back after their last block.
+      // spills a value, measured twice as slow; 28 bytes in all are left), and hand TMEM back after their
+      // last block.
       constexpr int kHeld = ALIGNED ? kWarpCols : 32;
       uint32_t v[2][kHeld];
       auto load = [&](int from) {

@@ -778,7 +778,7 @@ int64_t round256(int64_t v) { return (v + 255) / 256 * 256; }
 // whole tiles each; the rest is cut where that is faster.  In nanoseconds: a unit takes
 // about 500 for a CTA alone and 840 when every SM streams (memory); joining adds about 4000
 // at the end of the call (two passes through L2 and their fences), nothing where whole
-// tiles follow.
+// tiles follow.  (Measured on the product without a gate; a GATED unit has as many bytes and MMAs.)
 struct CutPlan {
   int split, parts;
 };
@@ -858,7 +858,8 @@ bool gemm_few(int64_t m, int64_t n) { return m <= 384 || tiles_of(m, n) <= 304; 
 // (1, 28672, 8192) 48 and 84, (64, 14336, 8192) 30 and 42; (64, 8192, 8192) 28 and 26, (128, 14336,
 // 8192) 41 and 43, (256, 8192, 8192) 49 and 28; (256, 1024, 1024) 8.8 and 10.2, (256, 2048, 2048)
 // 11.8 both, (2048, 1024, 1024) 14.8 and 11.6; unaligned (500, 1001, 1024) 8.9 and 13.7, (300,
-// 5001, 7168) 37 and 41, (2000, 5001, 2048) 63 and 51.
+// 5001, 7168) 37 and 41, (2000, 5001, 2048) 63 and 51.  One border for all lengths gives 2 us away on either
+// side of it, at (64, 8192, 8192) and (128, 14336, 8192).
 bool gemm_gated_few(int64_t m, int64_t n, int64_t k, bool aligned) {
   return m <= 64 || (k <= 1024 && tiles_of(m, n) <= 152) ||
          (!aligned && ceil_div(m, 256) * ceil_div(n, 128) <= 152);

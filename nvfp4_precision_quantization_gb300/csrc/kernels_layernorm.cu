@@ -16,10 +16,11 @@
 // own rounding.  The scale of a whole row needs max|y|, which b makes known only after s: a second
 // barrier, for those outputs alone.  The rest is norm_rows.cuh's.
 //
-// Measured (residual, bias): 4000 x 5000 FP32 53 us, 6.0 TB/s; 16384 x 8192 BF16 with E4M3 codes 182
-// us, 5.2 TB/s, and 232 us with dropout.  BF16 rows are bound by issue slots: 29 instructions an
-// element (the RMS norm's 23 take 147 us) and 12 more for the mask, at the 60 % of the slots that
-// 24 warps an SM with two barriers a row fill.  One row of 8192 4 us.
+// Measured (residual, bias): 4000 x 5000 FP32 54 us, 5.9 TB/s; 16384 x 8192 BF16 with E4M3 codes or
+// NVFP4 rows 184 us, 5.1 and 4.8 TB/s, and 239 us with dropout.  BF16 rows stop at 31 instructions an
+// element (25 with y alone, 171 us) and 12 more for the mask, in 55 to 60 % of the issue slots: the
+// rest is latency that 24 warps an SM with two barriers a row leave open.  The differences' sums are 1
+// of the instructions and 3 % of those times.  One row of 8192 4 us.
 #include "norm_rows.cuh"
 
 namespace nvfp4 {

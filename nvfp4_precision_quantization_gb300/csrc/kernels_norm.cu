@@ -6,8 +6,8 @@
 // because rounding after the product with the positive s is monotonic; the scale of the whole
 // row is therefore known one barrier after its last load.  The rest is norm_rows.cuh's.
 //
-// Measured (E4M3 output, residual): 16384 x 8192 BF16 147 us, 6.4 TB/s, 0.96 of a copy (182
-// us without the ring), NVFP4 rows 153 us; 4000 x 5000 FP32 in 128-column blocks 49 us, 5.3
+// Measured (E4M3 output, residual): 16384 x 8192 BF16 143 us, 6.6 TB/s, 0.98 of a copy (182
+// us without the ring), NVFP4 rows 144 us; 4000 x 5000 FP32 in 128-column blocks 47 us, 5.6
 // TB/s (barriers and shared-memory rotations are in sight there: issue slots are 54 % used);
 // one row of 8192 3.0 us, which is a launch and one pass of latencies.
 #include "norm_rows.cuh"
