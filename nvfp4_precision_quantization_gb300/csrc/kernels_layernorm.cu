@@ -4,17 +4,19 @@
 //   y = (h - m) s w + b
 //
 // The variance is that of the differences, not a difference of moments.  Each warp takes its own mean m_w
-// from registers, then the sums e_w of its n_w differences to it and Q_w of their squares.  With m
-// the mean of the team's first warp and off = m_w - m, the row's are
+// from registers, then the sums e_w of its n_w differences to it and Q_w of their squares.  With off =
+// m_w - m, for any m near the row's values, the row's are
 //   sum (h - m) = e_w + n_w off,   sum (h - m)^2 = Q_w + 2 off e_w + n_w off^2
 // (Chan, Golub, LeVeque, "Updating formulae and a pairwise algorithm for computing sample
 // variances", 1979, where e_w is 0; m_w is rounded here, and without e_w rows of 65536 +- 1 lost 2e-4
 // of their variance), and the first moves m to the row's mean and takes its part off the second.  m is
-// the mean of a share f of the row, so within sqrt(1 / f - 1) of its standard deviations: what is
-// taken off is at most 1 / f - 1 times what is left, f being 1/32 or more, and next to nothing in a
-// row whose columns are alike.  One barrier is enough, and a row far from zero loses nothing but its
-// own rounding.  The scale of a whole row needs max|y|, which b makes known only after s: a second
-// barrier, for those outputs alone.  The rest is norm_rows.cuh's.
+// the mean of the team's first warp where that is beyond one of its standard deviations, and 0 in rows
+// that lie around 0, whose sum of values is the better mean.  Either way it is within 2 / sqrt(f) of the
+// row's standard deviations of its mean, f >= 1/32 being the first warp's share (mostly within a
+// few hundredths, or one): so much is what is taken off, at most, beside what is left.  One barrier is
+// enough, and a row far from zero loses nothing but its own rounding.  The scale of a whole row needs
+// max|y|, which b makes known only after s: a second barrier, for those outputs alone.  The rest is
+// norm_rows.cuh's.
 //
 // Measured (residual, bias): 4000 x 5000 FP32 54 us, 5.9 TB/s; 16384 x 8192 BF16 with E4M3 codes or
 // NVFP4 rows 184 us, 5.1 and 4.8 TB/s, and 239 us with dropout.  BF16 rows stop at 31 instructions an
@@ -45,7 +47,8 @@ __device__ __forceinline__ float team_max(float m, float* red) {
 
 struct LayerNorm {
   static constexpr bool kMasked = true;
-  using Sums = float4;  // its mean, the sums of squared differences to it and of differences
+  // of values; of squared differences to their mean and of differences; the mean
+  using Sums = float4;
   // 24 warps an SM: with the 16 that the compiler's registers leave, a row's barriers lie open
   // (4000 x 5000 FP32 74 us, 53 so); 16 for two FP32 chunks a thread, which spill (16000 x 8192 FP32
   // 460 us with 24, 416 with 16)
@@ -67,7 +70,7 @@ struct LayerNorm::Team {
   static constexpr int kWarps = TPR / 32;
   static constexpr int kTree = kWarps <= 1 ? 1 : kWarps <= 2 ? 2 : kWarps <= 4 ? 4 : kWarps <= 8 ? 8 : kWarps <= 16 ? 16 : 32;
   float inv_warp;   // 1 / the columns of this thread's warp (0 where it has none)
-  float n;          // the columns of the team's warp `lane`, whose sums this lane joins
+  float n, n_first; // those of the team's warp `lane`, whose sums this lane joins, and of its first one
   float inv_cols;
 
   // columns of the team's warp w
@@ -85,6 +88,7 @@ struct LayerNorm::Team {
     const int w = (threadIdx.x & 31) % kTree, theirs = w < kWarps ? count(a.cols, w) : 0;
     inv_warp = inverse(count(a.cols, t / 32));
     n = (float)theirs;
+    n_first = (float)count(a.cols, 0);
     inv_cols = inverse(a.cols);
   }
 
@@ -102,13 +106,12 @@ struct LayerNorm::Team {
   __device__ __forceinline__ static bool finite(float x) {
     return fabsf(x) < __int_as_float(0x7f800000);
   }
-  // Mean and sum of squared differences to it, from those to a finite m: rest = sum (v - m), sq =
-  // sum (v - m)^2 (which is not below rest^2 / cols but for its rounding; a NaN stays).
-  __device__ __forceinline__ float2 around_mean(float m, float rest, float sq) const {
-    const float d = __fmul_rn(rest, inv_cols);
-    float s = __fmaf_rn(-rest, d, sq);
+  // The sum of squared differences to the mean, from sums of differences to some m and of their squares
+  // (not below 0 but for its rounding; an infinity or a NaN stays).
+  __device__ __forceinline__ float around_mean(float rest, float sq) const {
+    float s = __fmaf_rn(-rest, __fmul_rn(rest, inv_cols), sq);
     asm("max.NaN.f32 %0, %0, 0f00000000;" : "+f"(s));
-    return make_float2(__fadd_rn(m, d), s);
+    return s;
   }
 
   // Mean and sum of squared differences of a row whose part is in v (zeros past its end).
@@ -153,27 +156,33 @@ struct LayerNorm::Team {
       if constexpr (BARRIER) __syncthreads();
       const float other = __shfl_xor_sync(0xffffffffu, both, 16);
       const float sq = lane < 16 ? both : other, rest = lane < 16 ? other : both;
-      return finite(mean) ? around_mean(mean, rest, sq) : around_mean(0.0f, mean, sq);
+      const bool far = __fmul_rn(mean, mean) > __fmul_rn(sq, inv_cols);  // not where it is infinite
+      return make_float2(far ? __fmaf_rn(rest, inv_cols, mean) : mean, around_mean(rest, sq));
     } else {
       const int warp = threadIdx.x >> 5, first = warp - warp % kWarps;
-      if (lane == 0) red[warp].x = mean;
-      if (lane % 16 == 0) (lane == 0 ? red[warp].y : red[warp].z) = both;
+      if (lane == 0) {
+        red[warp].x = sum;
+        red[warp].y = both;
+        red[warp].w = mean;
+      } else if (lane == 16) {
+        red[warp].z = both;
+      }
       __syncthreads();
-      // this lane's warp's differences, to the mean of the team's first warp
+      const float4 own = red[first];
+      // (a NaN is not beyond)
+      const float m = __fmul_rn(__fmul_rn(own.w, own.w), n_first) > own.y ? own.w : 0.0f;
+      // this lane's warp's differences to m
       const int i = lane % kTree;
-      const float4 p = red[first + (i < kWarps ? i : 0)];
-      float m = red[first].x;
-      if (!finite(m)) m = 0.0f;
-      const float off = __fsub_rn(p.x, m);
-      // (the differences to a mean that is no number are none: it stands for them.  n is 0, and the
-      // differences of no account, where the warp has no columns)
-      const float sq = n > 0.0f ? __fmaf_rn(__fmul_rn(off, off), n,
-                                            __fmaf_rn(__fadd_rn(off, off), p.z, p.y)) : 0.0f;
-      float rest = n > 0.0f ? __fmaf_rn(off, n, p.z) : 0.0f;
-      if (!finite(p.x)) rest = p.x;
+      const float4 p = i < kWarps ? red[first + i] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+      const float off = n > 0.0f ? __fsub_rn(p.w, m) : 0.0f;  // (0: a warp without columns)
+      const float sq = __fmaf_rn(__fmul_rn(off, off), n, __fmaf_rn(__fadd_rn(off, off), p.z, p.y));
+      // (a sum that is no number has no differences, and stands for them)
+      const float rest = m != 0.0f && finite(p.x) ? __fmaf_rn(off, n, p.z) : p.x;
       const float joined = sum_of_two<kTree>(sq, rest, lane);
       const float other = __shfl_xor_sync(0xffffffffu, joined, kTree / 2);
-      return (lane & (kTree / 2)) ? around_mean(m, joined, other) : around_mean(m, other, joined);
+      const bool upper = lane & (kTree / 2);
+      const float all = upper ? joined : other;
+      return make_float2(__fmaf_rn(all, inv_cols, m), around_mean(all, upper ? other : joined));
     }
   }
 

@@ -242,6 +242,25 @@ def test_variance_does_not_depend_on_the_mean(rows, cols, far):
     _inside(mean, em, 2.0 ** -24 * em.abs() + chain * (spread + off + shift) + 2.0 ** -21 * moved, "mean")
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows", [1, 9, 2500])
+@pytest.mark.parametrize("cols", [64, 128, 1000, 1024, 2048, 5000, 7424, 8192, 12000, 20000])
+def test_small_means_are_those_of_the_sum(rows, cols, dtype):
+    """Integers of -3 .. 3: every sum is exact in FP32, so a mean, however near 0, is off by the roundings of 1 /
+    cols and of one product alone: 2^-23 of itself."""
+    g = torch.Generator(device=DEV)
+    g.manual_seed(rows * cols)
+    x = torch.randint(-3, 4, (rows, cols), generator=g, device=DEV).to(dtype)
+    x[0, 1::2] = -x[0, 0::2]  # a row that sums to 0
+    w = torch.ones(cols, device=DEV)
+    mean, rstd = torch.empty(rows, device=DEV), torch.empty(rows, device=DEV)
+    nv.nvfp4_add_layernorm(x, w, EPS, y=torch.empty_like(x), mean=mean, rstd=rstd)
+    _, em, es, _ = layernorm(x, None, w, None, EPS)
+    assert float(mean[0]) == 0.0
+    _inside(mean, em, 2.0 ** -23 * em.abs(), "mean")
+    _inside(rstd, es, 2.0 ** -18 * es, "rstd")
+
+
 @pytest.mark.parametrize("cols", [2048, 1003])
 def test_fused_is_the_two_operators(cols):
     """The fused sum is bit for bit that of nvfp4_dropout with the same mask, and in place."""
