@@ -19,10 +19,10 @@
 // norm_rows.cuh's.
 //
 // Measured (residual, bias): 4000 x 5000 FP32 54 us, 5.9 TB/s; 16384 x 8192 BF16 with E4M3 codes or
-// NVFP4 rows 184 us, 5.1 and 4.8 TB/s, and 239 us with dropout.  BF16 rows stop at 31 instructions an
-// element (25 with y alone, 171 us) and 12 more for the mask, in 55 to 60 % of the issue slots: the
-// rest is latency that 24 warps an SM with two barriers a row leave open.  The differences' sums are 1
-// of the instructions and 3 % of those times.  One row of 8192 4 us.
+// NVFP4 rows 186 us, 5.1 and 4.7 TB/s, and 242 us with dropout.  BF16 rows stop at 31 instructions an
+// element (25 with y alone, 170 us) and 12 more for the mask, in 55 to 60 % of the issue slots: the
+// rest is latency that 24 warps an SM with two barriers a row leave open.  The differences' sums and
+// their join are 1.5 of the instructions and 4 % of those times.  One row of 8192 4 us.
 #include "norm_rows.cuh"
 
 namespace nvfp4 {

@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(TPR < 256 ? 256 : TPR,
         drop.apply(base + col, v[c], a.res != nullptr ? &cr : nullptr);
       } else if (a.res != nullptr) {
         // (loaded under this condition alone: as above it costs 10 to 18 registers more, and rows of
-        // more than 16384 columns, 64 a thread, spill: 4000 x 28672 BF16 149 us, 168 so)
+        // more than 16384 columns, 64 a thread, spill: 4000 x 28672 BF16 148 us, 168 so)
         const Chunk<BF16> cr = residual();
 #pragma unroll
         for (int i = 0; i < kChunk; ++i) v[c][i] = __fadd_rn(v[c][i], cr.get(i));
